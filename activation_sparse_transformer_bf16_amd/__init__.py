@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # TWELL_LIBRARY names another build of the same library (the host-sanitizer
@@ -51,6 +51,15 @@ class TwellHybridC(ctypes.Structure):
     ]
 
 
+class TwellInt8C(ctypes.Structure):
+    """Mirror of ``twell_int8`` (include/twell.h)."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("ld", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+    ]
+
+
 class TwellError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{message} (status {status})")
@@ -70,7 +79,8 @@ def _load():
         raise ImportError(f"{LIB_PATH} has ABI version {lib.twell_abi_version()}, this binding needs {ABI_VERSION}: "
                           "rebuild it")
     P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-    M = ctypes.POINTER(TwellMatrixC)
+    L, R = ctypes.c_int64, ctypes.c_float
+    M, Q = ctypes.POINTER(TwellMatrixC), ctypes.POINTER(TwellInt8C)
     sig = {
         "twell_abi_version": (I, []),
         "twell_status_str": (ctypes.c_char_p, [I]),
@@ -96,6 +106,11 @@ def _load():
         "twell_mfma_probe": (I, [P, I, I, P]),
         "twell_ffn_backward": (I, [ctypes.POINTER(TwellHybridC), P, P, P, P, P, ctypes.c_float, I, P, P, P, P,
                                    P, Z, P]),
+        "twell_rmsnorm": (I, [P, L, P, L, P, R, I, I, I, P, L, P, L, Q, P]),
+        "twell_rmsnorm_backward_workspace_size": (Z, [I, I, I]),
+        "twell_rmsnorm_backward": (I, [P, L, P, L, P, P, L, R, I, I, I, P, L, P, P, Z, P]),
+        "twell_quantize_rows": (I, [P, L, I, Q, P]),
+        "twell_int8_matmul": (I, [Q, Q, P, I, P, L, P]),
     }
     # Private function objects: changing argtypes on the public handle (lib())
     # cannot make this binding pass truncated pointers.
@@ -124,7 +139,9 @@ EXPORTS = ("twell_abi_version", "twell_status_str", "twell_last_error", "twell_p
            "twell_l1_workspace_size", "twell_l1_norm", "twell_l1_grad",
            "twell_ffn_backward_workspace_size", "twell_ffn_backward", "twell_sparse_ffn_fused",
            "twell_stream_probe", "twell_mfma_probe", "twell_ffn_forward_noalloc", "twell_sparse_ffn_grouped",
-           "twell_sparse_ffn_grouped_workspace_size")
+           "twell_sparse_ffn_grouped_workspace_size",
+           "twell_rmsnorm", "twell_rmsnorm_backward_workspace_size", "twell_rmsnorm_backward",
+           "twell_quantize_rows", "twell_int8_matmul")
 
 # Size of the static device scratch behind twell_ffn_forward_noalloc
 # (TWELL_NOALLOC_SCRATCH_BYTES in include/twell.h).
@@ -613,6 +630,181 @@ def dense_ffn_forward(x, w_gate, w_up, w_down, gate_bias=None, y=None, workspace
     ws = _workspace(dense_ffn_workspace_size(T, d, F, x.dtype), device, workspace)
     _check(_lib.dense_ffn_forward(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(gate_bias),
                                   _ptr(y), T, d, F, _dtype_code(x.dtype), _ptr(ws), ws.numel(),
+                                  _stream(device)))
+    return y
+
+
+# --------------------------------------------------------------------------- block operators
+
+class RmsNormOut(NamedTuple):
+    """What ``twell_rmsnorm`` wrote (None: not asked for); ``h`` is x itself without a residual."""
+
+    y: object       # dtype [rows, d]
+    h: object       # dtype [rows, d]
+    q: object       # int8 [rows, d], rows 16-byte aligned
+    scale: object   # float32 [rows]
+
+
+def _rows(t, name, device, dtype, shape) -> int:
+    """Checks a 2-D tensor with unit stride along its rows; returns the row stride in elements."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    rows, cols = shape
+    if rows == 0:
+        return cols
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _vec(t, name, device, dtype, n) -> None:
+    _need(t, name, device, dtype, (n,))
+
+
+def _ceil16(n: int) -> int:
+    return (n + 15) // 16 * 16
+
+
+def _int8_rows(q, scale, name, device, shape) -> TwellInt8C:
+    """The descriptor of int8 rows given as tensors: every row 16-byte aligned,
+    with its last 16-byte chunk inside the tensor's storage."""
+    torch = _torch()
+    ld = _rows(q, name, device, torch.int8, shape)
+    _vec(scale, f"{name}_scale", device, torch.float32, shape[0])
+    rows, cols = shape
+    if rows <= 1:
+        ld = _ceil16(cols)
+    elif ld % 16:
+        raise ValueError(f"{name}: row stride {ld} is not a multiple of 16 (lay rows out as twell_quantize_rows does)")
+    if rows and q.storage_offset() + (rows - 1) * ld + _ceil16(cols) > q.untyped_storage().nbytes():
+        raise ValueError(f"{name}: the last row's 16-byte chunks run past the tensor's storage")
+    return TwellInt8C(rows, cols, ld, q.data_ptr(), scale.data_ptr())
+
+
+def _new_int8_rows(rows: int, cols: int, device):
+    """An int8 [rows, cols] view of 16-byte aligned rows, and the scales [rows]."""
+    torch = _torch()
+    ld = _ceil16(cols)
+    q = torch.empty((rows, ld), dtype=torch.int8, device=device)
+    return (q if ld == cols else q[:, :cols]), torch.empty((rows,), dtype=torch.float32, device=device)
+
+
+def _empty_rows(rows: int, cols: int, dtype, device):
+    return _torch().empty((rows, cols), dtype=dtype, device=device)
+
+
+def twell_rmsnorm(x, weight, eps: float = 1e-6, residual=None, quantize: bool = False, h=None, y=None, q=None,
+                  scale=None, want_y: bool = True) -> RmsNormOut:
+    """h = x + residual, y = h / rms(h) * weight and, with ``quantize`` (or ``q``
+    and ``scale`` given), the normed rows in 8 bits with a scale each.
+
+    x, residual, h, y: [rows, d] with unit stride along d (any row stride).  ``h``
+    and ``y`` may be ``x`` or ``residual`` themselves.  ``want_y=False`` with
+    ``quantize`` writes the 8 bits alone."""
+    device, dtype = x.device, x.dtype
+    code = _dtype_code(dtype)
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D [rows, d], got shape {tuple(x.shape)}")
+    shape = rows, d = tuple(x.shape)
+    ld_x = _rows(x, "x", device, dtype, shape)
+    _vec(weight, "weight", device, dtype, d)
+    ld_r = ld_h = ld_y = d
+    if residual is not None:
+        ld_r = _rows(residual, "residual", device, dtype, shape)
+        if h is None:
+            h = _empty_rows(rows, d, dtype, device)
+    if h is not None:
+        ld_h = _rows(h, "h", device, dtype, shape)
+    if y is None and want_y:
+        y = _empty_rows(rows, d, dtype, device)
+    if y is not None:
+        ld_y = _rows(y, "y", device, dtype, shape)
+    if (q is None) != (scale is None):
+        raise ValueError("q and scale are given together")
+    if q is None and quantize:
+        q, scale = _new_int8_rows(rows, d, device)
+    qd = None if q is None else ctypes.byref(_int8_rows(q, scale, "q", device, shape))
+    _check(_lib.twell_rmsnorm(x.data_ptr(), ld_x, _ptr(residual), ld_r, weight.data_ptr(), eps, rows, d, code,
+                              _ptr(h), ld_h, _ptr(y), ld_y, qd, _stream(device)))
+    return RmsNormOut(y, x if h is None else h, q, scale)
+
+
+def twell_rmsnorm_backward_workspace_size(rows: int, d: int, dtype) -> int:
+    return int(_lib.twell_rmsnorm_backward_workspace_size(rows, d, _dtype_code(dtype)))
+
+
+def twell_rmsnorm_backward(dy, h, weight, eps: float = 1e-6, dh=None, dx=None, dweight=None, workspace=None):
+    """Gradients of the norm from the stored h: (dx, dweight); dx [rows, d] in
+    the activation dtype (the gradient of x and of the residual alike), with
+    the residual stream's gradient ``dh`` added when given; dweight float32 [d]."""
+    torch = _torch()
+    device, dtype = h.device, h.dtype
+    code = _dtype_code(dtype)
+    if h.dim() != 2:
+        raise ValueError(f"h must be 2-D [rows, d], got shape {tuple(h.shape)}")
+    shape = rows, d = tuple(h.shape)
+    ld_h = _rows(h, "h", device, dtype, shape)
+    ld_dy = _rows(dy, "dy", device, dtype, shape)
+    _vec(weight, "weight", device, dtype, d)
+    ld_dh = d if dh is None else _rows(dh, "dh", device, dtype, shape)
+    if dx is None:
+        dx = _empty_rows(rows, d, dtype, device)
+    ld_dx = _rows(dx, "dx", device, dtype, shape)
+    if dweight is None:
+        dweight = torch.empty((d,), dtype=torch.float32, device=device)
+    _vec(dweight, "dweight", device, torch.float32, d)
+    ws = _workspace(_lib.twell_rmsnorm_backward_workspace_size(rows, d, code), device, workspace)
+    _check(_lib.twell_rmsnorm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, weight.data_ptr(), _ptr(dh), ld_dh,
+                                       eps, rows, d, code, dx.data_ptr(), ld_dx, dweight.data_ptr(), ws.data_ptr(),
+                                       ws.numel(), _stream(device)))
+    return dx, dweight
+
+
+def twell_quantize_rows(x, q=None, scale=None):
+    """Rows of x [rows, cols] in 8 bits: (q int8 [rows, cols], scale float32 [rows]),
+    x ~ q * scale[:, None]."""
+    device, dtype = x.device, x.dtype
+    code = _dtype_code(dtype)
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D [rows, cols], got shape {tuple(x.shape)}")
+    shape = tuple(x.shape)
+    ld_x = _rows(x, "x", device, dtype, shape)
+    if (q is None) != (scale is None):
+        raise ValueError("q and scale are given together")
+    if q is None:
+        q, scale = _new_int8_rows(*shape, device)
+    out = _int8_rows(q, scale, "q", device, shape)
+    _check(_lib.twell_quantize_rows(x.data_ptr(), ld_x, code, ctypes.byref(out), _stream(device)))
+    return q, scale
+
+
+def twell_int8_matmul(a, a_scale, b, b_scale, row_bias=None, dtype=None, y=None):
+    """y[m, n] = (sum_k a[m, k] b[n, k]) * a_scale[m] * b_scale[n] (+ row_bias[m])
+    for int8 rows a [M, K], b [N, K] as twell_quantize_rows lays them out; y
+    [M, N] in ``dtype`` (default bfloat16, or that of a given ``y``)."""
+    torch = _torch()
+    device = a.device
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a and b must be 2-D")
+    M, K = a.shape
+    N = b.shape[0]
+    ad = _int8_rows(a, a_scale, "a", device, (M, K))
+    bd = _int8_rows(b, b_scale, "b", device, (N, K))
+    if row_bias is not None:
+        _vec(row_bias, "row_bias", device, torch.float32, M)
+    if dtype is None:
+        dtype = torch.bfloat16 if y is None else y.dtype
+    code = _dtype_code(dtype)
+    if y is None:
+        y = _empty_rows(M, N, dtype, device)
+    ld_y = _rows(y, "y", device, dtype, (M, N))
+    _check(_lib.twell_int8_matmul(ctypes.byref(ad), ctypes.byref(bd), _ptr(row_bias), code, y.data_ptr(), ld_y,
                                   _stream(device)))
     return y
 

@@ -798,3 +798,145 @@ twell_status dense_ffn_forward(const void *x, const void *w_gate, const void *w_
 }
 
 }  // extern "C"
+
+namespace {
+
+// One operand of the block operators: rows of `cols` elements, `ld` apart.
+// Only the element alignment is needed; wider rows are the kernels' choice.
+twell_status check_rows(const char *name, const void *p, int64_t ld, int cols, int elem, int rows) {
+  if (ld < cols)
+    return fail(TWELL_ERR_INVALID_ARG, "%s: row stride %lld is below the row length %d", name, (long long)ld, cols);
+  if (ld > ((int64_t)1 << 40)) return fail(TWELL_ERR_INVALID_ARG, "%s: row stride %lld too large", name, (long long)ld);
+  if (rows > 0 && p == nullptr) return fail(TWELL_ERR_INVALID_ARG, "null %s", name);
+  if (!aligned(p, elem)) return fail(TWELL_ERR_UNSUPPORTED, "misaligned %s", name);
+  return TWELL_OK;
+}
+
+twell_status check_int8(const char *name, const twell_int8 *q) {
+  if (q == nullptr) return fail(TWELL_ERR_INVALID_ARG, "null %s", name);
+  if (q->rows < 0 || q->cols <= 0) return fail(TWELL_ERR_INVALID_ARG, "%s: need rows >= 0 and cols > 0", name);
+  twell_status st = check_rows(name, q->q, q->ld, q->cols, 1, q->rows);
+  if (st != TWELL_OK) return st;
+  if (q->rows > 0 && q->scale == nullptr) return fail(TWELL_ERR_INVALID_ARG, "%s: null scale", name);
+  if (!aligned(q->q, 16) || q->ld % 16 != 0)
+    return fail(TWELL_ERR_UNSUPPORTED, "%s: rows must be 16-byte aligned (base and stride)", name);
+  if (!aligned(q->scale, 4)) return fail(TWELL_ERR_UNSUPPORTED, "%s: misaligned scale", name);
+  return TWELL_OK;
+}
+
+twell_status check_norm_shape(int rows, int d, int dtype) {
+  if (!valid_dtype(dtype)) return fail(TWELL_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (rows < 0 || d <= 0) return fail(TWELL_ERR_INVALID_ARG, "need rows >= 0 and a row length > 0");
+  if (d > (1 << 24) || norm_chunks(d, to_dt((twell_dtype)dtype)) > NORM_MAX_CHUNKS)
+    return fail(TWELL_ERR_UNSUPPORTED, "row length %d not built (at most %d)", d,
+                NORM_MAX_CHUNKS * 1024 / dt_size((twell_dtype)dtype));
+  return TWELL_OK;
+}
+
+twell_status check_eps(float eps) {
+  if (!(eps >= 0.0f && eps <= 3.0e38f)) return fail(TWELL_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  return TWELL_OK;
+}
+
+size_t norm_backward_ws(int rows, int d, twell_dtype dtype) {
+  return align_up((size_t)norm_backward_partials(rows, d, to_dt(dtype)) * d * 4, ALIGN_WS);
+}
+
+}  // namespace
+
+extern "C" {
+
+twell_status twell_rmsnorm(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual,
+                           const void *weight, float eps, int rows, int d, twell_dtype dtype, void *h,
+                           int64_t ld_h, void *y, int64_t ld_y, const twell_int8 *q, void *stream) {
+  g_err[0] = 0;
+  twell_status st = check_norm_shape(rows, d, (int)dtype);
+  if (st != TWELL_OK) return st;
+  if ((st = check_eps(eps)) != TWELL_OK) return st;
+  const int e = dt_size(dtype);
+  if ((st = check_rows("x", x, ld_x, d, e, rows)) != TWELL_OK) return st;
+  if (residual != nullptr && (st = check_rows("residual", residual, ld_residual, d, e, rows)) != TWELL_OK) return st;
+  if (h != nullptr && (st = check_rows("h", h, ld_h, d, e, rows)) != TWELL_OK) return st;
+  if (y != nullptr && (st = check_rows("y", y, ld_y, d, e, rows)) != TWELL_OK) return st;
+  if (q != nullptr) {
+    if ((st = check_int8("q", q)) != TWELL_OK) return st;
+    if (q->rows != rows || q->cols != d)
+      return fail(TWELL_ERR_INVALID_ARG, "q is %d x %d, the rows are %d x %d", q->rows, q->cols, rows, d);
+  }
+  if (rows == 0) return TWELL_OK;
+  if (weight == nullptr) return fail(TWELL_ERR_INVALID_ARG, "null weight");
+  if (!aligned(weight, e)) return fail(TWELL_ERR_UNSUPPORTED, "misaligned weight");
+  if (h == nullptr && y == nullptr && q == nullptr) return fail(TWELL_ERR_INVALID_ARG, "no output (h, y and q are NULL)");
+  NormArgs a{to_dt(dtype), rows, d, x, ld_x, residual, ld_residual, weight, eps, h, ld_h, y, ld_y,
+             q ? q->q : nullptr, q ? q->ld : 0, q ? q->scale : nullptr};
+  TW_TRY(norm_rows(a, static_cast<hipStream_t>(stream)), "RMS norm");
+  return TWELL_OK;
+}
+
+size_t twell_rmsnorm_backward_workspace_size(int rows, int d, twell_dtype dtype) {
+  char saved[sizeof(g_err)];
+  memcpy(saved, g_err, sizeof(g_err));
+  const twell_status st = check_norm_shape(rows, d, (int)dtype);
+  memcpy(g_err, saved, sizeof(g_err));
+  return st == TWELL_OK ? norm_backward_ws(rows, d, dtype) : 0;
+}
+
+twell_status twell_rmsnorm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t ld_h, const void *weight,
+                                    const void *dh, int64_t ld_dh, float eps, int rows, int d, twell_dtype dtype,
+                                    void *dx, int64_t ld_dx, float *dweight, void *workspace, size_t ws_bytes,
+                                    void *stream) {
+  g_err[0] = 0;
+  twell_status st = check_norm_shape(rows, d, (int)dtype);
+  if (st != TWELL_OK) return st;
+  if ((st = check_eps(eps)) != TWELL_OK) return st;
+  const int e = dt_size(dtype);
+  if ((st = check_rows("dy", dy, ld_dy, d, e, rows)) != TWELL_OK) return st;
+  if ((st = check_rows("h", h, ld_h, d, e, rows)) != TWELL_OK) return st;
+  if (dh != nullptr && (st = check_rows("dh", dh, ld_dh, d, e, rows)) != TWELL_OK) return st;
+  if ((st = check_rows("dx", dx, ld_dx, d, e, rows)) != TWELL_OK) return st;
+  if (weight == nullptr || dweight == nullptr) return fail(TWELL_ERR_INVALID_ARG, "null weight or dweight");
+  if (!aligned(weight, e) || !aligned(dweight, 4)) return fail(TWELL_ERR_UNSUPPORTED, "misaligned weight or dweight");
+  const size_t need = norm_backward_ws(rows, d, dtype);
+  if (workspace == nullptr || ws_bytes < need)
+    return fail(TWELL_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? ws_bytes : 0);
+  if (!aligned(workspace, ALIGN_WS)) return fail(TWELL_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
+  NormBackwardArgs a{to_dt(dtype), rows, d, dy, ld_dy, h, ld_h, weight, dh, ld_dh, eps, dx, ld_dx, dweight,
+                     static_cast<float *>(workspace), norm_backward_partials(rows, d, to_dt(dtype))};
+  TW_TRY(norm_backward(a, static_cast<hipStream_t>(stream)), "RMS norm backward");
+  return TWELL_OK;
+}
+
+twell_status twell_quantize_rows(const void *x, int64_t ld_x, twell_dtype dtype, const twell_int8 *out,
+                                 void *stream) {
+  g_err[0] = 0;
+  twell_status st = check_int8("out", out);
+  if (st != TWELL_OK) return st;
+  if ((st = check_norm_shape(out->rows, out->cols, (int)dtype)) != TWELL_OK) return st;
+  if ((st = check_rows("x", x, ld_x, out->cols, dt_size(dtype), out->rows)) != TWELL_OK) return st;
+  if (out->rows == 0) return TWELL_OK;
+  NormArgs a{to_dt(dtype), out->rows, out->cols, x, ld_x, nullptr, 0, nullptr, 0.0f, nullptr, 0, nullptr, 0,
+             out->q, out->ld, out->scale};
+  TW_TRY(norm_rows(a, static_cast<hipStream_t>(stream)), "row quantiser");
+  return TWELL_OK;
+}
+
+twell_status twell_int8_matmul(const twell_int8 *a, const twell_int8 *b, const float *row_bias, twell_dtype dtype,
+                               void *y, int64_t ld_y, void *stream) {
+  g_err[0] = 0;
+  if (!valid_dtype((int)dtype)) return fail(TWELL_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  twell_status st = check_int8("a", a);
+  if (st != TWELL_OK) return st;
+  if ((st = check_int8("b", b)) != TWELL_OK) return st;
+  if (a->cols != b->cols) return fail(TWELL_ERR_INVALID_ARG, "a has %d columns, b %d", a->cols, b->cols);
+  if (a->cols > INT8_MAX_K)
+    return fail(TWELL_ERR_UNSUPPORTED, "%d columns not built (at most %d)", a->cols, INT8_MAX_K);
+  if ((st = check_rows("y", y, ld_y, b->rows, dt_size(dtype), a->rows > 0 && b->rows > 0)) != TWELL_OK) return st;
+  if (!aligned(row_bias, 4)) return fail(TWELL_ERR_UNSUPPORTED, "misaligned row_bias");
+  if (a->rows == 0 || b->rows == 0) return TWELL_OK;
+  Int8Args ia{to_dt(dtype), a->rows, b->rows, a->cols, a->q, a->ld, a->scale, b->q, b->ld, b->scale, row_bias, y,
+              ld_y};
+  TW_TRY(int8_matmul(ia, static_cast<hipStream_t>(stream)), "8-bit product");
+  return TWELL_OK;
+}
+
+}  // extern "C"

@@ -282,6 +282,73 @@ hipError_t ffn_backward_dense_dw(const BackwardArgs &a, hipStream_t s);
 int backward_dense_partial_tiles(int dense_cap, int d);
 int backward_dense_rows_padded(int dense_cap, Dt dt);
 
+// Residual RMS norm and the row quantiser (norm.hip).  Row strides (ld_*) are
+// in elements.  weight == null: the quantiser (x rows to 8 bits, r = 1).
+struct NormArgs {
+  Dt dtype;
+  int rows, d;
+  const void *x;
+  int64_t ld_x;
+  const void *residual;  // or null
+  int64_t ld_res;
+  const void *weight;    // [d], or null
+  float eps;
+  void *h;               // x + residual, or null
+  int64_t ld_h;
+  void *y;               // or null
+  int64_t ld_y;
+  int8_t *q;             // or null
+  int64_t ld_q;
+  float *scale;          // [rows] with q
+};
+// A row is held in registers: at most NORM_MAX_CHUNKS chunks of 64 lanes x 16 bytes.
+constexpr int NORM_MAX_CHUNKS = 128;
+inline int norm_chunks(int d, Dt dt) {
+  const int e = 64 * (dt == Dt::BF16 ? 8 : 4);
+  return (d + e - 1) / e;
+}
+hipError_t norm_rows(const NormArgs &a, hipStream_t s);
+
+// Its gradient: dx and, through n_partial rows of fp32 partial sums, dweight.
+struct NormBackwardArgs {
+  Dt dtype;
+  int rows, d;
+  const void *dy;
+  int64_t ld_dy;
+  const void *h;
+  int64_t ld_h;
+  const void *weight;
+  const void *dh;        // gradient arriving at h along the residual stream, or null
+  int64_t ld_dh;
+  float eps;
+  void *dx;
+  int64_t ld_dx;
+  float *dweight;        // [d]
+  float *partial;        // [n_partial][d]
+  int n_partial;         // norm_backward_partials(): the workgroups of the row kernel
+};
+constexpr int NORM_BACKWARD_WGS = 512;
+int norm_backward_partials(int rows, int d, Dt dt);
+hipError_t norm_backward(const NormBackwardArgs &a, hipStream_t s);
+
+// Product of 8-bit rows (int8.hip): a [M][K], b [N][K], rows 16-byte aligned
+// with ceil(K / 16) * 16 readable bytes each; y [M][N] with row stride ld_y.
+constexpr int INT8_MAX_K = 65536;
+struct Int8Args {
+  Dt dtype;              // of y
+  int M, N, K;
+  const int8_t *a;
+  int64_t ld_a;
+  const float *a_scale;  // [M]
+  const int8_t *b;
+  int64_t ld_b;
+  const float *b_scale;  // [N]
+  const float *bias;     // [M] or null
+  void *y;
+  int64_t ld_y;
+};
+hipError_t int8_matmul(const Int8Args &a, hipStream_t s);
+
 // *p = 0 with a one-thread kernel (safe under stream capture).
 hipError_t zero_int(int *p, hipStream_t s);
 

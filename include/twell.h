@@ -484,6 +484,95 @@ twell_status twell_ffn_backward(const twell_hybrid *h, const void *x, const void
                                 float *dw_up, float *dw_down, void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * Operators of the block around the layer: the residual RMS norm in front of
+ * it (and its gradient), rows of 8-bit integers, and the product of such rows.
+ * They take any sizes and row strides: ld_* is a row's distance from the next
+ * in ELEMENTS, at least its length; rows are [rows][d] with unit stride along
+ * d.  Buffers need the alignment of their element type only; rows that are
+ * 16-byte aligned (base and stride) go through wider loads.  The general rules
+ * above (streams, no allocation, host validation) apply, but not their limits
+ * on d and F and their 16-byte alignment.
+ *
+ * twell_int8 -- rows of 8-bit integers with one scale each: the value of
+ * element (t, j) is q[t * ld + j] * scale[t].  q is 16-byte aligned and ld a
+ * multiple of 16; every row has ceil(cols / 16) * 16 READABLE bytes (a buffer
+ * of rows * ld bytes does), of which those past cols hold anything: no
+ * operator writes them, and they do not reach any result.
+ */
+typedef struct {
+  int32_t rows, cols;
+  int64_t ld;           /* bytes from row to row: a multiple of 16, >= cols */
+  int8_t *q;            /* [rows][ld] */
+  float *scale;         /* [rows] */
+} twell_int8;
+
+/*
+ * twell_rmsnorm -- the residual addition and the root-mean-square norm:
+ *     h = round(x + residual)        (h = x when residual is NULL)
+ *     r_t = 1 / sqrt(mean_j h_tj^2 + eps)
+ *     y_tj = round(h_tj * r_t * weight_j)
+ * and, with q non-NULL, the normed rows in 8 bits, formed from the unrounded
+ * values: z = h * weight, m_t = max(max_j |z_tj|, 2^-100),
+ *     q_tj = round-to-even(z_tj * (127 / m_t)),  scale_t = r_t * (m_t / 127).
+ * q does not depend on r (it cancels), so it is the same to the bit for any
+ * order of the sum.  A row with an infinite or NaN z gets q = 0 and scale NaN.
+ * Sums are fp32 (the mean square has to stay below 2^128); the norm is of the
+ * stored (rounded) h, which is what twell_rmsnorm_backward takes.
+ * h, y and q are each optional (NULL: not written), but one of them is needed.
+ * h and y may be x or residual themselves (same address and stride): each row
+ * is read whole before any of it is written.
+ * rows >= 0 (0: nothing is done); d at most 65536 (bf16), 32768 (fp32).
+ * Errors: INVALID_ARG (negative or zero sizes, a stride below d, NULL x or
+ * weight or no output with rows > 0, eps negative or not finite, q's rows or
+ * cols not the input's), UNSUPPORTED (d, alignment), HIP.
+ */
+twell_status twell_rmsnorm(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual,
+                           const void *weight, float eps, int rows, int d, twell_dtype dtype, void *h,
+                           int64_t ld_h, void *y, int64_t ld_y, const twell_int8 *q, void *stream);
+
+/*
+ * twell_rmsnorm_backward -- gradients of y = round(h * r * weight) from the
+ * stored h (rounding passes through as the identity), with g = dy * weight:
+ *     dx_t = round(dh_t + r_t * (g_t - h_t * r_t^2 * mean_j(g_tj * h_tj)))
+ *     dweight_j = sum_t dy_tj * h_tj * r_t
+ * dh: the gradient that reaches h along the residual stream, or NULL for none.
+ * dx is the gradient of h, and so of x and of the residual alike.  dx may be
+ * dy or dh itself (same address and stride).  dweight [d] fp32, overwritten
+ * (zeros with rows == 0).  Sums run in a fixed order (deterministic).
+ * workspace: >= twell_rmsnorm_backward_workspace_size() bytes, 256-byte
+ * aligned (at most 512 rows of d floats).
+ * Errors: as twell_rmsnorm, WORKSPACE.
+ */
+size_t twell_rmsnorm_backward_workspace_size(int rows, int d, twell_dtype dtype);
+twell_status twell_rmsnorm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t ld_h,
+                                    const void *weight, const void *dh, int64_t ld_dh, float eps, int rows,
+                                    int d, twell_dtype dtype, void *dx, int64_t ld_dx, float *dweight,
+                                    void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * twell_quantize_rows -- x [out->rows][out->cols] to 8 bits: twell_rmsnorm's
+ * definition of q and scale with z = x and r = 1.  For the weights (a row per
+ * output channel, once at load time) and for activations that no norm writes.
+ * Errors: as twell_rmsnorm.
+ */
+twell_status twell_quantize_rows(const void *x, int64_t ld_x, twell_dtype dtype, const twell_int8 *out,
+                                 void *stream);
+
+/*
+ * twell_int8_matmul -- the product of 8-bit rows, with a scale for each token
+ * (row of a) and for each output channel (row of b):
+ *     y_mn = round((sum_k a_mk b_nk) * a->scale_m * b->scale_n + row_bias_m)
+ * on the matrix cores, the sums in 32-bit integers (exact).  y [a->rows]
+ * [b->rows] in dtype; row_bias: one fp32 value per row of a (the layer's gate
+ * bias), or NULL.  a->cols == b->cols, at most 65536.  y may not overlap the
+ * inputs.
+ * Errors: INVALID_ARG (NULL pointers, sizes, strides, different cols),
+ * UNSUPPORTED (cols, alignment, a stride that is not a multiple of 16), HIP.
+ */
+twell_status twell_int8_matmul(const twell_int8 *a, const twell_int8 *b, const float *row_bias,
+                               twell_dtype dtype, void *y, int64_t ld_y, void *stream);
+
+/*
  * twell_stream_probe -- streaming HBM probe (a measurement aid, not part of
  * the layer's computation; the pages define no such operation).
  *
