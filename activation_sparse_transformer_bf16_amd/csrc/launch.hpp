@@ -327,7 +327,7 @@ struct NormBackwardArgs {
   float *partial;        // [n_partial][d]
   int n_partial;         // norm_backward_partials(): the workgroups of the row kernel
 };
-constexpr int NORM_BACKWARD_WGS = 512;
+constexpr int NORM_BACKWARD_WGS = 256;
 int norm_backward_partials(int rows, int d, Dt dt);
 hipError_t norm_backward(const NormBackwardArgs &a, hipStream_t s);
 

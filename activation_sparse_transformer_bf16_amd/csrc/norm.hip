@@ -15,9 +15,9 @@
 // values it stands for are NaN and not silently zero.
 //
 // A row stays in the registers of its W waves between its loads and its
-// stores (NC chunks of 16 bytes per lane), so every input is read and every
-// output written once; an output may be the same buffer as an input of the
-// same row, since all of a row's loads come before its stores.
+// stores (NC chunks of 16 bytes per lane, in storage bits), so every input is
+// read and every output written once; an output may be the same buffer as an
+// input of the same row, since all of a row's loads come before its stores.
 #include "launch.hpp"
 
 namespace twell {
@@ -26,69 +26,127 @@ constexpr float Q_MAX = 127.0f;
 constexpr float Q_TINY = 0x1p-100f;
 constexpr uint32_t INF_BITS = 0x7F800000u;
 
-// One 16-byte chunk of a row as fp32: elements e0 .. e0 + E - 1, 0 past d.
-// AL: rows are 16-byte aligned, so a whole chunk is one load.
-template <Dt D, bool AL>
-__device__ __forceinline__ void load_chunk(const void *row, int e0, int d, float (&v)[16 / DtT<D>::size]) {
+// A row of d elements.  AL: 16-byte aligned and a whole number of 16-byte
+// chunks; it is then read and written through a buffer descriptor of exactly
+// its bytes, so that chunks past its end load zeros and store nothing, with no
+// branch.  Otherwise element by element.  `p` is the same for a whole wave.
+//
+// Stores of whole rows (h, y, dx) carry the non-temporal bit: written this way
+// they leave L2 to the inputs (bf16, 8192 x 2048 with residual and 8 bits:
+// 29.6 -> 23.4 us, and no slower with the product that reads them behind it).
+// Stores of q do not: its reader then misses (the quantiser of 8192 x 8192
+// and the 8-bit product together 151 against 160 us).  Loads carry the bit
+// (NT) where no other kernel's copy in cache is worth keeping: in the
+// quantiser (36.3 -> 32.8 us) and the gradient (16384 x 4096: 96 -> 89 us);
+// in the norm it costs 4 us, as x and residual come from the kernel before.
+constexpr int NON_TEMPORAL = 2;
+template <Dt D, bool AL, bool NT = false>
+struct Row {
   using T = typename DtT<D>::T;
-  constexpr int E = 16 / DtT<D>::size;
-  const T *p = static_cast<const T *>(row) + e0;
-  if (AL && e0 + E <= d) {
-    const u32x4_t w = *reinterpret_cast<const u32x4_t *>(p);
-    if constexpr (D == Dt::BF16) {
+  static constexpr int E = 16 / DtT<D>::size;  // elements per chunk
+  __amdgpu_buffer_rsrc_t rsrc;
+  T *p;
+  int d;
+
+  __device__ __forceinline__ Row(const void *base, int64_t t, int64_t ld, int d_)
+      : p(const_cast<T *>(static_cast<const T *>(base)) + t * ld), d(d_) {
+    if constexpr (AL) rsrc = __builtin_amdgcn_make_buffer_rsrc(p, 0, d * (int)sizeof(T), 0x00020000);
+  }
+  // elements e0 .. e0 + E - 1, +0 past the end
+  __device__ __forceinline__ u32x4_t load(int e0) const {
+    if constexpr (AL) {
+      return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rsrc, e0 * (int)sizeof(T), 0, NT ? NON_TEMPORAL : 0));
+    } else {
+      u32x4_t w = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16lo(w[i]);
-        v[2 * i + 1] = bf16hi(w[i]);
+      for (int i = 0; i < E; ++i) {
+        if (e0 + i < d) {
+          if constexpr (D == Dt::BF16)
+            w[i / 2] |= (uint32_t)p[e0 + i] << (16 * (i % 2));
+          else
+            w[i] = __float_as_uint(p[e0 + i]);
+        }
       }
+      return w;
+    }
+  }
+  __device__ __forceinline__ void store(int e0, u32x4_t w) const {
+    if constexpr (AL) {
+      __builtin_amdgcn_raw_buffer_store_b128(w, rsrc, e0 * (int)sizeof(T), 0, NON_TEMPORAL);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+      for (int i = 0; i < E; ++i) {
+        if (e0 + i < d) {
+          if constexpr (D == Dt::BF16)
+            p[e0 + i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+          else
+            p[e0 + i] = __uint_as_float(w[i]);
+        }
+      }
     }
-  } else {
+  }
+};
+
+template <Dt D>
+__device__ __forceinline__ void unpack(u32x4_t w, float (&v)[16 / DtT<D>::size]) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = e0 + i < d ? to_f32(p[i]) : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (D == Dt::BF16) {
+      v[2 * i] = bf16lo(w[i]);
+      v[2 * i + 1] = bf16hi(w[i]);
+    } else {
+      v[i] = __uint_as_float(w[i]);
+    }
   }
 }
 
-// Rounds v to the storage type, in place, and stores the chunk.
-template <Dt D, bool AL>
-__device__ __forceinline__ void store_chunk(void *row, int e0, int d, const float (&v)[16 / DtT<D>::size]) {
-  using T = typename DtT<D>::T;
-  constexpr int E = 16 / DtT<D>::size;
-  T *p = static_cast<T *>(row) + e0;
-  if (AL && e0 + E <= d) {
-    u32x4_t w;
-    if constexpr (D == Dt::BF16) {
+// Rounds to the storage type.
+template <Dt D>
+__device__ __forceinline__ u32x4_t pack_chunk(const float (&v)[16 / DtT<D>::size]) {
+  u32x4_t w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = (uint32_t)bf16_rne(v[2 * i]) | ((uint32_t)bf16_rne(v[2 * i + 1]) << 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
-    }
-    *reinterpret_cast<u32x4_t *>(p) = w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (e0 + i < d) p[i] = from_f32<D>(v[i]);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (D == Dt::BF16)
+      w[i] = (uint32_t)bf16_rne(v[2 * i]) | ((uint32_t)bf16_rne(v[2 * i + 1]) << 16);
+    else
+      w[i] = __float_as_uint(v[i]);
   }
+  return w;
 }
+
+// The chunk's bits only from here on: without this the compiler keeps the
+// unpacked values of the first pass over a row alive for the second, twice the
+// registers, which costs waves or spills.
+__device__ __forceinline__ void keep_packed(u32x4_t &w) { asm volatile("" : "+v"(w)); }
 
 // E (8 or 4) 8-bit values of a row from element e0; rows of q are 16-byte
-// aligned.  Nothing past d is written.
-template <int E>
+// aligned.  Nothing past d is written.  Adding 1.5 * 2^23 to the product
+// rounds it to a whole number (ties to even) whose low byte is the 8-bit
+// value; the product is rounded by itself first (no fused multiply-add), as
+// the definition says.
+template <int E, bool AL>
 __device__ __forceinline__ void store_q(int8_t *row, int e0, int d, const float (&z)[E], float inv, bool bad) {
+#pragma clang fp contract(off)
   uint32_t w[E / 4];
 #pragma unroll
   for (int k = 0; k < E / 4; ++k) {
-    w[k] = 0;
+    uint32_t b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int v = bad ? 0 : (int)rintf(z[4 * k + i] * inv);
-      w[k] |= (uint32_t)(v & 255) << (8 * i);
+      const float p = z[4 * k + i] * inv;
+      b[i] = __float_as_uint(p + 12582912.0f);
     }
+    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u);  // bytes b0, b1, 0, 0
+    const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);  // bytes 0, 0, b2, b3
+    w[k] = bad ? 0u : (lo | hi);
   }
-  if (e0 + E <= d) {
+  if constexpr (AL) {
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(row, 0, d, 0x00020000);
+    if constexpr (E == 8)
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{w[0], w[1]}, rsrc, e0, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b32(w[0], rsrc, e0, 0, 0);
+  } else if (e0 + E <= d) {
     if constexpr (E == 8)
       *reinterpret_cast<u32x2_t *>(row + e0) = u32x2_t{w[0], w[1]};
     else
@@ -100,231 +158,336 @@ __device__ __forceinline__ void store_q(int8_t *row, int e0, int d, const float 
   }
 }
 
-__device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m, 64));
-  return v;
+// Sum and maximum over the 64 lanes of a wave with DPP moves; every lane gets
+// the result (from lane 63).
+__device__ __forceinline__ float wave_total(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wave_sum_to_lane63(v)), 63));
+}
+__device__ __forceinline__ uint32_t wave_top(uint32_t v) {
+#define TWELL_DPP_MAX(CTRL, ROWS) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false))
+  TWELL_DPP_MAX(0xB1, 0xF);   // quad_perm 1,0,3,2
+  TWELL_DPP_MAX(0x4E, 0xF);   // quad_perm 2,3,0,1
+  TWELL_DPP_MAX(0x124, 0xF);  // row_ror 4
+  TWELL_DPP_MAX(0x128, 0xF);  // row_ror 8
+  TWELL_DPP_MAX(0x142, 0xA);  // row_bcast15 into rows 1, 3
+  TWELL_DPP_MAX(0x143, 0xC);  // row_bcast31 into rows 2, 3
+#undef TWELL_DPP_MAX
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// Sum (a, b) and maximum (of bits) over the W waves that hold one row; every
-// lane gets the result, in the same order whatever the lane.
+// Three values of every wave, in LDS.
+struct RowSums {
+  float a, b;
+  uint32_t top;
+};
+
+// Sums and maximum over the W waves that hold one row (`wave` is uniform);
+// the same order for every lane.  `buf`: a slot per wave, not written again
+// before the next barrier.
 template <int W>
-__device__ __forceinline__ void row_reduce(float &a, float &b, uint32_t &top, float (*lds)[3], int wave) {
-  a = wave_sum(a);
-  b = wave_sum(b);
-  top = wave_max_bits(top);
+__device__ __forceinline__ RowSums row_reduce(float a, float b, uint32_t top, RowSums *buf, int wave) {
+  RowSums s{wave_total(a), wave_total(b), wave_top(top)};
   if constexpr (W > 1) {
-    if ((threadIdx.x & 63) == 0) {
-      lds[wave][0] = a;
-      lds[wave][1] = b;
-      lds[wave][2] = __uint_as_float(top);
-    }
+    if ((threadIdx.x & 63) == 0) buf[wave] = s;
     __syncthreads();
-    const int w0 = wave / W * W;
-    a = b = 0.0f;
-    top = 0;
+    const RowSums *row = buf + wave / W * W;
+    s = row[0];
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      a += lds[w0 + w][0];
-      b += lds[w0 + w][1];
-      top = max(top, __float_as_uint(lds[w0 + w][2]));
+    for (int w = 1; w < W; ++w) {
+      s.a += row[w].a;
+      s.b += row[w].b;
+      s.top = max(s.top, row[w].top);
     }
   }
+  return s;
 }
 
-// Waves of a workgroup and rows it takes at a time.
+// Waves of a workgroup of the forward and the quantiser.
 constexpr int row_waves(int W) { return W > 4 ? W : 4; }
 
 // x, residual, weight -> h, y, q + scale (each output optional).  NORM false:
-// the plain quantiser (h = x, no weight, r = 1).
+// the plain quantiser (h = x, no weight, r = 1).  With eight chunks per lane
+// the weight is loaded again where it is used instead of being held.
 template <Dt D, int W, int NC, bool AL, bool NORM>
 __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
   constexpr int E = 16 / DtT<D>::size;
-  constexpr int S = DtT<D>::size;
   constexpr int RB = row_waves(W) / W;
-  __shared__ float lds[2][row_waves(W)][3];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr bool HOLD = NORM && NC <= 4;
+  __shared__ RowSums sums[2][row_waves(W)];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int d = a.d;
+  const int first = ((wave % W) * 64 + lane) * E;  // the lane's element of chunk 0
+  constexpr int STEP = W * 64 * E;
+  const Row<D, AL> weight(a.weight, 0, 0, d);
   int turn = 0;
   for (int64_t t0 = (int64_t)blockIdx.x * RB; t0 < a.rows; t0 += (int64_t)gridDim.x * RB) {
     const int64_t t = t0 + wave / W;
     const bool live = t < a.rows;  // the same for all waves of a row
-    const char *xr = static_cast<const char *>(a.x) + t * a.ld_x * S;
-    const char *rr = NORM && a.residual ? static_cast<const char *>(a.residual) + t * a.ld_res * S : nullptr;
-    float v[NC][E], z[NC][E];
-    float ss = 0.0f, none = 0.0f;
+    u32x4_t hv[NC], wv[HOLD ? NC : 1];
+    float ss = 0.0f;
     uint32_t top = 0;
     if (live) {
+      const Row<D, AL, !NORM> x(a.x, t, a.ld_x, d);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) load_chunk<D, AL>(xr, ((c * W + wave % W) * 64 + lane) * E, d, v[c]);
-      if (rr != nullptr) {
+      for (int c = 0; c < NC; ++c) hv[c] = x.load(first + c * STEP);
+      if constexpr (HOLD) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) load_chunk<D, AL>(rr, ((c * W + wave % W) * 64 + lane) * E, d, z[c]);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int i = 0; i < E; ++i) v[c][i] = to_f32(from_f32<D>(v[c][i] + z[c][i]));
+        for (int c = 0; c < NC; ++c) wv[c] = weight.load(first + c * STEP);
       }
-      if constexpr (NORM) {
+      if (NORM && a.residual != nullptr) {
+        const Row<D, AL> residual(a.residual, t, a.ld_res, d);
+        u32x4_t rv[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) load_chunk<D, AL>(a.weight, ((c * W + wave % W) * 64 + lane) * E, d, z[c]);
+        for (int c = 0; c < NC; ++c) rv[c] = residual.load(first + c * STEP);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          float u[E], v[E];
+          unpack<D>(hv[c], u);
+          unpack<D>(rv[c], v);
+#pragma unroll
+          for (int i = 0; i < E; ++i) u[i] += v[i];
+          hv[c] = pack_chunk<D>(u);
+        }
       }
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+      for (int c = 0; c < NC; ++c) {
+        float u[E], z[E];
+        unpack<D>(hv[c], u);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          ss += v[c][i] * v[c][i];
-          if (a.q != nullptr) {
-            const float p = NORM ? v[c][i] * z[c][i] : v[c][i];
-            top = max(top, __float_as_uint(p) & 0x7FFFFFFFu);
-          }
+          if (NORM) ss += u[i] * u[i];
+          z[i] = u[i];
         }
+        if (a.q != nullptr) {
+          if constexpr (NORM) {
+            float w[E];
+            unpack<D>(HOLD ? wv[c] : weight.load(first + c * STEP), w);
+#pragma unroll
+            for (int i = 0; i < E; ++i) z[i] = u[i] * w[i];
+          }
+#pragma unroll
+          for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(z[i]) & 0x7FFFFFFFu);
+        }
+      }
     }
-    row_reduce<W>(ss, none, top, lds[turn], wave);
+    const RowSums s = row_reduce<W>(ss, 0.0f, top, sums[turn], wave);
     turn ^= 1;  // the next row's sums go to the other half: no barrier before they are written
     if (!live) continue;
-    const float r = NORM ? rsqrtf(ss / (float)d + a.eps) : 1.0f;
-    const bool bad = top >= INF_BITS;
-    const float m = fmaxf(__uint_as_float(top), Q_TINY);
-    const float inv = Q_MAX / m;
-    char *hr = a.h ? static_cast<char *>(a.h) + t * a.ld_h * S : nullptr;
-    char *yr = a.y ? static_cast<char *>(a.y) + t * a.ld_y * S : nullptr;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int e0 = ((c * W + wave % W) * 64 + lane) * E;
-      if (NORM && hr != nullptr) store_chunk<D, AL>(hr, e0, d, v[c]);
-      if (NORM && yr != nullptr) {
-        float y[E];
+      keep_packed(hv[c]);
+      if constexpr (HOLD) keep_packed(wv[c]);
+    }
+    const float r = NORM ? rsqrtf(s.a / (float)d + a.eps) : 1.0f;
+    const bool bad = s.top >= INF_BITS;
+    const float m = fmaxf(__uint_as_float(s.top), Q_TINY);
+    const float inv = Q_MAX / m;
+    const Row<D, AL> h(a.h, t, a.ld_h, d), y(a.y, t, a.ld_y, d);
 #pragma unroll
-        for (int i = 0; i < E; ++i) y[i] = v[c][i] * r * z[c][i];
-        store_chunk<D, AL>(yr, e0, d, y);
-      }
-      if (a.q != nullptr) {
-        float p[E];
+    for (int c = 0; c < NC; ++c) {
+      const int e0 = first + c * STEP;
+      float u[E];
+      unpack<D>(hv[c], u);
+      if constexpr (NORM) {
+        float w[E];
+        unpack<D>(HOLD ? wv[c] : weight.load(e0), w);
+        if (a.h != nullptr) h.store(e0, hv[c]);
+        if (a.y != nullptr) {
+          float v[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) p[i] = NORM ? v[c][i] * z[c][i] : v[c][i];
-        store_q<E>(a.q + t * a.ld_q, e0, d, p, inv, bad);
+          for (int i = 0; i < E; ++i) v[i] = u[i] * r * w[i];
+          y.store(e0, pack_chunk<D>(v));
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[i] *= w[i];
       }
+      if (a.q != nullptr) store_q<E, AL>(a.q + t * a.ld_q, e0, d, u, inv, bad);
     }
     if (a.q != nullptr && lane == 0 && wave % W == 0)
       a.scale[t] = bad ? __uint_as_float(0x7FC00000u) : r * (m / Q_MAX);
   }
 }
 
-// Gradient: a workgroup walks rows t = its own, + grid, ...; each wave keeps
-// its columns' dw sums in registers over all its rows, the workgroup adds its
-// row groups in order and writes one row of partial sums.
+// Gradient: a workgroup of 16 waves walks groups of RB = 16 / W rows, its
+// own, + grid, ...; each wave keeps its columns' dw sums in registers over all
+// its rows, the workgroup adds its row groups in order and writes one row of
+// partial sums.  The weight is held in registers where it fits, and loaded for each
+// row where it does not; with eight chunks per lane the registers hold no sums
+// either: the workgroup, which then takes one row at a time, adds each row to
+// its partial row in memory (every element by the one lane that owns it).
+constexpr int BACK_WAVES = 16;
 template <Dt D, int W, int NC, bool AL>
-__global__ __launch_bounds__(64 * row_waves(W)) void k_norm_backward(NormBackwardArgs a) {
+__global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardArgs a) {
   constexpr int E = 16 / DtT<D>::size;
-  constexpr int S = DtT<D>::size;
-  constexpr int RW = row_waves(W), RB = RW / W;
-  __shared__ float lds[2][RW][3];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int RB = BACK_WAVES / W;
+  constexpr bool HOLD = NC <= 4;         // the sums
+  constexpr bool HOLD_W = NC * E <= 16;  // the weight
+  static_assert(HOLD || RB == 1, "sums in memory: one row per workgroup at a time");
+  __shared__ RowSums sums[2][BACK_WAVES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int d = a.d;
-  float w[NC][E], dw[NC][E];
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    load_chunk<D, AL>(a.weight, ((c * W + wave % W) * 64 + lane) * E, d, w[c]);
-#pragma unroll
-    for (int i = 0; i < E; ++i) dw[c][i] = 0.0f;
-  }
-  int turn = 0;
-  for (int64_t t0 = (int64_t)blockIdx.x * RB; t0 < a.rows; t0 += (int64_t)gridDim.x * RB) {
-    const int64_t t = t0 + wave / W;
-    const bool live = t < a.rows;
-    float h[NC][E], g[NC][E];
-    float ss = 0.0f, dot = 0.0f;
-    if (live) {
-      const char *hr = static_cast<const char *>(a.h) + t * a.ld_h * S;
-      const char *gr = static_cast<const char *>(a.dy) + t * a.ld_dy * S;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        load_chunk<D, AL>(hr, ((c * W + wave % W) * 64 + lane) * E, d, h[c]);
-        load_chunk<D, AL>(gr, ((c * W + wave % W) * 64 + lane) * E, d, g[c]);
-      }
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          ss += h[c][i] * h[c][i];
-          dot += g[c][i] * w[c][i] * h[c][i];
-        }
-    }
-    uint32_t top = 0;
-    row_reduce<W>(ss, dot, top, lds[turn], wave);
-    turn ^= 1;  // the next row's sums go to the other half: no barrier before they are written
-    if (live) {
-      const float r = rsqrtf(ss / (float)d + a.eps);
-      const float k = r * r * (dot / (float)d);
-      const char *sr = a.dh ? static_cast<const char *>(a.dh) + t * a.ld_dh * S : nullptr;
-      char *xr = static_cast<char *>(a.dx) + t * a.ld_dx * S;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int e0 = ((c * W + wave % W) * 64 + lane) * E;
-        float o[E];
-        if (sr != nullptr)
-          load_chunk<D, AL>(sr, e0, d, o);
-        else
-#pragma unroll
-          for (int i = 0; i < E; ++i) o[i] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          dw[c][i] += g[c][i] * h[c][i] * r;
-          o[i] += r * (g[c][i] * w[c][i] - h[c][i] * k);
-        }
-        store_chunk<D, AL>(xr, e0, d, o);
-      }
-    }
-  }
-  // the workgroup's partial row: its RB row groups added in order
+  const int first = ((wave % W) * 64 + lane) * E;
+  constexpr int STEP = W * 64 * E;
   float *out = a.partial + (size_t)blockIdx.x * d;
-  if constexpr (RB == 1) {
+  const Row<D, AL> weight(a.weight, 0, 0, d);
+  u32x4_t wv[HOLD_W ? NC : 1];
+  float dw[HOLD ? NC : 1][E];
+  if constexpr (HOLD_W) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) wv[c] = weight.load(first + c * STEP);
+  }
+  if constexpr (HOLD) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int e = ((c * W + wave % W) * 64 + lane) * E + i;
-        if (e < d) out[e] = dw[c][i];
-      }
+      for (int i = 0; i < E; ++i) dw[c][i] = 0.0f;
   } else {
-    __shared__ float sum[RB][W * 64 * E];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      for (int i = 0; i < E; ++i)
+        if (first + c * STEP + i < d) out[first + c * STEP + i] = 0.0f;
+  }
+  // A wave's rows are t, t + step, ...: with at most two chunks per lane the
+  // next row is loaded before the present one is worked on.
+  const int64_t step = (int64_t)gridDim.x * RB;
+  constexpr bool AHEAD = NC <= 2;
+  u32x4_t hv[NC], gv[NC], sv[NC];
+  auto load_row = [&](int64_t t) {
+    if (t >= a.rows) return;
+    const Row<D, AL, true> h(a.h, t, a.ld_h, d), dy(a.dy, t, a.ld_dy, d);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      __syncthreads();
+      hv[c] = h.load(first + c * STEP);
+      gv[c] = dy.load(first + c * STEP);
+    }
+    if (AHEAD && a.dh != nullptr) {
+      const Row<D, AL, true> dh(a.dh, t, a.ld_dh, d);
 #pragma unroll
-      for (int i = 0; i < E; ++i) sum[wave / W][((wave % W) * 64 + lane) * E + i] = dw[c][i];
-      __syncthreads();
-      for (int e = threadIdx.x; e < W * 64 * E; e += 64 * RW) {
-        float s = 0.0f;
+      for (int c = 0; c < NC; ++c) sv[c] = dh.load(first + c * STEP);
+    }
+  };
 #pragma unroll
-        for (int g = 0; g < RB; ++g) s += sum[g][e];
-        const int j = c * W * 64 * E + e;
-        if (j < d) out[j] = s;
+  for (int c = 0; c < NC; ++c) sv[c] = u32x4_t{0u, 0u, 0u, 0u};
+  int turn = 0;
+  if (AHEAD) load_row((int64_t)blockIdx.x * RB + wave / W);
+  for (int64_t t0 = (int64_t)blockIdx.x * RB; t0 < a.rows; t0 += step) {
+    const int64_t t = t0 + wave / W;
+    const bool live = t < a.rows;
+    if (!AHEAD) load_row(t);
+    u32x4_t hc[NC], gc[NC], sc[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      hc[c] = hv[c];
+      gc[c] = gv[c];
+      sc[c] = sv[c];
+    }
+    if (AHEAD) load_row(t + step);
+    float ss = 0.0f, dot = 0.0f;
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float h[E], g[E], w[E];
+        unpack<D>(hc[c], h);
+        unpack<D>(gc[c], g);
+        unpack<D>(HOLD_W ? wv[c] : weight.load(first + c * STEP), w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          ss += h[i] * h[i];
+          dot += g[i] * w[i] * h[i];
+        }
+      }
+    }
+    const RowSums s = row_reduce<W>(ss, dot, 0u, sums[turn], wave);
+    turn ^= 1;
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        keep_packed(hc[c]);
+        keep_packed(gc[c]);
+        if constexpr (HOLD_W) keep_packed(wv[c]);
+      }
+      const float r = rsqrtf(s.a / (float)d + a.eps);
+      const float k = r * r * (s.b / (float)d);
+      const Row<D, AL, true> dh(a.dh, t, a.ld_dh, d), dx(a.dx, t, a.ld_dx, d);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int e0 = first + c * STEP;
+        float h[E], g[E], w[E], o[E];
+        unpack<D>(hc[c], h);
+        unpack<D>(gc[c], g);
+        unpack<D>(HOLD_W ? wv[c] : weight.load(e0), w);
+        if (!AHEAD && a.dh != nullptr) sc[c] = dh.load(e0);
+        unpack<D>(sc[c], o);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const float p = g[i] * h[i] * r;
+          if constexpr (HOLD)
+            dw[c][i] += p;
+          else if (e0 + i < d)
+            out[e0 + i] += p;
+          o[i] += r * (g[i] * w[i] - h[i] * k);
+        }
+        dx.store(e0, pack_chunk<D>(o));
+        // one chunk after the other: interleaved, their values do not fit the registers
+        if constexpr (NC > 2) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  if constexpr (HOLD) {
+    // the workgroup's partial row: its RB row groups added in order
+    if constexpr (RB == 1) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (first + c * STEP + i < d) out[first + c * STEP + i] = dw[c][i];
+    } else {
+      __shared__ float sum[RB][STEP];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < E; ++i) sum[wave / W][first + i] = dw[c][i];
+        __syncthreads();
+        for (int e = threadIdx.x; e < STEP; e += 64 * BACK_WAVES) {
+          float v = 0.0f;
+#pragma unroll
+          for (int g = 0; g < RB; ++g) v += sum[g][e];
+          if (c * STEP + e < d) out[c * STEP + e] = v;
+        }
       }
     }
   }
 }
 
-// dw_j = the partial rows added in order: 64 columns per workgroup, 16 groups
-// of rows, their sums added in order.
-constexpr int DW_GROUPS = 16;
-__global__ __launch_bounds__(64 * DW_GROUPS) void k_norm_dweight(const float *__restrict__ partial, int n, int d,
-                                                                 float *__restrict__ dweight) {
-  __shared__ float sum[DW_GROUPS][64];
-  const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
-  const int j = blockIdx.x * 64 + lane;
-  const int per = (n + DW_GROUPS - 1) / DW_GROUPS;
-  float s = 0.0f;
-  if (j < d)
-    for (int i = grp * per; i < min(n, (grp + 1) * per); ++i) s += partial[(size_t)i * d + j];
-  sum[grp][lane] = s;
-  __syncthreads();
-  if (grp == 0 && j < d) {
-    float v = 0.0f;
+// dw_j = the partial rows added in a fixed order: 16 columns per workgroup, 64
+// groups of consecutive rows, then the groups in order.
+constexpr int DW_COLS = 16, DW_GROUPS = 64;
+static_assert(NORM_BACKWARD_WGS % DW_GROUPS == 0, "whole loads per group");
+__global__ __launch_bounds__(DW_COLS *DW_GROUPS) void k_norm_dweight(const float *__restrict__ partial, int n, int d,
+                                                                     float *__restrict__ dweight) {
+  constexpr int PER = NORM_BACKWARD_WGS / DW_GROUPS;
+  __shared__ float sum[DW_GROUPS][DW_COLS + 1];
+  const int col = threadIdx.x % DW_COLS, grp = threadIdx.x / DW_COLS;
+  const int j = blockIdx.x * DW_COLS + col;
+  float v[PER];
 #pragma unroll
-    for (int g = 0; g < DW_GROUPS; ++g) v += sum[g][lane];
-    dweight[j] = v;
+  for (int i = 0; i < PER; ++i) {
+    const int row = grp * PER + i;
+    v[i] = j < d && row < n ? partial[(size_t)row * d + j] : 0.0f;
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) s += v[i];
+  sum[grp][col] = s;
+  __syncthreads();
+  if (threadIdx.x < DW_COLS && j < d) {
+    float t = 0.0f;
+#pragma unroll
+    for (int g = 0; g < DW_GROUPS; ++g) t += sum[g][col];
+    dweight[j] = t;
   }
 }
 
@@ -336,9 +499,8 @@ static bool rows16(const void *p, int64_t ld, int s) {
 
 template <Dt D, int W, int NC, bool NORM>
 static hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
-  constexpr int S = DtT<D>::size;
-  constexpr int RB = row_waves(W) / W;
-  const bool al = rows16(a.x, a.ld_x, S) && rows16(a.residual, a.ld_res, S) && rows16(a.weight, 0, S) &&
+  constexpr int S = DtT<D>::size, RB = row_waves(W) / W;
+  const bool al = (a.d * S) % 16 == 0 && rows16(a.x, a.ld_x, S) && rows16(a.residual, a.ld_res, S) && rows16(a.weight, 0, S) &&
                   rows16(a.h, a.ld_h, S) && rows16(a.y, a.ld_y, S);
   // at most 2^20 workgroups, which take more rows in turn
   const dim3 grid(std::min((a.rows - 1) / RB + 1, 1 << 20)), block(64 * row_waves(W));
@@ -349,14 +511,16 @@ static hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Chunks of 64 lanes x 16 bytes in a row: one wave up to 4 of them, 4 waves
-// up to 16, 16 waves up to NORM_MAX_CHUNKS.
+// Chunks of 64 lanes x 16 bytes in a row: a wave each up to 4 of them, then 4
+// waves, 16 from 17 chunks on (measured at 4, 8 and 16 chunks, W = 1 ... 16:
+// fewer waves with more chunks each hold fewer rows in flight, 24.1 against
+// 23.0 us at 8192 x 2048 bf16; more waves pay for the barrier, 27.9 us).
 template <Dt D, bool NORM>
 static hipError_t norm_rows_dt(const NormArgs &a, hipStream_t s) {
   const int chunks = norm_chunks(a.d, D);
   if (chunks <= 1) return launch_rows<D, 1, 1, NORM>(a, s);
-  if (chunks <= 2) return launch_rows<D, 1, 2, NORM>(a, s);
-  if (chunks <= 4) return launch_rows<D, 1, 4, NORM>(a, s);
+  if (chunks <= 2) return launch_rows<D, 2, 1, NORM>(a, s);
+  if (chunks <= 4) return launch_rows<D, 4, 1, NORM>(a, s);
   if (chunks <= 8) return launch_rows<D, 4, 2, NORM>(a, s);
   if (chunks <= 16) return launch_rows<D, 4, 4, NORM>(a, s);
   if (chunks <= 64) return launch_rows<D, 16, 4, NORM>(a, s);
@@ -374,9 +538,9 @@ hipError_t norm_rows(const NormArgs &a, hipStream_t s) {
 template <Dt D, int W, int NC>
 static hipError_t launch_backward(const NormBackwardArgs &a, hipStream_t s) {
   constexpr int S = DtT<D>::size;
-  const bool al = rows16(a.dy, a.ld_dy, S) && rows16(a.h, a.ld_h, S) && rows16(a.weight, 0, S) &&
+  const bool al = (a.d * S) % 16 == 0 && rows16(a.dy, a.ld_dy, S) && rows16(a.h, a.ld_h, S) && rows16(a.weight, 0, S) &&
                   rows16(a.dh, a.ld_dh, S) && rows16(a.dx, a.ld_dx, S);
-  const dim3 grid(a.n_partial), block(64 * row_waves(W));
+  const dim3 grid(a.n_partial), block(64 * BACK_WAVES);
   if (al)
     hipLaunchKernelGGL((k_norm_backward<D, W, NC, true>), grid, block, 0, s, a);
   else
@@ -389,25 +553,30 @@ static hipError_t backward_dt(const NormBackwardArgs &a, hipStream_t s) {
   const int chunks = norm_chunks(a.d, D);
   if (chunks <= 1) return launch_backward<D, 1, 1>(a, s);
   if (chunks <= 2) return launch_backward<D, 1, 2>(a, s);
-  if (chunks <= 4) return launch_backward<D, 1, 4>(a, s);
+  if (chunks <= 4) return launch_backward<D, 2, 2>(a, s);
   if (chunks <= 8) return launch_backward<D, 4, 2>(a, s);
-  if (chunks <= 16) return launch_backward<D, 4, 4>(a, s);
+  if (chunks <= 16) return launch_backward<D, 8, 2>(a, s);
+  if (chunks <= 32) return launch_backward<D, 16, 2>(a, s);
   if (chunks <= 64) return launch_backward<D, 16, 4>(a, s);
   if (chunks <= NORM_MAX_CHUNKS) return launch_backward<D, 16, 8>(a, s);
   return hipErrorInvalidValue;
 }
 
+// Workgroups of the row kernel: a row group each, at most NORM_BACKWARD_WGS.
 int norm_backward_partials(int rows, int d, Dt dt) {
-  const int rb = norm_chunks(d, dt) <= 4 ? 4 : 1;  // rows per workgroup step
+  const int chunks = norm_chunks(d, dt);
+  const int rb = BACK_WAVES / (chunks <= 2 ? 1 : chunks <= 4 ? 2 : chunks <= 8 ? 4 : chunks <= 16 ? 8 : 16);
   return std::max(1, std::min((int)(((int64_t)rows + rb - 1) / rb), NORM_BACKWARD_WGS));
 }
 
-hipError_t norm_backward(const NormBackwardArgs &a, hipStream_t s) {
-  // with no rows the one workgroup writes a partial row of zeros
+hipError_t norm_backward(const NormBackwardArgs &args, hipStream_t s) {
+  // one workgroup writes dweight itself (zeros with no rows)
+  NormBackwardArgs a = args;
+  if (a.n_partial == 1) a.partial = a.dweight;
   hipError_t e = a.dtype == Dt::BF16 ? backward_dt<Dt::BF16>(a, s) : backward_dt<Dt::F32>(a, s);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_norm_dweight, dim3((a.d + 63) / 64), dim3(64 * DW_GROUPS), 0, s, a.partial, a.n_partial, a.d,
-                     a.dweight);
+  if (e != hipSuccess || a.n_partial == 1) return e;
+  hipLaunchKernelGGL(k_norm_dweight, dim3((a.d + DW_COLS - 1) / DW_COLS), dim3(DW_COLS * DW_GROUPS), 0, s, a.partial,
+                     a.n_partial, a.d, a.dweight);
   return hipGetLastError();
 }
 

@@ -540,7 +540,7 @@ twell_status twell_rmsnorm(const void *x, int64_t ld_x, const void *residual, in
  * dy or dh itself (same address and stride).  dweight [d] fp32, overwritten
  * (zeros with rows == 0).  Sums run in a fixed order (deterministic).
  * workspace: >= twell_rmsnorm_backward_workspace_size() bytes, 256-byte
- * aligned (at most 512 rows of d floats).
+ * aligned (at most 256 rows of d floats).
  * Errors: as twell_rmsnorm, WORKSPACE.
  */
 size_t twell_rmsnorm_backward_workspace_size(int rows, int d, twell_dtype dtype);
