@@ -10,6 +10,7 @@ library has not been built (``python activation_sparse_transformer_bf16_amd/buil
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import NamedTuple, Optional, Tuple
@@ -110,7 +111,8 @@ def _load():
         "twell_rmsnorm_backward_workspace_size": (Z, [I, I, I]),
         "twell_rmsnorm_backward": (I, [P, L, P, L, P, P, L, R, I, I, I, P, L, P, P, Z, P]),
         "twell_quantize_rows": (I, [P, L, I, Q, P]),
-        "twell_int8_matmul": (I, [Q, Q, P, I, P, L, P]),
+        "twell_int8_matmul_workspace_size": (Z, [I, I, I]),
+        "twell_int8_matmul": (I, [Q, Q, P, I, P, L, P, Z, P]),
     }
     # Private function objects: changing argtypes on the public handle (lib())
     # cannot make this binding pass truncated pointers.
@@ -148,7 +150,7 @@ EXPORTS = ("twell_abi_version", "twell_status_str", "twell_last_error", "twell_p
            "twell_stream_probe", "twell_mfma_probe", "twell_ffn_forward_noalloc", "twell_sparse_ffn_grouped",
            "twell_sparse_ffn_grouped_workspace_size",
            "twell_rmsnorm", "twell_rmsnorm_backward_workspace_size", "twell_rmsnorm_backward",
-           "twell_quantize_rows", "twell_int8_matmul")
+           "twell_quantize_rows", "twell_int8_matmul_workspace_size", "twell_int8_matmul")
 
 # Size of the static device scratch behind twell_ffn_forward_noalloc
 # (TWELL_NOALLOC_SCRATCH_BYTES in include/twell.h).
@@ -823,7 +825,12 @@ def twell_quantize_rows(x, q=None, scale=None):
     return q, scale
 
 
-def twell_int8_matmul(a, a_scale, b, b_scale, row_bias=None, dtype=None, y=None):
+@functools.lru_cache(maxsize=4096)
+def twell_int8_matmul_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_lib.twell_int8_matmul_workspace_size(M, N, K))
+
+
+def twell_int8_matmul(a, a_scale, b, b_scale, row_bias=None, dtype=None, y=None, workspace=None):
     """y[m, n] = (sum_k a[m, k] b[n, k]) * a_scale[m] * b_scale[n] (+ row_bias[m])
     for int8 rows a [M, K], b [N, K] as twell_quantize_rows lays them out; y
     [M, N] in ``dtype`` (default bfloat16, or that of a given ``y``)."""
@@ -843,7 +850,12 @@ def twell_int8_matmul(a, a_scale, b, b_scale, row_bias=None, dtype=None, y=None)
         y = a_scale.new_empty((M, N), dtype=dtype)
     else:
         ld_y = _rows(y, "y", device, dtype, (M, N))
-    st = _lib.twell_int8_matmul(ad, bd, bp, code, y.data_ptr(), ld_y, _raw_stream(device))
+    nbytes = twell_int8_matmul_workspace_size(M, N, K)
+    ws, wn = None, 0
+    if nbytes:
+        workspace = _workspace(nbytes, device, workspace)
+        ws, wn = workspace.data_ptr(), workspace.numel()
+    st = _lib.twell_int8_matmul(ad, bd, bp, code, y.data_ptr(), ld_y, ws, wn, _raw_stream(device))
     if st:
         _check(st)
     return y

@@ -920,8 +920,12 @@ twell_status twell_quantize_rows(const void *x, int64_t ld_x, twell_dtype dtype,
   return TWELL_OK;
 }
 
+size_t twell_int8_matmul_workspace_size(int M, int N, int K) {
+  return M < 0 || N < 0 || K <= 0 || K > INT8_MAX_K ? 0 : int8_matmul_workspace(M, N, K);
+}
+
 twell_status twell_int8_matmul(const twell_int8 *a, const twell_int8 *b, const float *row_bias, twell_dtype dtype,
-                               void *y, int64_t ld_y, void *stream) {
+                               void *y, int64_t ld_y, void *workspace, size_t ws_bytes, void *stream) {
   g_err[0] = 0;
   if (!valid_dtype((int)dtype)) return fail(TWELL_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
   twell_status st = check_int8("a", a);
@@ -933,9 +937,13 @@ twell_status twell_int8_matmul(const twell_int8 *a, const twell_int8 *b, const f
   if ((st = check_rows("y", y, ld_y, b->rows, dt_size(dtype), a->rows > 0 && b->rows > 0)) != TWELL_OK) return st;
   if (!aligned(row_bias, 4)) return fail(TWELL_ERR_UNSUPPORTED, "misaligned row_bias");
   if (a->rows == 0 || b->rows == 0) return TWELL_OK;
+  const size_t need = int8_matmul_workspace(a->rows, b->rows, a->cols);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need))
+    return fail(TWELL_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? ws_bytes : 0);
+  if (!aligned(workspace, ALIGN_WS)) return fail(TWELL_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
   Int8Args ia{to_dt(dtype), a->rows, b->rows, a->cols, a->q, a->ld, a->scale, b->q, b->ld, b->scale, row_bias, y,
               ld_y};
-  TW_TRY(int8_matmul(ia, static_cast<hipStream_t>(stream)), "8-bit product");
+  TW_TRY(int8_matmul(ia, workspace, static_cast<hipStream_t>(stream)), "8-bit product");
   return TWELL_OK;
 }
 

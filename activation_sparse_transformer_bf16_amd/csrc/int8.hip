@@ -13,10 +13,12 @@
 // rows hold there does not count.  Rows past M and N repeat the last row and
 // are not stored.
 //
-// Two kernels:
+// Three kernels:
 //  * k_int8_tile: tiles of BM x BN outputs, operands through a ring of LDS
-//    stages (the direct-to-LDS loads and fragment layout of gemm.hpp).
-//  * k_int8_rows: at most 64 rows of a (decoding): 16 columns per workgroup,
+//    stages (the direct-to-LDS loads of gemm.hpp); where the tiles are too few
+//    for the chip, K is cut into ranges whose integer sums go to the workspace,
+//  * k_int8_join, which adds them and writes the results.
+//  * k_int8_rows: at most 16 rows of a (decoding): 16 columns per workgroup,
 //    the waves split K, operands straight into registers.
 #include "gemm.hpp"
 #include "launch.hpp"
@@ -31,6 +33,27 @@ __device__ __forceinline__ float scaled(int acc, float sa, float sb, float bias)
   return (float)acc * sa * sb + bias;
 }
 
+// Four results of one row from column n on.
+template <Dt D>
+__device__ __forceinline__ void store4(typename DtT<D>::T *row, int n, int N, i32x4_t s, float sa,
+                                       const float (&sb)[4], float bias, bool wide) {
+  float v[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = scaled(s[q], sa, sb[q], bias);
+  typename DtT<D>::T *p = row + n;
+  if (wide && n + 4 <= N) {
+    if constexpr (D == Dt::BF16)
+      *reinterpret_cast<u32x2_t *>(p) = u32x2_t{(uint32_t)bf16_rne(v[0]) | ((uint32_t)bf16_rne(v[1]) << 16),
+                                               (uint32_t)bf16_rne(v[2]) | ((uint32_t)bf16_rne(v[3]) << 16)};
+    else
+      *reinterpret_cast<f32x4_t *>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < N) p[q] = from_f32<D>(v[q]);
+  }
+}
+
 // Zeroes the bytes of a 16-byte chunk from its byte `left` on.
 __device__ __forceinline__ u32x4_t keep_bytes(u32x4_t v, int left) {
 #pragma unroll
@@ -41,14 +64,135 @@ __device__ __forceinline__ u32x4_t keep_bytes(u32x4_t v, int left) {
   return v;
 }
 
-// E consecutive results of one row (E * sizeof(T) == 16) from 16 staged bytes.
+// ---- tiles ----------------------------------------------------------------------
+//
+// The products are v_mfma_i32_16x16x64_i8, not the 32x32x32 form of the same
+// rate: per operation it reads and writes half as many accumulators.  On
+// random operands the chip lowers its clock to hold its power, and from
+// registers alone this form then sustains 3.95 POP/s against 3.37.
+
+// Wave-wide copies global -> LDS [lds, lds + 16 or 4 bytes x 64 lanes).  The
+// wait states cover a descriptor or address register written just before by
+// the vector ALU, and M0.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void copy16_buffer(u32x4_t rsrc, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(lds)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void copy16(const void *g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(const void *g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// A fragment read takes 16 rows of four chunks each, lane 16 c + r chunk c of
+// row r.  A 16-byte LDS read is served in four groups of lanes, 0-3, 12-15 and
+// 20-27; 4-11, 16-19 and 28-31; and the same 32 lanes further (measured by
+// letting pairs of lanes collide): each joins four rows of either half of the
+// 16 with chunks c and c + 1.  Exchanging the chunk pairs in the upper eight
+// rows puts a group's 16 lanes on 16 different bank quads.
+template <int SWZ>
+__device__ __forceinline__ int i8_swizzle(int row) {
+  return (row >> SWZ) & 2;
+}
+
+// Rows r0 .. r0 + NR - 1 of one operand, 64 bytes (four 16-byte chunks) of
+// each per slab, slab after slab: NR * 4 lane slots = NR / 16 wave
+// instructions, spread over the WAVES waves.  Chunk c of row r is kept in LDS
+// at c ^ i8_swizzle<SWZ>(r) of its 64-byte row.
+//
+// The loads go through a descriptor that starts at the present slab of the
+// tile's first row and ends with the last chunk of its last row, so that
+// nothing outside the operand is read: lanes past its end load nothing.  Its
+// lane offsets are 32-bit, enough while the tile's rows span less than 2^31
+// bytes; FAR keeps a 64-bit address per lane instead, and repeats the last row
+// and the last chunk where there are no more.
+template <int NR, int WAVES, int SWZ, bool FAR>
+struct I8Rows {
+  static constexpr int PER_WAVE = NR / 16 / WAVES;
+  static_assert(PER_WAVE >= 1 && NR % (16 * WAVES) == 0, "whole 1 KB blocks per wave");
+  uint64_t start;  // of the present slab
+  uint32_t left;   // bytes from there to the end
+  const int8_t *ptr[FAR ? PER_WAVE : 1];
+  uint32_t off[PER_WAVE], lds[PER_WAVE], last;
+
+  __device__ __forceinline__ void init(int wave, int lane, int region, const int8_t *base, int64_t ld, int r0,
+                                       int rows, int K) {
+    last = (uint32_t)(K - 1) / 16 * 16;
+    const int n = min(NR, rows - r0);
+    start = (uint64_t)(uintptr_t)(base + (int64_t)r0 * ld);
+    left = (uint32_t)(n - 1) * (uint32_t)ld + last + 16u;
+#pragma unroll
+    for (int j = 0; j < PER_WAVE; ++j) {
+      const int blk = wave * PER_WAVE + j;
+      const int row = blk * 16 + (lane >> 2);
+      const uint32_t c = (uint32_t)((lane & 3) ^ i8_swizzle<SWZ>(row)) * 16;
+      lds[j] = region + blk * 1024;
+      if constexpr (FAR) {
+        ptr[j] = base + (int64_t)min(r0 + row, rows - 1) * ld;
+        off[j] = c;
+      } else {
+        off[j] = (uint32_t)row * (uint32_t)ld + c;
+      }
+    }
+  }
+  // copy j of the present slab into its stage
+  __device__ __forceinline__ void issue(int j, uint32_t stage) {
+    if constexpr (FAR) {
+      copy16(ptr[j] + min(off[j], last), __builtin_amdgcn_readfirstlane((int)(stage + lds[j])));
+    } else {
+      const u32x4_t rsrc = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)start),
+                            (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(start >> 32) & 0xFFFFu)),
+                            (uint32_t)__builtin_amdgcn_readfirstlane((int)left), 0x00020000u};
+      copy16_buffer(rsrc, off[j], __builtin_amdgcn_readfirstlane((int)(stage + lds[j])));
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    if constexpr (FAR) {
+#pragma unroll
+      for (int j = 0; j < PER_WAVE; ++j) off[j] += SLAB;
+    } else {
+      start += SLAB;
+      left -= SLAB;
+    }
+  }
+  __device__ __forceinline__ void issue_all(uint32_t stage) {
+#pragma unroll
+    for (int j = 0; j < PER_WAVE; ++j) issue(j, stage);
+    advance();
+  }
+};
+
+// A fragment: lane l holds chunk l / 16 (K bytes 16 (l / 16) .. + 15) of row l % 16.
+template <int SWZ>
+__device__ __forceinline__ i32x4_t read_i8(const char *region, int row, int lane) {
+  return *reinterpret_cast<const i32x4_t *>(region + row * SLAB + (((lane >> 4) ^ i8_swizzle<SWZ>(row)) << 4));
+}
+
+// The tile column of fragment j's row rho.  A result lane holds rows 4h .. 4h+3
+// of the b fragment (h = lane / 16) in its four registers; bf16 results put
+// the columns so that fragments 2p and 2p + 1 give a lane 8 columns in a row,
+// fp32 ones take them as they come: 16 bytes per lane either way.
 template <Dt D>
-__device__ __forceinline__ void put_results(void *row, int n, int N, u32x4_t v, bool wide) {
+__device__ __forceinline__ int i8_col(int j, int rho) {
+  return D == Dt::BF16 ? 32 * (j >> 1) + 8 * (rho >> 2) + 4 * (j & 1) + (rho & 3) : 16 * j + rho;
+}
+
+// 16 bytes of y per lane; a run that is not whole (past N, or rows that are
+// not 16-byte aligned) goes element by element.
+template <Dt D>
+__device__ __forceinline__ void store_run(void *row, int n, int N, u32x4_t v, bool wide, bool stream) {
   using T = typename DtT<D>::T;
   constexpr int E = 16 / DtT<D>::size;
   T *p = static_cast<T *>(row) + n;
   if (wide && n + E <= N) {
-    *reinterpret_cast<u32x4_t *>(p) = v;
+    if (stream)
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t *>(p));
+    else
+      *reinterpret_cast<u32x4_t *>(p) = v;
   } else {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -61,75 +205,54 @@ __device__ __forceinline__ void put_results(void *row, int n, int N, u32x4_t v, 
   }
 }
 
-// ---- tiles ----------------------------------------------------------------------
-
-// Rows of one operand tile: as DmaRows, with chunks past `last` (the byte
-// offset of a row's last readable chunk) read from there.
-template <int NR, int WAVES>
-struct I8Rows {
-  static constexpr int PER_WAVE = NR / 16 / WAVES;
-  static_assert(PER_WAVE >= 1 && NR % (16 * WAVES) == 0, "whole 1 KB blocks per wave");
-  const int8_t *ptr[PER_WAVE];
-  uint32_t off[PER_WAVE];  // the lane's byte offset in the slab
-  uint32_t lds[PER_WAVE];  // the wave's 1 KB block in the stage
-
-  __device__ __forceinline__ void init(int wave_u, int lane, int region, const int8_t *base, int64_t ld, int r0,
-                                       int rows) {
-#pragma unroll
-    for (int j = 0; j < PER_WAVE; ++j) {
-      const int blk = wave_u * PER_WAVE + j;
-      const int row = blk * 16 + (lane >> 2);
-      off[j] = ((lane & 3) ^ ((row >> 2) & 3)) * 16;
-      ptr[j] = base + (int64_t)min(r0 + row, rows - 1) * ld;
-      lds[j] = region + blk * 1024;
-    }
-  }
-  __device__ __forceinline__ void issue(int kt, uint32_t last, uint32_t stage) {
-#pragma unroll
-    for (int j = 0; j < PER_WAVE; ++j) dma16(ptr[j] + min(off[j] + (uint32_t)kt * SLAB, last), stage + lds[j]);
-  }
-};
-
-// The second operand's rows become the lanes of the result and the first's its
-// registers: with b first, a lane holds one row m and runs of 4 columns n.
-template <int NWM, int NWN>
-__device__ __forceinline__ void mfma_i8(i32x16_t (&acc)[NWM][NWN], const Frag<NWM, NWN> &f) {
-#pragma unroll
-  for (int i = 0; i < NWM; ++i)
-#pragma unroll
-    for (int j = 0; j < NWN; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, f.b[j]),
-                                                       __builtin_bit_cast(i32x4_t, f.a[i]), acc[i][j], 0, 0, 0);
+// LDS writes of a wave visible to the whole wave.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// LDS: the ring, then sa, bias and sb of the tile (fp32).
 template <class Cfg, int BN>
 struct I8Tile {
   static constexpr int RING = gemm_dma_ring_bytes<Cfg>(BN);
-  static constexpr int VALS = 2 * Cfg::BM + BN;  // sa, bias, sb
-  static constexpr int PITCH = 64 * 4 + 16;      // bytes of a staged row of 64 fp32 results
-  static constexpr int STAGED = Cfg::WAVES * 32 * PITCH;
-  static constexpr int LDS = (RING > STAGED ? RING : STAGED) + VALS * 4;
+  static constexpr int VALS = 2 * Cfg::BM + BN;
+  static_assert(Cfg::BM % 64 == 0 && BN % 64 == 0, "copied 64 at a time");
+  static constexpr int LDS = RING + VALS * 4;
 };
 
-template <Dt D, class Cfg, int BN>
-__global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile(Int8Args a, bool wide) {
+// Tiles of BM x BN outputs through a ring of LDS stages (gemm.hpp): a wave owns
+// 64 columns (4 b fragments) and 2 H 16-row blocks of a, taken in two halves
+// of H.  Registers hold the b fragments, and both halves of a: while the lower
+// half is multiplied the upper one is read, and while the upper half is
+// multiplied the next slab's lower half, each b fragment after its last use.
+template <Dt D, class Cfg, int BN, bool FAR>
+__global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile(Int8Args a, bool wide,
+                                                                                     bool stream, int tiles) {
   using T = typename DtT<D>::T;
   using WT = WaveTile<BN, Cfg>;
   using L = I8Tile<Cfg, BN>;
   constexpr int BM = Cfg::BM, WAVES = Cfg::WAVES, STAGES = Cfg::STAGES;
-  constexpr int NWM = WT::NWM, NWN = WT::NWN;
+  constexpr int H = WT::NWM, NB = 4;
   constexpr int STAGE = (BM + BN) * SLAB;
-  constexpr int OPS = I8Rows<BM, WAVES>::PER_WAVE + I8Rows<BN, WAVES>::PER_WAVE;
+  constexpr int SB = D == Dt::BF16 ? 3 : 2;  // b's swizzle: the rows of a fragment are 8 (4) apart in groups of 4
+  using RowsA = I8Rows<BM, WAVES, 2, FAR>;
+  using RowsB = I8Rows<BN, WAVES, SB, FAR>;
+  constexpr int OPS = RowsA::PER_WAVE + RowsB::PER_WAVE;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row0 = WT::row0(wave), col0 = WT::col0(wave);
   int tm, tn;
-  tile_coords(blockIdx.x, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN, tm, tn);
+  tile_coords(blockIdx.x % tiles, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
+  // this workgroup's range of K: from here on the operands begin and end with it
+  const int part = blockIdx.x / tiles;
+  const int k0 = part * a.k_part;
+  a.a += k0;
+  a.b += k0;
+  a.K = min(a.K - k0, a.k_part);
   const uint32_t base = lds_address(smem);
-  float *vals = reinterpret_cast<float *>(smem + L::LDS - L::VALS * 4);
-  const uint32_t vbase = base + L::LDS - L::VALS * 4;
 
   // scales and biases, 64 at a time; issued before the stages, so that the
   // stage waits below cover them (loads complete in order)
@@ -138,57 +261,79 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile
     if (g % WAVES != wave) continue;
     const float *src = g < BM / 64       ? a.a_scale + min(m0 + 64 * g + lane, a.M - 1)
                        : g < 2 * BM / 64 ? (a.bias ? a.bias + min(m0 + 64 * (g - BM / 64) + lane, a.M - 1) : nullptr)
-                                         : a.b_scale + min(n0 + 64 * (g - 2 * BM / 64) + lane, a.N - 1);
-    if (g < BM / 64 || g >= 2 * BM / 64 || a.bias != nullptr) dma4(src, vbase + 256 * g);
+                                            : a.b_scale + min(n0 + 64 * (g - 2 * BM / 64) + lane, a.N - 1);
+    if (g < BM / 64 || g >= 2 * BM / 64 || a.bias != nullptr)
+      copy4(src, __builtin_amdgcn_readfirstlane((int)(base + L::RING + 256 * g)));
   }
-  I8Rows<BM, WAVES> da;
-  I8Rows<BN, WAVES> db;
-  da.init(wave, lane, 0, a.a, a.ld_a, m0, a.M);
-  db.init(wave, lane, BM * SLAB, a.b, a.ld_b, n0, a.N);
+  RowsA da;
+  RowsB db;
+  da.init(wave, lane, 0, a.a, a.ld_a, m0, a.M, a.K);
+  db.init(wave, lane, BM * SLAB, a.b, a.ld_b, n0, a.N, a.K);
   const int nk = (a.K + SLAB - 1) / SLAB;
-  const uint32_t last = (uint32_t)(a.K - 1) / 16 * 16;
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) {
     if (s < nk) {
-      da.issue(s, last, base + s * STAGE);
-      db.issue(s, last, base + s * STAGE);
+      da.issue_all(base + s * STAGE);
+      db.issue_all(base + s * STAGE);
     }
   }
-  i32x16_t acc[NWM][NWN];
+  i32x4_t acc[2 * H][NB];
 #pragma unroll
-  for (int i = 0; i < NWM; ++i)
+  for (int i = 0; i < 2 * H; ++i)
 #pragma unroll
-    for (int j = 0; j < NWN; ++j)
+    for (int j = 0; j < NB; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  const int rho = lane & 15;
+  i32x4_t alo[H], ahi[H], b[NB];
+  auto read_a = [&](i32x4_t(&f)[H], int slot, int half) {
 #pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
+    for (int i = 0; i < H; ++i) f[i] = read_i8<2>(smem + slot * STAGE, row0 + 16 * (half * H + i) + rho, lane);
+  };
+  auto read_b = [&](int j, int slot) {
+    b[j] = read_i8<SB>(smem + slot * STAGE + BM * SLAB, col0 + i8_col<D>(j, rho), lane);
+  };
+  auto multiply = [&](const i32x4_t(&f)[H], int half, int j) {
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+      acc[half * H + i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[j], f[i], acc[half * H + i][j], 0, 0, 0);
+  };
   wait_stages<OPS>(min(nk - 1, STAGES - 1));
   __syncthreads();
-  Frag<NWM, NWN> f0, f1;
-  read_frag<BM>(f0, smem, row0, col0, 0, lane);
+#pragma unroll
+  for (int j = 0; j < NB; ++j) read_b(j, 0);
+  read_a(alo, 0, 0);
   auto slab = [&](auto wait_c, auto issue_c, int kt) {
     constexpr int WAIT = decltype(wait_c)::value;
     constexpr bool ISSUE = decltype(issue_c)::value;
-    const int slot = kt % STAGES;
-    read_frag<BM>(f1, smem + slot * STAGE, row0, col0, 1, lane);
-    mfma_i8(acc, f0);
+    const int slot = kt % STAGES, next = (kt + 1) % STAGES;
+    read_a(ahi, slot, 1);
 #pragma unroll
-    for (int q = 0; q < NWM + NWN; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
-    }
+    for (int j = 0; j < NB; ++j) multiply(alo, 0, j);
+    __builtin_amdgcn_sched_barrier(0);
+    // every wave has read all of slab kt (the barrier waits for its LDS
+    // reads) and slab kt + 1 has landed for every wave
     wait_vmcnt<WAIT * OPS>();
     __syncthreads();
-    if constexpr (ISSUE) {
-      const uint32_t sb = base + slot * STAGE;
-      da.issue(kt + STAGES, last, sb);
-      db.issue(kt + STAGES, last, sb);
-    }
-    read_frag<BM>(f0, smem + ((kt + 1) % STAGES) * STAGE, row0, col0, 0, lane);
-    mfma_i8(acc, f1);
+    read_a(alo, next, 0);
+    // the loads of slab kt + STAGES among the products, not in one block
 #pragma unroll
-    for (int q = 0; q < NWM + NWN; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
+    for (int j = 0; j < NB; ++j) {
+      multiply(ahi, 1, j);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (ISSUE) {
+#pragma unroll
+        for (int q = j; q < OPS; q += NB) {
+          if (q < RowsA::PER_WAVE)
+            da.issue(q, base + slot * STAGE);
+          else
+            db.issue(q - RowsA::PER_WAVE, base + slot * STAGE);
+        }
+      }
+      read_b(j, next);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (ISSUE) {
+      da.advance();
+      db.advance();
     }
   };
   using I0 = std::integral_constant<int, 0>;
@@ -205,187 +350,261 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile
   if (kt == nk - 3) slab(I1(), BF(), kt++);
   if (kt == nk - 2) slab(I0(), BF(), kt++);
   // the last slab: the a side counts up to K only
-  read_frag<BM>(f1, smem + (kt % STAGES) * STAGE, row0, col0, 1, lane);
+  read_a(ahi, kt % STAGES, 1);
   if (a.K % SLAB != 0) {
-    const int left = a.K - kt * SLAB - 16 * (lane >> 5);
+    const int left = a.K - kt * SLAB - 16 * (lane >> 4);
 #pragma unroll
-    for (int i = 0; i < NWM; ++i) {
-      f0.a[i] = keep_bytes(f0.a[i], left);
-      f1.a[i] = keep_bytes(f1.a[i], left - 32);
+    for (int i = 0; i < H; ++i) {
+      alo[i] = __builtin_bit_cast(i32x4_t, keep_bytes(__builtin_bit_cast(u32x4_t, alo[i]), left));
+      ahi[i] = __builtin_bit_cast(i32x4_t, keep_bytes(__builtin_bit_cast(u32x4_t, ahi[i]), left));
     }
   }
-  mfma_i8(acc, f0);
-  mfma_i8(acc, f1);
-  __syncthreads();  // the ring is free: every wave has read its last fragments
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    multiply(alo, 0, j);
+    multiply(ahi, 1, j);
+  }
 
-  // Results: 32 rows x 64 columns at a time through the wave's own LDS rows,
-  // so that global stores are whole runs of a row.
-  constexpr int S = DtT<D>::size;
-  constexpr int PITCH = 64 * S + 16;
-  char *mine = smem + wave * 32 * L::PITCH;
-  const float *va = vals, *vbias = vals + BM, *vb = vals + 2 * BM;
-  const int h = lane >> 5, r = lane & 31;
+  if (a.partial != nullptr) {
+    // the range's sums, 4 columns per lane; rows of n_pad (a multiple of 4)
+    const int n_pad = (a.N + 3) / 4 * 4;
 #pragma unroll
-  for (int i = 0; i < NWM; ++i) {
-    const float sa = va[row0 + 32 * i + r];
-    const float bias = a.bias ? vbias[row0 + 32 * i + r] : 0.0f;
+    for (int i = 0; i < 2 * H; ++i) {
+      const int m = m0 + row0 + 16 * i + rho;
+      if (m >= a.M) continue;
+      int *row = a.partial + ((int64_t)part * a.M + m) * n_pad;
 #pragma unroll
-    for (int j = 0; j < NWN; ++j)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4_t sb = *reinterpret_cast<const f32x4_t *>(vb + col0 + 32 * j + 8 * g + 4 * h);
-        float v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = scaled(acc[i][j][4 * g + q], sa, sb[q], bias);
-        char *dst = mine + r * PITCH + (32 * j + 8 * g + 4 * h) * S;
-        if constexpr (D == Dt::BF16)
-          *reinterpret_cast<u32x2_t *>(dst) = u32x2_t{(uint32_t)bf16_rne(v[0]) | ((uint32_t)bf16_rne(v[1]) << 16),
-                                                     (uint32_t)bf16_rne(v[2]) | ((uint32_t)bf16_rne(v[3]) << 16)};
-        else
-          *reinterpret_cast<f32x4_t *>(dst) = f32x4_t{v[0], v[1], v[2], v[3]};
+      for (int j = 0; j < NB; ++j) {
+        const int n = n0 + col0 + i8_col<D>(j, 4 * (lane >> 4));
+        if (n < a.N) *reinterpret_cast<i32x4_t *>(row + n) = acc[i][j];
       }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    constexpr int PER_ROW = 64 * S / 16;  // lanes per row
-#pragma unroll
-    for (int p = 0; p < 32 * PER_ROW / 64; ++p) {
-      const int rr = p * (64 / PER_ROW) + lane / PER_ROW, c = lane % PER_ROW;
-      const int m = m0 + row0 + 32 * i + rr, n = n0 + col0 + c * (16 / S);
-      const u32x4_t v = *reinterpret_cast<const u32x4_t *>(mine + rr * PITCH + c * 16);
-      if (m < a.M && n < a.N) put_results<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, v, wide);
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    return;
+  }
+  __syncthreads();  // every wave has read its last fragments: the ring is free
+
+  // Results, 16 rows of 64 columns at a time through the wave's own LDS rows,
+  // so that a store covers whole 128-byte lines.
+  constexpr int S = DtT<D>::size;
+  constexpr int PITCH = 64 * S + 16, PER_ROW = 64 * S / 16;  // bytes of a staged row, lanes that store it
+  static_assert(WAVES * 16 * PITCH <= L::RING, "the staged rows fit the ring");
+  char *mine = smem + wave * 16 * PITCH;
+  const float *va = reinterpret_cast<const float *>(smem + L::RING), *vbias = va + BM, *vb = va + 2 * BM;
+  const int h = lane >> 4;
+  f32x4_t sb[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) sb[j] = *reinterpret_cast<const f32x4_t *>(vb + col0 + i8_col<D>(j, 4 * h));
+#pragma unroll
+  for (int i = 0; i < 2 * H; ++i) {
+    const int row = row0 + 16 * i;
+    const float sa = va[row + rho];
+    const float bias = a.bias ? vbias[row + rho] : 0.0f;
+    float v[NB][4];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[j][q] = scaled(acc[i][j][q], sa, sb[j][q], bias);
+#pragma unroll
+    for (int j = 0; j < NB; j += D == Dt::BF16 ? 2 : 1) {
+      u32x4_t w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (D == Dt::BF16)
+          w[k] = (uint32_t)bf16_rne(v[j + k / 2][2 * (k % 2)]) | ((uint32_t)bf16_rne(v[j + k / 2][2 * (k % 2) + 1]) << 16);
+        else
+          w[k] = __float_as_uint(v[j][k]);
+      }
+      *reinterpret_cast<u32x4_t *>(mine + rho * PITCH + i8_col<D>(j, 4 * h) * S) = w;
+    }
+    wave_sync();
+#pragma unroll
+    for (int p = 0; p < PER_ROW / 4; ++p) {
+      const int r = p * (64 / PER_ROW) + lane / PER_ROW, c = lane % PER_ROW;
+      const int m = m0 + row + r, n = n0 + col0 + c * (16 / S);
+      const u32x4_t w = *reinterpret_cast<const u32x4_t *>(mine + r * PITCH + c * 16);
+      if (m < a.M && n < a.N) store_run<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, w, wide, stream);
+    }
+    wave_sync();
+  }
+}
+
+// The ranges' sums added, scaled and written: 4 columns per thread.
+template <Dt D>
+__global__ __launch_bounds__(256) void k_int8_join(Int8Args a, int parts, bool wide) {
+  using T = typename DtT<D>::T;
+  const int n_pad = (a.N + 3) / 4 * 4;
+  const int64_t total = (int64_t)a.M * n_pad / 4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int m = (int)(i / (n_pad / 4)), n = (int)(i % (n_pad / 4)) * 4;
+    const float sa = a.a_scale[m], bias = a.bias ? a.bias[m] : 0.0f;
+    float sb[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sb[q] = a.b_scale[min(n + q, a.N - 1)];
+    i32x4_t s = {0, 0, 0, 0};
+    for (int p = 0; p < parts; ++p) s += *reinterpret_cast<const i32x4_t *>(a.partial + p * total * 4 + i * 4);
+    store4<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, s, sa, sb, bias, wide);
   }
 }
 
 // ---- few rows -------------------------------------------------------------------
 
-// MT blocks of 16 rows of a, NT blocks of 16 columns, WAVES waves that split K
-// in runs of 64 * U bytes.
-template <Dt D, int MT, int NT, int WAVES, int U>
+// 16 rows of a and 16 columns; WAVES waves take runs of 64 * U bytes of K in
+// turn, and add their sums through LDS.
+template <Dt D, int WAVES, int U>
 __global__ __launch_bounds__(64 * WAVES) void k_int8_rows(Int8Args a, bool wide) {
   using T = typename DtT<D>::T;
-  __shared__ i32x4_t red[WAVES][MT * NT][64];
+  __shared__ i32x4_t red[WAVES][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * 16 * NT;
+  const int n0 = blockIdx.x * 16;
   const int r = lane & 15, kl = (lane >> 4) * 16;
-  const int8_t *pa[MT], *pb[NT];
+  const int8_t *pa = a.a + (int64_t)min(r, a.M - 1) * a.ld_a;
+  const int8_t *pb = a.b + (int64_t)min(n0 + r, a.N - 1) * a.ld_b;
+  // the results' row and columns, and their scales, loaded before the sums
+  const int n = n0 + (kl >> 2);
+  const float sa = a.a_scale[min(r, a.M - 1)], bias = a.bias ? a.bias[min(r, a.M - 1)] : 0.0f;
+  float sb[4];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) pa[i] = a.a + (int64_t)min(16 * i + r, a.M - 1) * a.ld_a;
-#pragma unroll
-  for (int j = 0; j < NT; ++j) pb[j] = a.b + (int64_t)min(n0 + 16 * j + r, a.N - 1) * a.ld_b;
-  i32x4_t acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  for (int q = 0; q < 4; ++q) sb[q] = a.b_scale[min(n + q, a.N - 1)];
+  i32x4_t acc = {0, 0, 0, 0};
   const int last = (a.K - 1) / 16 * 16;
   for (int k0 = wave * 64 * U; k0 < a.K; k0 += WAVES * 64 * U) {
-    u32x4_t fa[U][MT], fb[U][NT];
+    u32x4_t fa[U], fb[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = min(k0 + 64 * u + kl, last);
+    for (int u = 0; u < U; ++u) fb[u] = *reinterpret_cast<const u32x4_t *>(pb + min(k0 + 64 * u + kl, last));
 #pragma unroll
-      for (int j = 0; j < NT; ++j) fb[u][j] = *reinterpret_cast<const u32x4_t *>(pb[j] + k);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = min(k0 + 64 * u + kl, last);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fa[u][i] = *reinterpret_cast<const u32x4_t *>(pa[i] + k);
-    }
+    for (int u = 0; u < U; ++u) fa[u] = *reinterpret_cast<const u32x4_t *>(pa + min(k0 + 64 * u + kl, last));
     if (k0 + 64 * U > a.K) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) fa[u][i] = keep_bytes(fa[u][i], a.K - (k0 + 64 * u + kl));
+      for (int u = 0; u < U; ++u) fa[u] = keep_bytes(fa[u], a.K - (k0 + 64 * u + kl));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, fb[u][j]),
-                                                           __builtin_bit_cast(i32x4_t, fa[u][i]), acc[i][j], 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, fb[u]),
+                                                 __builtin_bit_cast(i32x4_t, fa[u]), acc, 0, 0, 0);
   }
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) red[wave][i * NT + j][lane] = acc[i][j];
+  red[wave][lane] = acc;
   __syncthreads();
-  // wave w adds the waves' sums of blocks w, w + WAVES, ...: integers, so the
-  // order does not matter; a lane holds row lane % 16 and 4 columns
-  for (int blk = wave; blk < MT * NT; blk += WAVES) {
-    i32x4_t s = red[0][blk][lane];
+  if (wave == 0 && r < a.M && n < a.N) {
+    i32x4_t s = red[0][lane];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) s += red[w][blk][lane];
-    const int m = 16 * (blk / NT) + r, n = n0 + 16 * (blk % NT) + 4 * (lane >> 4);
-    if (m >= a.M || n >= a.N) continue;
-    const float sa = a.a_scale[m], bias = a.bias ? a.bias[m] : 0.0f;
-    float v[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = scaled(s[q], sa, a.b_scale[min(n + q, a.N - 1)], bias);
-    T *p = static_cast<T *>(a.y) + (int64_t)m * a.ld_y + n;
-    if (wide && n + 4 <= a.N) {
-      if constexpr (D == Dt::BF16)
-        *reinterpret_cast<u32x2_t *>(p) = u32x2_t{(uint32_t)bf16_rne(v[0]) | ((uint32_t)bf16_rne(v[1]) << 16),
-                                                 (uint32_t)bf16_rne(v[2]) | ((uint32_t)bf16_rne(v[3]) << 16)};
-      else
-        *reinterpret_cast<f32x4_t *>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (n + q < a.N) p[q] = from_f32<D>(v[q]);
-    }
+    for (int w = 1; w < WAVES; ++w) s += red[w][lane];
+    store4<D>(static_cast<T *>(a.y) + (int64_t)r * a.ld_y, n, a.N, s, sa, sb, bias, wide);
   }
 }
 
 // ---- launch -----------------------------------------------------------------------
 
-using I8Big = DmaCfg<256, 8, 4>;
-using I8Mid = DmaCfg<128, 4, 4>;
-using I8Small = DmaCfg<64, 4, 4>;
+// The tile shapes: rows, columns, and the time of one 64-byte slab of K per
+// tile on a CU, in units of 10 ns (measured over K = 2048 and 8192 with the
+// chip full; the smaller ones are bound by the loads a CU can have in flight,
+// the largest by the power of the matrix cores).
+enum I8Shape { I8_256x256, I8_256x128, I8_128x128, I8_64x128, I8_SHAPES };
+struct I8ShapeCost {
+  int bm, bn, slab;
+};
+constexpr I8ShapeCost I8_COST[I8_SHAPES] = {{256, 256, 80}, {256, 128, 53}, {128, 128, 30}, {64, 128, 19}};
+constexpr int I8_TILE_COST = 250;   // of a tile besides its slabs: start, ring fill, results
+constexpr int I8_JOIN_COST = 250;   // of the second launch
+constexpr int I8_MAX_PARTS = 16;
+constexpr size_t I8_MAX_PARTIAL = (size_t)64 << 20;
 
-template <Dt D, class Cfg, int BN>
-static hipError_t launch_tile(const Int8Args &a, bool wide, hipStream_t s) {
-  auto kern = k_int8_tile<D, Cfg, BN>;
+struct I8Plan {
+  int shape, parts, k_part;  // parts == 1: no workspace
+  size_t bytes;
+};
+
+static int64_t i8_tiles(int shape, int M, int N) {
+  return (int64_t)((M - 1) / I8_COST[shape].bm + 1) * ((N - 1) / I8_COST[shape].bn + 1);
+}
+
+// The shape and number of K ranges with the least estimated time: 256 CUs take
+// the tiles in rounds; the ranges' sums are written and read once (4 bytes
+// each way at about 4 TB/s).
+static I8Plan i8_plan(int M, int N, int K) {
+  const int nk = (K + SLAB - 1) / SLAB;
+  I8Plan best{I8_256x256, 1, nk * SLAB, 0};
+  int64_t least = INT64_MAX;
+  for (int shape = 0; shape < I8_SHAPES; ++shape) {
+    const int64_t tiles = i8_tiles(shape, M, N);
+    for (int want = 1; want <= I8_MAX_PARTS; want *= 2) {
+      const int per = (nk + want - 1) / want, parts = (nk + per - 1) / per;
+      const size_t sums = (size_t)parts * M * ((N + 3) / 4 * 4);
+      if (want > 1 && (parts < want || per < 4 || sums * 4 > I8_MAX_PARTIAL)) break;
+      const int64_t rounds = (tiles * parts + 255) / 256;
+      const int64_t cost = rounds * (per * I8_COST[shape].slab + I8_TILE_COST) +
+                           (parts > 1 ? I8_JOIN_COST + (int64_t)(sums / 5000) : 0);
+      if (cost < least) {
+        least = cost;
+        best = I8Plan{shape, parts, per * SLAB, parts > 1 ? sums * 4 : 0};
+      }
+    }
+  }
+  return best;
+}
+
+// Rows too far apart for 32-bit offsets within a tile: those go through
+// 64-bit addresses, in one tile shape and without ranges.
+static bool i8_far(const Int8Args &a) {
+  return std::max(a.ld_a, a.ld_b) > ((int64_t)1 << 31) / 256 - INT8_MAX_K;
+}
+
+// At most 16 rows: one block of rows, and the matrix instruction's shape leaves
+// nothing to share.  5.4 us for one token of 8192 x 2048, 8 us from tiles.
+static bool i8_few(int M) { return M <= 16; }
+
+size_t int8_matmul_workspace(int M, int N, int K) {
+  return M <= 0 || N <= 0 || i8_few(M) ? 0 : i8_plan(M, N, K).bytes;
+}
+
+template <Dt D, class Cfg, int BN, bool FAR = false>
+static hipError_t launch_tile(const Int8Args &a, int parts, bool wide, hipStream_t s) {
+  auto kern = k_int8_tile<D, Cfg, BN, FAR>;
   constexpr int lds = I8Tile<Cfg, BN>::LDS;
   hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   const int64_t tiles = (int64_t)((a.M - 1) / Cfg::BM + 1) * ((a.N - 1) / BN + 1);
-  if (tiles > (1 << 22)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(Cfg::THREADS), lds, s, a, wide);
-  return hipGetLastError();
-}
-
-template <Dt D, int MT, int NT, int WAVES, int U>
-static hipError_t launch_few(const Int8Args &a, bool wide, hipStream_t s) {
-  hipLaunchKernelGGL((k_int8_rows<D, MT, NT, WAVES, U>), dim3((a.N - 1) / (16 * NT) + 1), dim3(64 * WAVES), 0, s, a,
-                     wide);
+  if (tiles * parts > (1 << 22)) return hipErrorInvalidValue;
+  // Results beyond the Infinity Cache are stored non-temporally, so that they
+  // do not take cache lines from the operands of the tiles still to come (470
+  // MB, 16384 x 14336 x 4096: 765 against 802 us); smaller ones stay there for
+  // their reader (134 MB, 8192 x 8192 x 2048: 127 against 129 us).
+  const bool stream = (size_t)a.M * a.N * DtT<D>::size > ((size_t)256 << 20);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * parts)), dim3(Cfg::THREADS), lds, s, a, wide, stream, (int)tiles);
   return hipGetLastError();
 }
 
 template <Dt D>
-static hipError_t matmul_dt(const Int8Args &a, hipStream_t s) {
+static hipError_t matmul_dt(const Int8Args &args, void *workspace, hipStream_t s) {
+  Int8Args a = args;
   const bool wide = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && (a.ld_y * DtT<D>::size) % 16 == 0;
-  if (a.M <= 16) return launch_few<D, 1, 1, 8, 4>(a, wide, s);
-  if (a.M <= 32) return launch_few<D, 2, 1, 8, 4>(a, wide, s);
-  if (a.M <= 64) return launch_few<D, 4, 1, 8, 4>(a, wide, s);
-  const int64_t big = (int64_t)((a.M - 1) / 256 + 1) * ((a.N - 1) / 256 + 1);
-  const int64_t mid = (int64_t)((a.M - 1) / 128 + 1) * ((a.N - 1) / 128 + 1);
-  if (big >= 192) return launch_tile<D, I8Big, 256>(a, wide, s);
-  if (mid >= 256) return launch_tile<D, I8Mid, 128>(a, wide, s);
-  return launch_tile<D, I8Small, 128>(a, wide, s);
+  if (i8_few(a.M)) {
+    hipLaunchKernelGGL((k_int8_rows<D, 8, 4>), dim3((a.N - 1) / 16 + 1), dim3(64 * 8), 0, s, a, wide);
+    return hipGetLastError();
+  }
+  a.k_part = (a.K + SLAB - 1) / SLAB * SLAB;
+  a.partial = nullptr;
+  if (i8_far(a)) return launch_tile<D, DmaCfg<64, 4, 4>, 128, true>(a, 1, wide, s);
+  const I8Plan p = i8_plan(a.M, a.N, a.K);
+  a.k_part = p.k_part;
+  if (p.parts > 1) a.partial = static_cast<int *>(workspace);
+  hipError_t e = hipErrorInvalidValue;
+  switch (p.shape) {
+    case I8_256x256: e = launch_tile<D, DmaCfg<256, 8, 4>, 256>(a, p.parts, wide, s); break;
+    case I8_256x128: e = launch_tile<D, DmaCfg<256, 8, 4>, 128>(a, p.parts, wide, s); break;
+    case I8_128x128: e = launch_tile<D, DmaCfg<128, 4, 4>, 128>(a, p.parts, wide, s); break;
+    case I8_64x128: e = launch_tile<D, DmaCfg<64, 4, 4>, 128>(a, p.parts, wide, s); break;
+  }
+  if (e != hipSuccess || p.parts == 1) return e;
+  const int64_t groups = (int64_t)a.M * ((a.N + 3) / 4);
+  hipLaunchKernelGGL(k_int8_join<D>, dim3((unsigned)std::min<int64_t>((groups + 255) / 256, 1 << 16)), dim3(256), 0, s, a,
+                     p.parts, wide);
+  return hipGetLastError();
 }
 
-hipError_t int8_matmul(const Int8Args &a, hipStream_t s) {
+hipError_t int8_matmul(const Int8Args &a, void *workspace, hipStream_t s) {
   if (a.M <= 0 || a.N <= 0) return hipSuccess;
-  return a.dtype == Dt::BF16 ? matmul_dt<Dt::BF16>(a, s) : matmul_dt<Dt::F32>(a, s);
+  return a.dtype == Dt::BF16 ? matmul_dt<Dt::BF16>(a, workspace, s) : matmul_dt<Dt::F32>(a, workspace, s);
 }
 
 }  // namespace twell

@@ -346,8 +346,11 @@ struct Int8Args {
   const float *bias;     // [M] or null
   void *y;
   int64_t ld_y;
+  int *partial = nullptr;  // set by int8_matmul: integer sums of the K ranges, [ranges][M][N rounded up to 4]
+  int k_part = 0;          // and the ranges' length
 };
-hipError_t int8_matmul(const Int8Args &a, hipStream_t s);
+size_t int8_matmul_workspace(int M, int N, int K);
+hipError_t int8_matmul(const Int8Args &a, void *workspace, hipStream_t s);
 
 // *p = 0 with a one-thread kernel (safe under stream capture).
 hipError_t zero_int(int *p, hipStream_t s);

@@ -495,9 +495,9 @@ twell_status twell_ffn_backward(const twell_hybrid *h, const void *x, const void
  *
  * twell_int8 -- rows of 8-bit integers with one scale each: the value of
  * element (t, j) is q[t * ld + j] * scale[t].  q is 16-byte aligned and ld a
- * multiple of 16; every row has ceil(cols / 16) * 16 READABLE bytes (a buffer
- * of rows * ld bytes does), of which those past cols hold anything: no
- * operator writes them, and they do not reach any result.
+ * multiple of 16; the bytes from q to the last row's (ceil(cols / 16) * 16)th
+ * are READABLE (a buffer of rows * ld bytes is enough).  Those past a row's
+ * cols hold anything: no operator writes them, and they reach no result.
  */
 typedef struct {
   int32_t rows, cols;
@@ -566,11 +566,18 @@ twell_status twell_quantize_rows(const void *x, int64_t ld_x, twell_dtype dtype,
  * [b->rows] in dtype; row_bias: one fp32 value per row of a (the layer's gate
  * bias), or NULL.  a->cols == b->cols, at most 65536.  y may not overlap the
  * inputs.
+ * workspace: >= twell_int8_matmul_workspace_size(a->rows, b->rows, a->cols)
+ * bytes, 256-byte aligned; NULL where that is 0.  Products with too few output
+ * tiles for the GPU cut K into ranges and keep their integer sums there (at
+ * most 64 MB); adding those is exact as well.
  * Errors: INVALID_ARG (NULL pointers, sizes, strides, different cols),
- * UNSUPPORTED (cols, alignment, a stride that is not a multiple of 16), HIP.
+ * UNSUPPORTED (cols, alignment, a stride that is not a multiple of 16),
+ * WORKSPACE, HIP.
  */
+size_t twell_int8_matmul_workspace_size(int M, int N, int K);
 twell_status twell_int8_matmul(const twell_int8 *a, const twell_int8 *b, const float *row_bias,
-                               twell_dtype dtype, void *y, int64_t ld_y, void *stream);
+                               twell_dtype dtype, void *y, int64_t ld_y, void *workspace, size_t ws_bytes,
+                               void *stream);
 
 /*
  * twell_stream_probe -- streaming HBM probe (a measurement aid, not part of

@@ -113,19 +113,32 @@ def test_quantize_validation(kw, status):
     (dict(a=_q(cols=65537, ld=65552), b=_q(cols=65537, ld=65552)), UNSUPPORTED),
     (dict(a=_q(ld=500)), INVALID), (dict(a=_q(ld=514)), UNSUPPORTED), (dict(b=_q(q=FAKE + 4)), UNSUPPORTED),
     (dict(a=_q(scale=None)), INVALID), (dict(ld_y=7), INVALID), (dict(y=FAKE + 1), UNSUPPORTED),
-    (dict(bias=FAKE + 1), UNSUPPORTED),
+    (dict(bias=FAKE + 1), UNSUPPORTED), (dict(ws=FAKE + 16), UNSUPPORTED),
+    (dict(a=_q(rows=64, cols=8192, ld=8192), b=_q(cols=8192, ld=8192), ws=None), WORKSPACE),
+    (dict(a=_q(rows=64, cols=8192, ld=8192), b=_q(cols=8192, ld=8192), ws_bytes=100), WORKSPACE),
 ])
 def test_product_validation(kw, status):
-    a = dict(a=_q(), b=_q(), bias=None, dtype=BF16, y=FAKE, ld_y=8)
+    a = dict(a=_q(), b=_q(), bias=None, dtype=BF16, y=FAKE, ld_y=8, ws=FAKE, ws_bytes=1 << 40)
     a.update(kw)
-    assert L.twell_int8_matmul(_ref(a["a"]), _ref(a["b"]), a["bias"], a["dtype"], a["y"], a["ld_y"], None) == status
+    assert L.twell_int8_matmul(_ref(a["a"]), _ref(a["b"]), a["bias"], a["dtype"], a["y"], a["ld_y"], a["ws"],
+                               a["ws_bytes"], None) == status
     assert twell.twell_last_error() != ""
+
+
+def test_product_workspace():
+    ws = twell.twell_int8_matmul_workspace_size
+    assert ws(1, 8192, 2048) == 0 and ws(8192, 8192, 2048) == 0 and ws(0, 64, 64) == 0
+    assert ws(64, 64, 0) == 0 and ws(64, 64, 70000) == 0 and ws(-1, 64, 64) == 0
+    # few tiles and a long K: whole [M][N] matrices of 4-byte sums
+    for M, N, K in [(64, 2048, 8192), (17, 333, 65536), (256, 2048, 8192), (100, 1, 4096)]:
+        n = ws(M, N, K)
+        assert n > 0 and n % (M * ((N + 3) // 4 * 4) * 4) == 0 and n <= 64 << 20, (M, N, K, n)
 
 
 def test_empty_products_launch_nothing():
     none = _q(rows=0, q=None, scale=None)
-    assert L.twell_int8_matmul(_ref(none), _ref(_q()), None, BF16, None, 8, None) == twell.TWELL_OK
-    assert L.twell_int8_matmul(_ref(_q()), _ref(none), None, BF16, None, 0, None) == twell.TWELL_OK
+    assert L.twell_int8_matmul(_ref(none), _ref(_q()), None, BF16, None, 8, None, 0, None) == twell.TWELL_OK
+    assert L.twell_int8_matmul(_ref(_q()), _ref(none), None, BF16, None, 0, None, 0, None) == twell.TWELL_OK
     assert L.twell_quantize_rows(None, 512, BF16, _ref(none), None) == twell.TWELL_OK
 
 

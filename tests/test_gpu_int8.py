@@ -58,13 +58,14 @@ def _check(y, a, sa, b, sb, bias, dtype):
 
 
 # M, N, K: single elements; below, at and above every tile edge; K inside,
-# at and just past 16-byte chunks and 64- and 128-byte slabs; few rows with many columns and
-# the other way round
+# at and just past 16-byte chunks and 64-byte slabs; few rows with many columns
+# and the other way round; few tiles with a long K (cut into ranges)
 SHAPES = [(1, 1, 1), (1, 5, 3), (2, 16, 16), (1, 64, 64), (1, 1000, 777), (3, 257, 100), (7, 96, 2048), (16, 16, 64),
           (17, 33, 65), (31, 100, 127), (32, 128, 128), (33, 130, 129), (64, 64, 192), (65, 63, 256), (100, 300, 320),
           (127, 129, 383), (128, 128, 512), (129, 257, 640), (200, 1, 300), (255, 256, 63), (256, 256, 1024),
           (257, 511, 1031), (300, 700, 48), (333, 1000, 777), (513, 515, 400), (1, 2048, 8192), (8, 8192, 512),
-          (48, 512, 4096), (700, 520, 2000), (1500, 300, 144), (1024, 1024, 1024)]
+          (48, 512, 4096), (64, 2048, 8192), (32, 300, 16384), (17, 131, 5003), (100, 1, 4096),
+          (300, 260, 20000), (129, 1000, 7777), (700, 520, 2000), (1500, 300, 144), (1024, 1024, 1024)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -163,6 +164,23 @@ def test_output_beyond_32_bit_offsets():
     y = buf.as_strided((M, N), (ld, 1))
     tw.twell_int8_matmul(_dev(a), _vec(np.ones(M)), _dev(b), _vec(np.ones(N)), y=y)
     _check(y, a, np.ones(M, np.float32), b, np.ones(N, np.float32), None, "bf16")
+
+
+def test_cut_products_repeat_and_take_a_workspace():
+    # K cut into ranges: the same bits again, over a workspace of any contents
+    import torch
+    M, N, K = 64, 515, 8200
+    a, b = _int8(M, K, 17), _int8(N, K, 18)
+    sa, sb = np.full(M, 0.5, np.float32), np.full(N, 0.125, np.float32)
+    n = tw.twell_int8_matmul_workspace_size(M, N, K)
+    assert n > 0
+    args = (_dev(a), _vec(sa), _dev(b), _vec(sb))
+    ws = torch.full((n + 256,), 85, dtype=torch.uint8, device="cuda:0")
+    y = tw.twell_int8_matmul(*args, dtype=torch.float32, workspace=ws)
+    assert bool((ws[n:] == 85).all())
+    _check(y, a, sa, b, sb, None, "f32")
+    again = tw.twell_int8_matmul(*args, dtype=torch.float32)
+    assert_bitwise(again.cpu().numpy(), y.cpu().numpy(), "y of a second run")
 
 
 def test_empty_and_another_stream():
