@@ -767,6 +767,7 @@ def twell_rmsnorm(x, weight, eps: float = 1e-6, residual=None, quantize: bool = 
     return RmsNormOut(y, x if h is None else h, q, scale)
 
 
+@functools.lru_cache(maxsize=4096)
 def twell_rmsnorm_backward_workspace_size(rows: int, d: int, dtype) -> int:
     return int(_lib.twell_rmsnorm_backward_workspace_size(rows, d, _dtype_code(dtype)))
 
@@ -796,7 +797,7 @@ def twell_rmsnorm_backward(dy, h, weight, eps: float = 1e-6, dh=None, dx=None, d
         dweight = h.new_empty((d,), dtype=_FLOAT32)
     else:
         _vec(dweight, "dweight", device, _FLOAT32, d)
-    ws = _workspace(_lib.twell_rmsnorm_backward_workspace_size(rows, d, code), device, workspace)
+    ws = _workspace(twell_rmsnorm_backward_workspace_size(rows, d, dtype), device, workspace)
     st = _lib.twell_rmsnorm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, wp, sp, ld_dh, eps, rows, d, code,
                                      dx.data_ptr(), ld_dx, dweight.data_ptr(), ws.data_ptr(), ws.numel(),
                                      _raw_stream(device))

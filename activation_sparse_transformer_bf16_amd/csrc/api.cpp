@@ -921,7 +921,7 @@ twell_status twell_quantize_rows(const void *x, int64_t ld_x, twell_dtype dtype,
 }
 
 size_t twell_int8_matmul_workspace_size(int M, int N, int K) {
-  return M < 0 || N < 0 || K <= 0 || K > INT8_MAX_K ? 0 : int8_matmul_workspace(M, N, K);
+  return M < 0 || N < 0 || M > INT8_MAX_ROWS || N > INT8_MAX_ROWS || K <= 0 || K > INT8_MAX_K ? 0 : int8_matmul_workspace(M, N, K);
 }
 
 twell_status twell_int8_matmul(const twell_int8 *a, const twell_int8 *b, const float *row_bias, twell_dtype dtype,
@@ -934,6 +934,8 @@ twell_status twell_int8_matmul(const twell_int8 *a, const twell_int8 *b, const f
   if (a->cols != b->cols) return fail(TWELL_ERR_INVALID_ARG, "a has %d columns, b %d", a->cols, b->cols);
   if (a->cols > INT8_MAX_K)
     return fail(TWELL_ERR_UNSUPPORTED, "%d columns not built (at most %d)", a->cols, INT8_MAX_K);
+  if (a->rows > INT8_MAX_ROWS || b->rows > INT8_MAX_ROWS)
+    return fail(TWELL_ERR_UNSUPPORTED, "%d x %d results not built (at most %d each way)", a->rows, b->rows, INT8_MAX_ROWS);
   if ((st = check_rows("y", y, ld_y, b->rows, dt_size(dtype), a->rows > 0 && b->rows > 0)) != TWELL_OK) return st;
   if (!aligned(row_bias, 4)) return fail(TWELL_ERR_UNSUPPORTED, "misaligned row_bias");
   if (a->rows == 0 || b->rows == 0) return TWELL_OK;

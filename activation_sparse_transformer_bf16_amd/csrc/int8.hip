@@ -183,13 +183,13 @@ __device__ __forceinline__ int i8_col(int j, int rho) {
 
 // 16 bytes of y per lane; a run that is not whole (past N, or rows that are
 // not 16-byte aligned) goes element by element.
-template <Dt D>
-__device__ __forceinline__ void store_run(void *row, int n, int N, u32x4_t v, bool wide, bool stream) {
+template <Dt D, bool STREAM>
+__device__ __forceinline__ void store_run(void *row, int n, int N, u32x4_t v, bool wide) {
   using T = typename DtT<D>::T;
   constexpr int E = 16 / DtT<D>::size;
   T *p = static_cast<T *>(row) + n;
   if (wide && n + E <= N) {
-    if (stream)
+    if constexpr (STREAM)
       __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t *>(p));
     else
       *reinterpret_cast<u32x4_t *>(p) = v;
@@ -226,9 +226,10 @@ struct I8Tile {
 // of H.  Registers hold the b fragments, and both halves of a: while the lower
 // half is multiplied the upper one is read, and while the upper half is
 // multiplied the next slab's lower half, each b fragment after its last use.
-template <Dt D, class Cfg, int BN, bool FAR>
-__global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile(Int8Args a, bool wide,
-                                                                                     bool stream, int tiles) {
+// STREAM: the results are stored non-temporally (a template, as the compiler
+// joins the two kinds of store into the ordinary one under a run-time choice).
+template <Dt D, class Cfg, int BN, bool FAR, bool STREAM>
+__global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile(Int8Args a, bool wide, int tiles) {
   using T = typename DtT<D>::T;
   using WT = WaveTile<BN, Cfg>;
   using L = I8Tile<Cfg, BN>;
@@ -422,7 +423,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile
       const int r = p * (64 / PER_ROW) + lane / PER_ROW, c = lane % PER_ROW;
       const int m = m0 + row + r, n = n0 + col0 + c * (16 / S);
       const u32x4_t w = *reinterpret_cast<const u32x4_t *>(mine + r * PITCH + c * 16);
-      if (m < a.M && n < a.N) store_run<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, w, wide, stream);
+      if (m < a.M && n < a.N) store_run<D, STREAM>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, w, wide);
     }
     wave_sync();
   }
@@ -557,21 +558,25 @@ size_t int8_matmul_workspace(int M, int N, int K) {
   return M <= 0 || N <= 0 || i8_few(M) ? 0 : i8_plan(M, N, K).bytes;
 }
 
-template <Dt D, class Cfg, int BN, bool FAR = false>
+template <Dt D, class Cfg, int BN, bool FAR = false, bool STREAM = false>
 static hipError_t launch_tile(const Int8Args &a, int parts, bool wide, hipStream_t s) {
-  auto kern = k_int8_tile<D, Cfg, BN, FAR>;
+  auto kern = k_int8_tile<D, Cfg, BN, FAR, STREAM>;
   constexpr int lds = I8Tile<Cfg, BN>::LDS;
   hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   const int64_t tiles = (int64_t)((a.M - 1) / Cfg::BM + 1) * ((a.N - 1) / BN + 1);
-  if (tiles * parts > (1 << 22)) return hipErrorInvalidValue;
-  // Results beyond the Infinity Cache are stored non-temporally, so that they
-  // do not take cache lines from the operands of the tiles still to come (470
-  // MB, 16384 x 14336 x 4096: 765 against 802 us); smaller ones stay there for
-  // their reader (134 MB, 8192 x 8192 x 2048: 127 against 129 us).
-  const bool stream = (size_t)a.M * a.N * DtT<D>::size > ((size_t)256 << 20);
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * parts)), dim3(Cfg::THREADS), lds, s, a, wide, stream, (int)tiles);
+  if (tiles * parts > (int64_t)UINT32_MAX / Cfg::THREADS) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * parts)), dim3(Cfg::THREADS), lds, s, a, wide, (int)tiles);
   return hipGetLastError();
+}
+
+// Results beyond the Infinity Cache are stored non-temporally, so that they do
+// not take cache lines from the operands of the tiles still to come (470 MB,
+// 16384 x 14336 x 4096: 765 against 802 us); smaller ones stay there for their
+// reader (134 MB, 8192 x 8192 x 2048: 127 against 129 us).
+template <Dt D>
+static bool i8_stream(const Int8Args &a) {
+  return (size_t)a.M * a.N * DtT<D>::size > ((size_t)256 << 20);
 }
 
 template <Dt D>
@@ -590,7 +595,10 @@ static hipError_t matmul_dt(const Int8Args &args, void *workspace, hipStream_t s
   if (p.parts > 1) a.partial = static_cast<int *>(workspace);
   hipError_t e = hipErrorInvalidValue;
   switch (p.shape) {
-    case I8_256x256: e = launch_tile<D, DmaCfg<256, 8, 4>, 256>(a, p.parts, wide, s); break;
+    case I8_256x256:
+      e = i8_stream<D>(a) ? launch_tile<D, DmaCfg<256, 8, 4>, 256, false, true>(a, p.parts, wide, s)
+                          : launch_tile<D, DmaCfg<256, 8, 4>, 256>(a, p.parts, wide, s);
+      break;
     case I8_256x128: e = launch_tile<D, DmaCfg<256, 8, 4>, 128>(a, p.parts, wide, s); break;
     case I8_128x128: e = launch_tile<D, DmaCfg<128, 4, 4>, 128>(a, p.parts, wide, s); break;
     case I8_64x128: e = launch_tile<D, DmaCfg<64, 4, 4>, 128>(a, p.parts, wide, s); break;

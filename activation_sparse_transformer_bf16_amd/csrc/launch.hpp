@@ -334,6 +334,7 @@ hipError_t norm_backward(const NormBackwardArgs &a, hipStream_t s);
 // Product of 8-bit rows (int8.hip): a [M][K], b [N][K], rows 16-byte aligned
 // with ceil(K / 16) * 16 readable bytes each; y [M][N] with row stride ld_y.
 constexpr int INT8_MAX_K = 65536;
+constexpr int INT8_MAX_ROWS = 1 << 26;  // of a and of b
 struct Int8Args {
   Dt dtype;              // of y
   int M, N, K;

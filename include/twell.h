@@ -564,8 +564,8 @@ twell_status twell_quantize_rows(const void *x, int64_t ld_x, twell_dtype dtype,
  *     y_mn = round((sum_k a_mk b_nk) * a->scale_m * b->scale_n + row_bias_m)
  * on the matrix cores, the sums in 32-bit integers (exact).  y [a->rows]
  * [b->rows] in dtype; row_bias: one fp32 value per row of a (the layer's gate
- * bias), or NULL.  a->cols == b->cols, at most 65536.  y may not overlap the
- * inputs.
+ * bias), or NULL.  a->cols == b->cols, at most 65536; at most 2^26 rows each.
+ * y may not overlap the inputs.
  * workspace: >= twell_int8_matmul_workspace_size(a->rows, b->rows, a->cols)
  * bytes, 256-byte aligned; NULL where that is 0.  Products with too few output
  * tiles for the GPU cut K into ranges and keep their integer sums there (at

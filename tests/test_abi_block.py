@@ -113,6 +113,7 @@ def test_quantize_validation(kw, status):
     (dict(a=_q(cols=65537, ld=65552), b=_q(cols=65537, ld=65552)), UNSUPPORTED),
     (dict(a=_q(ld=500)), INVALID), (dict(a=_q(ld=514)), UNSUPPORTED), (dict(b=_q(q=FAKE + 4)), UNSUPPORTED),
     (dict(a=_q(scale=None)), INVALID), (dict(ld_y=7), INVALID), (dict(y=FAKE + 1), UNSUPPORTED),
+    (dict(a=_q(rows=(1 << 26) + 1)), UNSUPPORTED), (dict(b=_q(rows=(1 << 26) + 1), ld_y=1 << 27), UNSUPPORTED),
     (dict(bias=FAKE + 1), UNSUPPORTED), (dict(ws=FAKE + 16), UNSUPPORTED),
     (dict(a=_q(rows=64, cols=8192, ld=8192), b=_q(cols=8192, ld=8192), ws=None), WORKSPACE),
     (dict(a=_q(rows=64, cols=8192, ld=8192), b=_q(cols=8192, ld=8192), ws_bytes=100), WORKSPACE),
