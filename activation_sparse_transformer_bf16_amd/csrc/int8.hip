@@ -429,20 +429,30 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile
   }
 }
 
-// The ranges' sums added, scaled and written: 4 columns per thread.
+// The ranges' sums added, scaled and written: 4 columns per thread, a row per
+// blockIdx.y; four ranges' loads in flight at a time.
 template <Dt D>
 __global__ __launch_bounds__(256) void k_int8_join(Int8Args a, int parts, bool wide) {
   using T = typename DtT<D>::T;
   const int n_pad = (a.N + 3) / 4 * 4;
-  const int64_t total = (int64_t)a.M * n_pad / 4;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int m = (int)(i / (n_pad / 4)), n = (int)(i % (n_pad / 4)) * 4;
-    const float sa = a.a_scale[m], bias = a.bias ? a.bias[m] : 0.0f;
-    float sb[4];
+  const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (n >= a.N) return;
+  float sb[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) sb[q] = a.b_scale[min(n + q, a.N - 1)];
+  for (int q = 0; q < 4; ++q) sb[q] = a.b_scale[min(n + q, a.N - 1)];
+  for (int m = blockIdx.y; m < a.M; m += gridDim.y) {
+    const float sa = a.a_scale[m], bias = a.bias ? a.bias[m] : 0.0f;
+    const int *src = a.partial + (int64_t)m * n_pad + n;
     i32x4_t s = {0, 0, 0, 0};
-    for (int p = 0; p < parts; ++p) s += *reinterpret_cast<const i32x4_t *>(a.partial + p * total * 4 + i * 4);
+    for (int p = 0; p < parts; p += 4) {
+      i32x4_t v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = *reinterpret_cast<const i32x4_t *>(src + (int64_t)min(p + k, parts - 1) * a.M * n_pad);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (p + k < parts) s += v[k];
+    }
     store4<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, s, sa, sb, bias, wide);
   }
 }
@@ -500,13 +510,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_int8_rows(Int8Args a, bool wide)
 // tile on a CU, in units of 10 ns (measured over K = 2048 and 8192 with the
 // chip full; the smaller ones are bound by the loads a CU can have in flight,
 // the largest by the power of the matrix cores).
-enum I8Shape { I8_256x256, I8_256x128, I8_128x128, I8_64x128, I8_SHAPES };
+enum I8Shape { I8_ROWS = -1, I8_256x256, I8_256x128, I8_128x128, I8_64x128, I8_SHAPES };
 struct I8ShapeCost {
   int bm, bn, slab;
 };
 constexpr I8ShapeCost I8_COST[I8_SHAPES] = {{256, 256, 80}, {256, 128, 53}, {128, 128, 30}, {64, 128, 19}};
 constexpr int I8_TILE_COST = 250;   // of a tile besides its slabs: start, ring fill, results
 constexpr int I8_JOIN_COST = 250;   // of the second launch
+constexpr int I8_ROWS_COST = 150;   // of k_int8_rows besides its bytes
 constexpr int I8_MAX_PARTS = 16;
 constexpr size_t I8_MAX_PARTIAL = (size_t)64 << 20;
 
@@ -526,6 +537,16 @@ static I8Plan i8_plan(int M, int N, int K) {
   const int nk = (K + SLAB - 1) / SLAB;
   I8Plan best{I8_256x256, 1, nk * SLAB, 0};
   int64_t least = INT64_MAX;
+  // the operands' bytes at 5 TB/s
+  const int64_t bytes = ((int64_t)M + N) * K / 50000;
+  // At most 16 rows: k_int8_rows, bound by the columns' bytes at 4.9 TB/s for
+  // one row and 3.4 for 16 (every workgroup reads all rows), or by the 16
+  // columns of one workgroup at 32 to 22 GB/s.  One row of 4096 x 14336: 10.6
+  // us, 13.2 from tiles; 16 rows of 14336 x 4096: 18.2 us, 14.3 from tiles.
+  if (M <= 16) {
+    best.shape = I8_ROWS;
+    least = I8_ROWS_COST + std::max((int64_t)N * K / (50000 - 1000 * M), (int64_t)K * (32 + M) / 660);
+  }
   for (int shape = 0; shape < I8_SHAPES; ++shape) {
     const int64_t tiles = i8_tiles(shape, M, N);
     for (int want = 1; want <= I8_MAX_PARTS; want *= 2) {
@@ -533,7 +554,7 @@ static I8Plan i8_plan(int M, int N, int K) {
       const size_t sums = (size_t)parts * M * ((N + 3) / 4 * 4);
       if (want > 1 && (parts < want || per < 4 || sums * 4 > I8_MAX_PARTIAL)) break;
       const int64_t rounds = (tiles * parts + 255) / 256;
-      const int64_t cost = rounds * (per * I8_COST[shape].slab + I8_TILE_COST) +
+      const int64_t cost = std::max(rounds * (per * I8_COST[shape].slab + I8_TILE_COST), bytes + I8_TILE_COST) +
                            (parts > 1 ? I8_JOIN_COST + (int64_t)(sums / 5000) : 0);
       if (cost < least) {
         least = cost;
@@ -550,12 +571,8 @@ static bool i8_far(const Int8Args &a) {
   return std::max(a.ld_a, a.ld_b) > ((int64_t)1 << 31) / 256 - INT8_MAX_K;
 }
 
-// At most 16 rows: one block of rows, and the matrix instruction's shape leaves
-// nothing to share.  5.4 us for one token of 8192 x 2048, 8 us from tiles.
-static bool i8_few(int M) { return M <= 16; }
-
 size_t int8_matmul_workspace(int M, int N, int K) {
-  return M <= 0 || N <= 0 || i8_few(M) ? 0 : i8_plan(M, N, K).bytes;
+  return M <= 0 || N <= 0 ? 0 : i8_plan(M, N, K).bytes;
 }
 
 template <Dt D, class Cfg, int BN, bool FAR = false, bool STREAM = false>
@@ -583,14 +600,14 @@ template <Dt D>
 static hipError_t matmul_dt(const Int8Args &args, void *workspace, hipStream_t s) {
   Int8Args a = args;
   const bool wide = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && (a.ld_y * DtT<D>::size) % 16 == 0;
-  if (i8_few(a.M)) {
+  const I8Plan p = i8_plan(a.M, a.N, a.K);
+  if (p.shape == I8_ROWS || (a.M <= 16 && i8_far(a))) {
     hipLaunchKernelGGL((k_int8_rows<D, 8, 4>), dim3((a.N - 1) / 16 + 1), dim3(64 * 8), 0, s, a, wide);
     return hipGetLastError();
   }
   a.k_part = (a.K + SLAB - 1) / SLAB * SLAB;
   a.partial = nullptr;
   if (i8_far(a)) return launch_tile<D, DmaCfg<64, 4, 4>, 128, true>(a, 1, wide, s);
-  const I8Plan p = i8_plan(a.M, a.N, a.K);
   a.k_part = p.k_part;
   if (p.parts > 1) a.partial = static_cast<int *>(workspace);
   hipError_t e = hipErrorInvalidValue;
@@ -604,9 +621,8 @@ static hipError_t matmul_dt(const Int8Args &args, void *workspace, hipStream_t s
     case I8_64x128: e = launch_tile<D, DmaCfg<64, 4, 4>, 128>(a, p.parts, wide, s); break;
   }
   if (e != hipSuccess || p.parts == 1) return e;
-  const int64_t groups = (int64_t)a.M * ((a.N + 3) / 4);
-  hipLaunchKernelGGL(k_int8_join<D>, dim3((unsigned)std::min<int64_t>((groups + 255) / 256, 1 << 16)), dim3(256), 0, s, a,
-                     p.parts, wide);
+  const dim3 grid((unsigned)((a.N - 1) / 1024 + 1), (unsigned)std::min(a.M, 1 << 15));
+  hipLaunchKernelGGL(k_int8_join<D>, grid, dim3(256), 0, s, a, p.parts, wide);
   return hipGetLastError();
 }
 

@@ -462,15 +462,20 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
   }
 }
 
-// dw_j = the partial rows added in a fixed order: 16 columns per workgroup, 64
-// groups of consecutive rows, then the groups in order.
-constexpr int DW_COLS = 16, DW_GROUPS = 64;
-static_assert(NORM_BACKWARD_WGS % DW_GROUPS == 0, "whole loads per group");
-__global__ __launch_bounds__(DW_COLS *DW_GROUPS) void k_norm_dweight(const float *__restrict__ partial, int n, int d,
-                                                                     float *__restrict__ dweight) {
-  constexpr int PER = NORM_BACKWARD_WGS / DW_GROUPS;
-  __shared__ float sum[DW_GROUPS][DW_COLS + 1];
-  const int col = threadIdx.x % DW_COLS, grp = threadIdx.x / DW_COLS;
+// dw_j = the partial rows added in a fixed order: 16 columns per workgroup; a
+// thread adds PER consecutive rows, a wave its four threads of a column, and
+// the first wave the 16 waves' sums.
+constexpr int DW_COLS = 16, DW_WAVES = 16;
+static_assert(NORM_BACKWARD_WGS % (4 * DW_WAVES) == 0, "whole rows per thread");
+__device__ __forceinline__ float column_sum(float s) {
+  s += __shfl_xor(s, 16, 64);
+  return s + __shfl_xor(s, 32, 64);
+}
+__global__ __launch_bounds__(64 * DW_WAVES) void k_norm_dweight(const float *__restrict__ partial, int n, int d,
+                                                                float *__restrict__ dweight) {
+  constexpr int PER = NORM_BACKWARD_WGS / (4 * DW_WAVES);
+  __shared__ float sum[DW_WAVES][DW_COLS];
+  const int col = threadIdx.x % DW_COLS, grp = threadIdx.x / DW_COLS, wave = threadIdx.x >> 6;
   const int j = blockIdx.x * DW_COLS + col;
   float v[PER];
 #pragma unroll
@@ -481,14 +486,15 @@ __global__ __launch_bounds__(DW_COLS *DW_GROUPS) void k_norm_dweight(const float
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) s += v[i];
-  sum[grp][col] = s;
+  s = column_sum(s);
+  if (grp % 4 == 0) sum[wave][col] = s;
   __syncthreads();
-  if (threadIdx.x < DW_COLS && j < d) {
-    float t = 0.0f;
+  if (wave != 0) return;
+  s = 0.0f;
 #pragma unroll
-    for (int g = 0; g < DW_GROUPS; ++g) t += sum[g][col];
-    dweight[j] = t;
-  }
+  for (int i = 0; i < 4; ++i) s += sum[4 * grp + i][col];
+  s = column_sum(s);
+  if (grp == 0 && j < d) dweight[j] = s;
 }
 
 // ---- launchers ----------------------------------------------------------------
@@ -575,7 +581,7 @@ hipError_t norm_backward(const NormBackwardArgs &args, hipStream_t s) {
   if (a.n_partial == 1) a.partial = a.dweight;
   hipError_t e = a.dtype == Dt::BF16 ? backward_dt<Dt::BF16>(a, s) : backward_dt<Dt::F32>(a, s);
   if (e != hipSuccess || a.n_partial == 1) return e;
-  hipLaunchKernelGGL(k_norm_dweight, dim3((a.d + DW_COLS - 1) / DW_COLS), dim3(DW_COLS * DW_GROUPS), 0, s, a.partial,
+  hipLaunchKernelGGL(k_norm_dweight, dim3((a.d + DW_COLS - 1) / DW_COLS), dim3(64 * DW_WAVES), 0, s, a.partial,
                      a.n_partial, a.d, a.dweight);
   return hipGetLastError();
 }
