@@ -225,7 +225,20 @@ struct I8Tile {
 // 64 columns (4 b fragments) and 2 H 16-row blocks of a, taken in two halves
 // of H.  Registers hold the b fragments, and both halves of a: while the lower
 // half is multiplied the upper one is read, and while the upper half is
-// multiplied the next slab's lower half, each b fragment after its last use.
+// multiplied the next slab's lower half, each b fragment after its last use;
+// the copies for the slab STAGES ahead go out between the products.
+//
+// Measured (256 x 256 tiles, Gaussian operands, back to back): 8192 x 8192 x
+// 2048 127-131 us, 2.1 POP/s; 8192^3 413 us, 2.66 POP/s; 16384 x 14336 x 4096
+// 762 us, 2.5 POP/s, against 2.0 POP/s of the library's 8-bit product at
+// 8192^3 and 5 POP/s of the specification.  The power of the chip bounds it:
+// operands of zeros take 103, 315 and 597 us.  By parts, at 8192^3 with random
+// operands and 32 x 32 x 32 products: registers only 3.4 POP/s, with the
+// fragment reads 3.0, with the copies into LDS 2.4; the 16 x 16 x 64 form then
+// gained 10%.  The results' stores cost the rest (8192 x 8192 x 2048: 110 us
+// without them); a persistent workgroup that starts the next tile's copies
+// before them gains nothing, nor do 128 x 128 wave tiles on four waves
+// (accumulators in AGPRs, 583 us at 8192^3).
 // STREAM: the results are stored non-temporally (a template, as the compiler
 // joins the two kinds of store into the ordinary one under a run-time choice).
 template <Dt D, class Cfg, int BN, bool FAR, bool STREAM>
@@ -460,7 +473,10 @@ __global__ __launch_bounds__(256) void k_int8_join(Int8Args a, int parts, bool w
 // ---- few rows -------------------------------------------------------------------
 
 // 16 rows of a and 16 columns; WAVES waves take runs of 64 * U bytes of K in
-// turn, and add their sums through LDS.
+// turn, and add their sums through LDS.  Bound by the latency and rate of the
+// columns' loads: one row of 8192 x 2048 5.0 us (3.4 TB/s), of 14336 x 14336 39
+// us (5.2 TB/s).  4 or 16 waves, U = 2 or 8, a second run loaded ahead and
+// non-temporal loads: within 3% there, up to 30% slower at 4096 x 14336.
 template <Dt D, int WAVES, int U>
 __global__ __launch_bounds__(64 * WAVES) void k_int8_rows(Int8Args a, bool wide) {
   using T = typename DtT<D>::T;
@@ -509,7 +525,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_int8_rows(Int8Args a, bool wide)
 // The tile shapes: rows, columns, and the time of one 64-byte slab of K per
 // tile on a CU, in units of 10 ns (measured over K = 2048 and 8192 with the
 // chip full; the smaller ones are bound by the loads a CU can have in flight,
-// the largest by the power of the matrix cores).
+// the largest by the power of the matrix cores).  64 x 2048 x 8192: 25 us in 64
+// x 128 tiles, 11.4 in 8 ranges of K; 1024 x 8192 x 2048: 28 us in 256 x 256
+// tiles, 21.6 in 256 x 128; 2048 x 2048 x 8192: 52 us in 256 x 128, 40 in 128 x 128.
 enum I8Shape { I8_ROWS = -1, I8_256x256, I8_256x128, I8_128x128, I8_64x128, I8_SHAPES };
 struct I8ShapeCost {
   int bm, bn, slab;
@@ -587,10 +605,10 @@ static hipError_t launch_tile(const Int8Args &a, int parts, bool wide, hipStream
   return hipGetLastError();
 }
 
-// Results beyond the Infinity Cache are stored non-temporally, so that they do
-// not take cache lines from the operands of the tiles still to come (470 MB,
-// 16384 x 14336 x 4096: 765 against 802 us); smaller ones stay there for their
-// reader (134 MB, 8192 x 8192 x 2048: 127 against 129 us).
+// Results beyond the Infinity Cache (256 MB) are stored non-temporally, so that
+// they do not take cache lines from the operands of the tiles still to come
+// (470 MB, 16384 x 14336 x 4096: 762 against 792 us); smaller ones, where it
+// makes no difference (134 to 235 MB, within 1%), stay there for their reader.
 template <Dt D>
 static bool i8_stream(const Int8Args &a) {
   return (size_t)a.M * a.N * DtT<D>::size > ((size_t)256 << 20);

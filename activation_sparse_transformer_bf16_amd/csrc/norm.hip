@@ -208,6 +208,10 @@ constexpr int row_waves(int W) { return W > 4 ? W : 4; }
 // x, residual, weight -> h, y, q + scale (each output optional).  NORM false:
 // the plain quantiser (h = x, no weight, r = 1).  With eight chunks per lane
 // the weight is loaded again where it is used instead of being held.
+//
+// Memory bound: bf16 8192 x 2048 with residual and 8 bits 23.5 us (151 MB, 6.4
+// TB/s; a plain copy of the card moves 6.1-6.3), the quantiser of 8192 x 8192
+// 32.5 us (201 MB, 6.2 TB/s); one row 2.3 us, launch and one round trip.
 template <Dt D, int W, int NC, bool AL, bool NORM>
 __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
   constexpr int E = 16 / DtT<D>::size;
@@ -316,6 +320,11 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
 // row where it does not; with eight chunks per lane the registers hold no sums
 // either: the workgroup, which then takes one row at a time, adds each row to
 // its partial row in memory (every element by the one lane that owns it).
+//
+// bf16 8192 x 2048 with dh: 24.7 us (134 MB, 5.4 TB/s) and 4 us for the sums;
+// 16384 x 4096 89 us (6.0 TB/s).  Two waves a row and two chunks a lane leave
+// room to load the next row ahead (1 us); one wave with four chunks spills
+// (40 us), 512 workgroups write twice the partial rows (28 us).
 constexpr int BACK_WAVES = 16;
 template <Dt D, int W, int NC, bool AL>
 __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardArgs a) {
