@@ -8,18 +8,17 @@
 // contiguous bytes per lane, and any assignment of K to lanes is right as long
 // as a and b share it.
 //
-// K need not fill the last slab: chunks past a row's last readable chunk are
-// loaded from that chunk again, and the a side is zeroed past K, so what the b
-// rows hold there does not count.  Rows past M and N repeat the last row and
-// are not stored.
+// K need not fill the last slab: nothing behind a row's last readable chunk
+// counts, as the a side is zeroed past K.  Nothing outside the operands is
+// read, and results past M and N are not stored.
 //
 // Three kernels:
 //  * k_int8_tile: tiles of BM x BN outputs, operands through a ring of LDS
 //    stages (the direct-to-LDS loads of gemm.hpp); where the tiles are too few
 //    for the chip, K is cut into ranges whose integer sums go to the workspace,
 //  * k_int8_join, which adds them and writes the results.
-//  * k_int8_rows: at most 16 rows of a (decoding): 16 columns per workgroup,
-//    the waves split K, operands straight into registers.
+//  * k_int8_small: products too small to fill the chip with such tiles: 16 to
+//    64 rows and columns per workgroup, whose waves split K.
 #include "gemm.hpp"
 #include "launch.hpp"
 
@@ -108,56 +107,38 @@ __device__ __forceinline__ int i8_swizzle(int row) {
 // tile's first row and ends with the last chunk of its last row, so that
 // nothing outside the operand is read: lanes past its end load nothing.  Its
 // lane offsets are 32-bit, enough while the tile's rows span less than 2^31
-// bytes; FAR keeps a 64-bit address per lane instead, and repeats the last row
-// and the last chunk where there are no more.
-template <int NR, int WAVES, int SWZ, bool FAR>
+// bytes (i8_far).
+template <int NR, int WAVES, int SWZ>
 struct I8Rows {
   static constexpr int PER_WAVE = NR / 16 / WAVES;
   static_assert(PER_WAVE >= 1 && NR % (16 * WAVES) == 0, "whole 1 KB blocks per wave");
   uint64_t start;  // of the present slab
   uint32_t left;   // bytes from there to the end
-  const int8_t *ptr[FAR ? PER_WAVE : 1];
-  uint32_t off[PER_WAVE], lds[PER_WAVE], last;
+  uint32_t off[PER_WAVE], lds[PER_WAVE];
 
   __device__ __forceinline__ void init(int wave, int lane, int region, const int8_t *base, int64_t ld, int r0,
                                        int rows, int K) {
-    last = (uint32_t)(K - 1) / 16 * 16;
     const int n = min(NR, rows - r0);
     start = (uint64_t)(uintptr_t)(base + (int64_t)r0 * ld);
-    left = (uint32_t)(n - 1) * (uint32_t)ld + last + 16u;
+    left = (uint32_t)(n - 1) * (uint32_t)ld + (uint32_t)((K + 15) / 16 * 16);
 #pragma unroll
     for (int j = 0; j < PER_WAVE; ++j) {
       const int blk = wave * PER_WAVE + j;
       const int row = blk * 16 + (lane >> 2);
-      const uint32_t c = (uint32_t)((lane & 3) ^ i8_swizzle<SWZ>(row)) * 16;
       lds[j] = region + blk * 1024;
-      if constexpr (FAR) {
-        ptr[j] = base + (int64_t)min(r0 + row, rows - 1) * ld;
-        off[j] = c;
-      } else {
-        off[j] = (uint32_t)row * (uint32_t)ld + c;
-      }
+      off[j] = (uint32_t)row * (uint32_t)ld + (uint32_t)((lane & 3) ^ i8_swizzle<SWZ>(row)) * 16;
     }
   }
   // copy j of the present slab into its stage
   __device__ __forceinline__ void issue(int j, uint32_t stage) {
-    if constexpr (FAR) {
-      copy16(ptr[j] + min(off[j], last), __builtin_amdgcn_readfirstlane((int)(stage + lds[j])));
-    } else {
-      const u32x4_t rsrc = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)start),
-                            (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(start >> 32) & 0xFFFFu)),
-                            (uint32_t)__builtin_amdgcn_readfirstlane((int)left), 0x00020000u};
-      copy16_buffer(rsrc, off[j], __builtin_amdgcn_readfirstlane((int)(stage + lds[j])));
-    }
+    const u32x4_t rsrc = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)start),
+                          (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(start >> 32) & 0xFFFFu)),
+                          (uint32_t)__builtin_amdgcn_readfirstlane((int)left), 0x00020000u};
+    copy16_buffer(rsrc, off[j], __builtin_amdgcn_readfirstlane((int)(stage + lds[j])));
   }
   __device__ __forceinline__ void advance() {
-    if constexpr (FAR) {
-#pragma unroll
-      for (int j = 0; j < PER_WAVE; ++j) off[j] += SLAB;
-    } else {
-      start += SLAB;
-      left -= SLAB;
-    }
+    start += SLAB;
+    left -= SLAB;
   }
   __device__ __forceinline__ void issue_all(uint32_t stage) {
 #pragma unroll
@@ -241,7 +222,7 @@ struct I8Tile {
 // (accumulators in AGPRs, 583 us at 8192^3).
 // STREAM: the results are stored non-temporally (a template, as the compiler
 // joins the two kinds of store into the ordinary one under a run-time choice).
-template <Dt D, class Cfg, int BN, bool FAR, bool STREAM>
+template <Dt D, class Cfg, int BN, bool STREAM>
 __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile(Int8Args a, bool wide, int tiles) {
   using T = typename DtT<D>::T;
   using WT = WaveTile<BN, Cfg>;
@@ -250,8 +231,8 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile
   constexpr int H = WT::NWM, NB = 4;
   constexpr int STAGE = (BM + BN) * SLAB;
   constexpr int SB = D == Dt::BF16 ? 3 : 2;  // b's swizzle: the rows of a fragment are 8 (4) apart in groups of 4
-  using RowsA = I8Rows<BM, WAVES, 2, FAR>;
-  using RowsB = I8Rows<BN, WAVES, SB, FAR>;
+  using RowsA = I8Rows<BM, WAVES, 2>;
+  using RowsB = I8Rows<BN, WAVES, SB>;
   constexpr int OPS = RowsA::PER_WAVE + RowsB::PER_WAVE;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int lane = threadIdx.x & 63;
@@ -470,121 +451,222 @@ __global__ __launch_bounds__(256) void k_int8_join(Int8Args a, int parts, bool w
   }
 }
 
-// ---- few rows -------------------------------------------------------------------
+// ---- small products ----------------------------------------------------------------
 
-// 16 rows of a and 16 columns; WAVES waves take runs of 64 * U bytes of K in
-// turn, and add their sums through LDS.  Bound by the latency and rate of the
-// columns' loads: one row of 8192 x 2048 5.0 us (3.4 TB/s), of 14336 x 14336 39
-// us (5.2 TB/s).  4 or 16 waves, U = 2 or 8, a second run loaded ahead and
-// non-temporal loads: within 3% there, up to 30% slower at 4096 x 14336.
-template <Dt D, int WAVES, int U>
-__global__ __launch_bounds__(64 * WAVES) void k_int8_rows(Int8Args a, bool wide) {
+// Tiles of 16 MF x 16 NF results, too small to share an operand's loads between
+// waves: the WAVES waves take slabs of 128 bytes of K in turn, each through a
+// ring of its own in LDS (so the loop has no barrier), and add their sums
+// through LDS at the end.
+//
+// Fragments loaded straight into registers cost four times the copies' time:
+// lanes next to each other hold different rows, so a load touches a line per
+// lane.  The copies take 8 lanes, 128 bytes, to a row, and the transposition
+// is the LDS read's.  Chunk c of row r is kept at c ^ (r / 2 % 8) of its 128
+// bytes: the 16 lanes of a read group (see i8_swizzle) then meet 16 different
+// bank quads.
+//
+// Bound by what a CU can have loaded, 105 GB/s each, after about 2 us for the
+// launch, the first loads and the sums, or by the memory's rate.  Measured (us,
+// in the shape chosen, against k_int8_tile with its ranges of K): 1 x 8192 x
+// 2048 4.9 (7.8), 1 x 14336 x 14336 36 (66; 205 MB), 16 x 2048 x 8192 5.4 (9.0),
+// 64 x 2048 x 2048 3.3 (7.4), 64 x 2048 x 8192 6.9 (11.3), 64 x 8192 x 2048 6.3
+// (9.2), 512 x 2048 x 4096 10.7 (14.8).  Fragments straight into registers take
+// 5.5, 41, 9.3, 4.8, 13 and 12 us for the first six.  Twice the waves with half the
+// ring, or longer rings, change 3% either way.
+template <int MF_, int NF_, int WAVES_, int STAGES_>
+struct I8Small {
+  static constexpr int MF = MF_, NF = NF_, WAVES = WAVES_, STAGES = STAGES_;
+  static constexpr int BM = 16 * MF, BN = 16 * NF, THREADS = 64 * WAVES;
+  static constexpr int ROW = 128, STAGE = (BM + BN) * ROW, OPS = STAGE / 1024;
+  static constexpr int FRAGS = MF * NF, PER = (FRAGS + WAVES - 1) / WAVES;  // fragments of the results, and of one wave
+  static constexpr int LDS = WAVES * STAGES * STAGE;
+  static_assert(WAVES * FRAGS * 1024 <= LDS && LDS <= 160 * 1024, "the sums take the rings' place");
+};
+template <Dt D, class C>
+__global__ __launch_bounds__(C::THREADS) void k_int8_small(Int8Args a, bool wide, int tiles) {
   using T = typename DtT<D>::T;
-  __shared__ i32x4_t red[WAVES][64];
+  constexpr int MF = C::MF, NF = C::NF, WAVES = C::WAVES, STAGES = C::STAGES, OPS = C::OPS;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * 16;
-  const int r = lane & 15, kl = (lane >> 4) * 16;
-  const int8_t *pa = a.a + (int64_t)min(r, a.M - 1) * a.ld_a;
-  const int8_t *pb = a.b + (int64_t)min(n0 + r, a.N - 1) * a.ld_b;
-  // the results' row and columns, and their scales, loaded before the sums
-  const int n = n0 + (kl >> 2);
-  const float sa = a.a_scale[min(r, a.M - 1)], bias = a.bias ? a.bias[min(r, a.M - 1)] : 0.0f;
-  float sb[4];
+  const int rho = lane & 15, h = lane >> 4;
+  // an eighth of the tiles, column of tiles after column, for each XCD
+  // (workgroups go to the 8 in turn), whose L2 then keeps their rows of b
+  const int tiles_m = (a.M - 1) / C::BM + 1, each = gridDim.x / 8;
+  const int tile = blockIdx.x % 8 * each + blockIdx.x / 8;
+  const int n0 = tile / tiles_m * C::BN, m0 = tile % tiles_m * C::BM;
+  if (tile >= tiles) return;
+
+  // the scales of the results that this wave writes, loaded before the sums
+  float sa[C::PER], bias[C::PER], sb[C::PER][4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) sb[q] = a.b_scale[min(n + q, a.N - 1)];
-  i32x4_t acc = {0, 0, 0, 0};
+  for (int p = 0; p < C::PER; ++p) {
+    const int f = min(wave + p * WAVES, C::FRAGS - 1);
+    const int m = min(m0 + 16 * (f / NF) + rho, a.M - 1), n = n0 + 16 * (f % NF) + 4 * h;
+    sa[p] = a.a_scale[m];
+    bias[p] = a.bias ? a.bias[m] : 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sb[p][q] = a.b_scale[min(n + q, a.N - 1)];
+  }
+
+  // copy j: rows 8 j .. 8 j + 7 of the stage, a's first, 128 bytes each
+  const int8_t *row[OPS];
+#pragma unroll
+  for (int j = 0; j < OPS; ++j) {
+    const int r = 8 * j + (lane >> 3);
+    row[j] = 8 * j < C::BM ? a.a + (int64_t)min(m0 + r, a.M - 1) * a.ld_a
+                           : a.b + (int64_t)min(n0 + r - C::BM, a.N - 1) * a.ld_b;
+  }
+  int chunk[2];  // the lane's, by the parity of j
+#pragma unroll
+  for (int p = 0; p < 2; ++p) chunk[p] = ((lane & 7) ^ (4 * p + (lane >> 4))) * 16;
   const int last = (a.K - 1) / 16 * 16;
-  for (int k0 = wave * 64 * U; k0 < a.K; k0 += WAVES * 64 * U) {
-    u32x4_t fa[U], fb[U];
+  const int slabs = (a.K + C::ROW - 1) / C::ROW;
+  const int mine = slabs > wave ? (slabs - wave - 1) / WAVES + 1 : 0;
+  char *ring = smem + wave * (STAGES * C::STAGE);
+  const uint32_t base = lds_address(ring);
+  auto issue = [&](int i) {
+    const int k0 = (wave + i * WAVES) * C::ROW;
+    const uint32_t stage = base + (uint32_t)(i % STAGES * C::STAGE);
 #pragma unroll
-    for (int u = 0; u < U; ++u) fb[u] = *reinterpret_cast<const u32x4_t *>(pb + min(k0 + 64 * u + kl, last));
+    for (int j = 0; j < OPS; ++j)
+      copy16(row[j] + min(k0 + chunk[j & 1], last), __builtin_amdgcn_readfirstlane((int)(stage + 1024 * j)));
+  };
 #pragma unroll
-    for (int u = 0; u < U; ++u) fa[u] = *reinterpret_cast<const u32x4_t *>(pa + min(k0 + 64 * u + kl, last));
-    if (k0 + 64 * U > a.K) {
+  for (int i = 0; i < STAGES; ++i)
+    if (i < mine) issue(i);
+  i32x4_t acc[MF][NF];
 #pragma unroll
-      for (int u = 0; u < U; ++u) fa[u] = keep_bytes(fa[u], a.K - (k0 + 64 * u + kl));
+  for (int x = 0; x < MF; ++x)
+#pragma unroll
+    for (int y = 0; y < NF; ++y) acc[x][y] = i32x4_t{0, 0, 0, 0};
+  for (int i = 0; i < mine; ++i) {
+    wait_stages<OPS>(min(mine - 1 - i, STAGES - 1));
+    const char *stage = ring + i % STAGES * C::STAGE + rho * C::ROW;
+    u32x4_t fa[2][MF], fb[2][NF];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int at = ((4 * s + h) ^ (rho >> 1)) * 16;
+#pragma unroll
+      for (int x = 0; x < MF; ++x) fa[s][x] = *reinterpret_cast<const u32x4_t *>(stage + x * 16 * C::ROW + at);
+#pragma unroll
+      for (int y = 0; y < NF; ++y) fb[s][y] = *reinterpret_cast<const u32x4_t *>(stage + (MF + y) * 16 * C::ROW + at);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage is read, and may be written again
+    if (i + STAGES < mine) issue(i + STAGES);
+    const int left = a.K - (wave + i * WAVES) * C::ROW;
+    if (left < C::ROW) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int x = 0; x < MF; ++x) fa[s][x] = keep_bytes(fa[s][x], left - 16 * (4 * s + h));
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, fb[u]),
-                                                 __builtin_bit_cast(i32x4_t, fa[u]), acc, 0, 0, 0);
-  }
-  red[wave][lane] = acc;
-  __syncthreads();
-  if (wave == 0 && r < a.M && n < a.N) {
-    i32x4_t s = red[0][lane];
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) s += red[w][lane];
-    store4<D>(static_cast<T *>(a.y) + (int64_t)r * a.ld_y, n, a.N, s, sa, sb, bias, wide);
+      for (int x = 0; x < MF; ++x)
+#pragma unroll
+        for (int y = 0; y < NF; ++y)
+          acc[x][y] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, fb[s][y]),
+                                                           __builtin_bit_cast(i32x4_t, fa[s][x]), acc[x][y], 0, 0, 0);
+  }
+  __syncthreads();  // every wave has read its stages
+  i32x4_t *sums = reinterpret_cast<i32x4_t *>(smem);
+#pragma unroll
+  for (int x = 0; x < MF; ++x)
+#pragma unroll
+    for (int y = 0; y < NF; ++y) sums[(wave * C::FRAGS + x * NF + y) * 64 + lane] = acc[x][y];
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < C::PER; ++p) {
+    const int f = wave + p * WAVES;
+    const int m = m0 + 16 * (f / NF) + rho, n = n0 + 16 * (f % NF) + 4 * h;
+    if (f >= C::FRAGS || m >= a.M || n >= a.N) continue;
+    i32x4_t s = sums[f * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) s += sums[(w * C::FRAGS + f) * 64 + lane];
+    store4<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, s, sa[p], sb[p], bias[p], wide);
   }
 }
 
 // ---- launch -----------------------------------------------------------------------
 
-// The tile shapes: rows, columns, and the time of one 64-byte slab of K per
-// tile on a CU, in units of 10 ns (measured over K = 2048 and 8192 with the
-// chip full; the smaller ones are bound by the loads a CU can have in flight,
-// the largest by the power of the matrix cores).  64 x 2048 x 8192: 25 us in 64
-// x 128 tiles, 11.4 in 8 ranges of K; 1024 x 8192 x 2048: 28 us in 256 x 256
-// tiles, 21.6 in 256 x 128; 2048 x 2048 x 8192: 52 us in 256 x 128, 40 in 128 x 128.
-enum I8Shape { I8_ROWS = -1, I8_256x256, I8_256x128, I8_128x128, I8_64x128, I8_SHAPES };
+// The tile shapes of k_int8_tile: rows, columns, and the time of one 64-byte
+// slab of K per tile on a CU, in units of 10 ns (measured over K = 2048 and
+// 8192 with the chip full; the smaller ones are bound by the loads a CU can have
+// in flight, the largest by the power of the matrix cores).  1024 x 8192 x 2048:
+// 28 us in 256 x 256 tiles, 21.6 in 256 x 128; 2048 x 2048 x 8192: 52 us in 256
+// x 128, 40 in 128 x 128.
+enum I8Shape { I8_256x256, I8_256x128, I8_128x128, I8_64x128, I8_SHAPES };
 struct I8ShapeCost {
   int bm, bn, slab;
 };
 constexpr I8ShapeCost I8_COST[I8_SHAPES] = {{256, 256, 80}, {256, 128, 53}, {128, 128, 30}, {64, 128, 19}};
 constexpr int I8_TILE_COST = 250;   // of a tile besides its slabs: start, ring fill, results
 constexpr int I8_JOIN_COST = 250;   // of the second launch
-constexpr int I8_ROWS_COST = 150;   // of k_int8_rows besides its bytes
 constexpr int I8_MAX_PARTS = 16;
 constexpr size_t I8_MAX_PARTIAL = (size_t)64 << 20;
 
+// Those of k_int8_small: rows, columns, workgroups that a CU holds, and the
+// time besides the loads, once and for each round of workgroups (fitted to 31
+// sizes of 1 to 2048 rows: 10% in the mean; over 50 sizes the shape chosen is
+// the fastest one, or within 7% of it but for 128 x 4096 x 16384, 14%).
+enum I8SmallShape { I8_16x16, I8_16x32, I8_32x32, I8_32x64, I8_64x64, I8_SMALL_SHAPES };
+struct I8SmallCost {
+  int bm, bn, held, start, round;
+};
+constexpr I8SmallCost I8_SMALL[I8_SMALL_SHAPES] = {
+    {16, 16, 2, 155, 85}, {16, 32, 3, 200, 40}, {32, 32, 2, 140, 115}, {32, 64, 1, 40, 235}, {64, 64, 1, 0, 380}};
+constexpr int I8_SMALL_RATE = 1050;  // bytes a CU loads in 10 ns
+
 struct I8Plan {
-  int shape, parts, k_part;  // parts == 1: no workspace
-  size_t bytes;
+  bool small;         // `shape` is an I8SmallShape
+  int shape;
+  int parts, k_part;  // k_int8_tile: the ranges of K
+  size_t bytes;       // of the workspace: 0 with one range
 };
 
-static int64_t i8_tiles(int shape, int M, int N) {
-  return (int64_t)((M - 1) / I8_COST[shape].bm + 1) * ((N - 1) / I8_COST[shape].bn + 1);
-}
+static int64_t i8_tiles(int bm, int bn, int M, int N) { return (int64_t)((M - 1) / bm + 1) * ((N - 1) / bn + 1); }
 
-// The shape and number of K ranges with the least estimated time: 256 CUs take
-// the tiles in rounds; the ranges' sums are written and read once (4 bytes
-// each way at about 4 TB/s).
+// The kernel, shape and number of K ranges with the least estimated time: 256
+// CUs take the tiles in rounds; the ranges' sums are written and read once (4
+// bytes each way at about 4 TB/s), the operands read at 5 TB/s at most.
 static I8Plan i8_plan(int M, int N, int K) {
   const int nk = (K + SLAB - 1) / SLAB;
-  I8Plan best{I8_256x256, 1, nk * SLAB, 0};
+  I8Plan best{false, I8_256x256, 1, nk * SLAB, 0};
   int64_t least = INT64_MAX;
-  // the operands' bytes at 5 TB/s
-  const int64_t bytes = ((int64_t)M + N) * K / 50000;
-  // At most 16 rows: k_int8_rows, bound by the columns' bytes at 4.9 TB/s for
-  // one row and 3.4 for 16 (every workgroup reads all rows), or by the 16
-  // columns of one workgroup at 32 to 22 GB/s.  One row of 4096 x 14336: 10.6
-  // us, 13.2 from tiles; 16 rows of 14336 x 4096: 18.2 us, 14.3 from tiles.
-  if (M <= 16) {
-    best.shape = I8_ROWS;
-    least = I8_ROWS_COST + std::max((int64_t)N * K / (50000 - 1000 * M), (int64_t)K * (32 + M) / 660);
+  const int64_t bytes = ((int64_t)M + N) * K;
+  for (int shape = 0; shape < I8_SMALL_SHAPES; ++shape) {
+    const I8SmallCost &c = I8_SMALL[shape];
+    const int64_t tiles = i8_tiles(c.bm, c.bn, M, N);
+    const int64_t per_cu = (tiles + 255) / 256, rounds = (tiles + 256 * c.held - 1) / (256 * c.held);
+    const int64_t cost =
+        c.start + rounds * c.round + per_cu * ((int64_t)(c.bm + c.bn) * K / I8_SMALL_RATE) + bytes / 140000;
+    if (cost < least) {
+      least = cost;
+      best = I8Plan{true, shape, 1, nk * SLAB, 0};
+    }
   }
   for (int shape = 0; shape < I8_SHAPES; ++shape) {
-    const int64_t tiles = i8_tiles(shape, M, N);
+    const int64_t tiles = i8_tiles(I8_COST[shape].bm, I8_COST[shape].bn, M, N);
     for (int want = 1; want <= I8_MAX_PARTS; want *= 2) {
       const int per = (nk + want - 1) / want, parts = (nk + per - 1) / per;
       const size_t sums = (size_t)parts * M * ((N + 3) / 4 * 4);
       if (want > 1 && (parts < want || per < 4 || sums * 4 > I8_MAX_PARTIAL)) break;
       const int64_t rounds = (tiles * parts + 255) / 256;
-      const int64_t cost = std::max(rounds * (per * I8_COST[shape].slab + I8_TILE_COST), bytes + I8_TILE_COST) +
+      const int64_t cost = std::max(rounds * (per * I8_COST[shape].slab + I8_TILE_COST), bytes / 50000 + I8_TILE_COST) +
                            (parts > 1 ? I8_JOIN_COST + (int64_t)(sums / 5000) : 0);
       if (cost < least) {
         least = cost;
-        best = I8Plan{shape, parts, per * SLAB, parts > 1 ? sums * 4 : 0};
+        best = I8Plan{false, shape, parts, per * SLAB, parts > 1 ? sums * 4 : 0};
       }
     }
   }
   return best;
 }
 
-// Rows too far apart for 32-bit offsets within a tile: those go through
-// 64-bit addresses, in one tile shape and without ranges.
+// Rows too far apart for 32-bit offsets within a tile: k_int8_small, which has
+// 64-bit addresses, takes those.
 static bool i8_far(const Int8Args &a) {
   return std::max(a.ld_a, a.ld_b) > ((int64_t)1 << 31) / 256 - INT8_MAX_K;
 }
@@ -593,15 +675,29 @@ size_t int8_matmul_workspace(int M, int N, int K) {
   return M <= 0 || N <= 0 ? 0 : i8_plan(M, N, K).bytes;
 }
 
-template <Dt D, class Cfg, int BN, bool FAR = false, bool STREAM = false>
+template <Dt D, class Cfg, int BN, bool STREAM = false>
 static hipError_t launch_tile(const Int8Args &a, int parts, bool wide, hipStream_t s) {
-  auto kern = k_int8_tile<D, Cfg, BN, FAR, STREAM>;
+  auto kern = k_int8_tile<D, Cfg, BN, STREAM>;
   constexpr int lds = I8Tile<Cfg, BN>::LDS;
   hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
-  const int64_t tiles = (int64_t)((a.M - 1) / Cfg::BM + 1) * ((a.N - 1) / BN + 1);
+  const int64_t tiles = i8_tiles(Cfg::BM, BN, a.M, a.N);
   if (tiles * parts > (int64_t)UINT32_MAX / Cfg::THREADS) return hipErrorInvalidValue;
   hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * parts)), dim3(Cfg::THREADS), lds, s, a, wide, (int)tiles);
+  return hipGetLastError();
+}
+
+template <Dt D, int MF, int NF, int WAVES, int STAGES>
+static hipError_t launch_small(const Int8Args &a, bool wide, hipStream_t s) {
+  using C = I8Small<MF, NF, WAVES, STAGES>;
+  auto kern = k_int8_small<D, C>;
+  if constexpr (C::LDS > 64 * 1024) {
+    hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t tiles = i8_tiles(C::BM, C::BN, a.M, a.N), wgs = (tiles + 7) / 8 * 8;
+  if (wgs > (int64_t)UINT32_MAX / C::THREADS) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(C::THREADS), C::LDS, s, a, wide, (int)tiles);
   return hipGetLastError();
 }
 
@@ -618,20 +714,24 @@ template <Dt D>
 static hipError_t matmul_dt(const Int8Args &args, void *workspace, hipStream_t s) {
   Int8Args a = args;
   const bool wide = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && (a.ld_y * DtT<D>::size) % 16 == 0;
-  const I8Plan p = i8_plan(a.M, a.N, a.K);
-  if (p.shape == I8_ROWS || (a.M <= 16 && i8_far(a))) {
-    hipLaunchKernelGGL((k_int8_rows<D, 8, 4>), dim3((a.N - 1) / 16 + 1), dim3(64 * 8), 0, s, a, wide);
-    return hipGetLastError();
+  I8Plan p = i8_plan(a.M, a.N, a.K);
+  if (i8_far(a) && !p.small) p = I8Plan{true, I8_64x64, 1, 0, 0};
+  if (p.small) {
+    switch (p.shape) {
+      case I8_16x16: return launch_small<D, 1, 1, 8, 2>(a, wide, s);
+      case I8_16x32: return launch_small<D, 1, 2, 4, 2>(a, wide, s);
+      case I8_32x32: return launch_small<D, 2, 2, 4, 2>(a, wide, s);
+      case I8_32x64: return launch_small<D, 2, 4, 8, 1>(a, wide, s);
+      case I8_64x64: return launch_small<D, 4, 4, 8, 1>(a, wide, s);
+    }
+    return hipErrorInvalidValue;
   }
-  a.k_part = (a.K + SLAB - 1) / SLAB * SLAB;
-  a.partial = nullptr;
-  if (i8_far(a)) return launch_tile<D, DmaCfg<64, 4, 4>, 128, true>(a, 1, wide, s);
   a.k_part = p.k_part;
-  if (p.parts > 1) a.partial = static_cast<int *>(workspace);
+  a.partial = p.parts > 1 ? static_cast<int *>(workspace) : nullptr;
   hipError_t e = hipErrorInvalidValue;
   switch (p.shape) {
     case I8_256x256:
-      e = i8_stream<D>(a) ? launch_tile<D, DmaCfg<256, 8, 4>, 256, false, true>(a, p.parts, wide, s)
+      e = i8_stream<D>(a) ? launch_tile<D, DmaCfg<256, 8, 4>, 256, true>(a, p.parts, wide, s)
                           : launch_tile<D, DmaCfg<256, 8, 4>, 256>(a, p.parts, wide, s);
       break;
     case I8_256x128: e = launch_tile<D, DmaCfg<256, 8, 4>, 128>(a, p.parts, wide, s); break;

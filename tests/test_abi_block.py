@@ -115,8 +115,8 @@ def test_quantize_validation(kw, status):
     (dict(a=_q(scale=None)), INVALID), (dict(ld_y=7), INVALID), (dict(y=FAKE + 1), UNSUPPORTED),
     (dict(a=_q(rows=(1 << 26) + 1)), UNSUPPORTED), (dict(b=_q(rows=(1 << 26) + 1), ld_y=1 << 27), UNSUPPORTED),
     (dict(bias=FAKE + 1), UNSUPPORTED), (dict(ws=FAKE + 16), UNSUPPORTED),
-    (dict(a=_q(rows=64, cols=8192, ld=8192), b=_q(cols=8192, ld=8192), ws=None), WORKSPACE),
-    (dict(a=_q(rows=64, cols=8192, ld=8192), b=_q(cols=8192, ld=8192), ws_bytes=100), WORKSPACE),
+    (dict(a=_q(rows=64, cols=40000, ld=40000), b=_q(cols=40000, ld=40000), ws=None), WORKSPACE),
+    (dict(a=_q(rows=64, cols=40000, ld=40000), b=_q(cols=40000, ld=40000), ws_bytes=100), WORKSPACE),
 ])
 def test_product_validation(kw, status):
     a = dict(a=_q(), b=_q(), bias=None, dtype=BF16, y=FAKE, ld_y=8, ws=FAKE, ws_bytes=1 << 40)
@@ -128,10 +128,10 @@ def test_product_validation(kw, status):
 
 def test_product_workspace():
     ws = twell.twell_int8_matmul_workspace_size
-    assert ws(1, 8192, 2048) == 0 and ws(8192, 8192, 2048) == 0 and ws(0, 64, 64) == 0
+    assert ws(1, 8192, 2048) == 0 and ws(64, 2048, 8192) == 0 and ws(8192, 8192, 2048) == 0 and ws(0, 64, 64) == 0
     assert ws(64, 64, 0) == 0 and ws(64, 64, 70000) == 0 and ws(-1, 64, 64) == 0
     # few tiles and a long K: whole [M][N] matrices of 4-byte sums
-    for M, N, K in [(64, 2048, 8192), (17, 333, 65536), (256, 2048, 8192), (100, 1, 4096)]:
+    for M, N, K in [(40, 515, 40000), (17, 333, 65536), (300, 260, 20000), (2349, 39, 29705)]:
         n = ws(M, N, K)
         assert n > 0 and n % (M * ((N + 3) // 4 * 4) * 4) == 0 and n <= 64 << 20, (M, N, K, n)
 

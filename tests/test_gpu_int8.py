@@ -65,7 +65,9 @@ SHAPES = [(1, 1, 1), (1, 5, 3), (2, 16, 16), (1, 64, 64), (1, 1000, 777), (3, 25
           (127, 129, 383), (128, 128, 512), (129, 257, 640), (200, 1, 300), (255, 256, 63), (256, 256, 1024),
           (257, 511, 1031), (300, 700, 48), (333, 1000, 777), (513, 515, 400), (1, 2048, 8192), (8, 8192, 512),
           (48, 512, 4096), (64, 2048, 8192), (32, 300, 16384), (17, 131, 5003), (100, 1, 4096),
-          (300, 260, 20000), (129, 1000, 7777), (700, 520, 2000), (1500, 300, 144), (1024, 1024, 1024)]
+          (300, 260, 20000), (129, 1000, 7777), (700, 520, 2000), (1500, 300, 144), (1024, 1024, 1024),
+          (2076, 18, 42), (122, 1133, 548), (440, 578, 832), (257, 1996, 983), (101, 4171, 39), (4564, 391, 33),
+          (4104, 928, 19), (2067, 3593, 150), (4, 6, 50556), (1, 1524, 24721), (2349, 39, 29705), (1637, 257, 28417)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -139,13 +141,14 @@ def test_special_scales(M):
     assert np.array_equal(y[~np.isnan(want)], want[~np.isnan(want)])
 
 
-def test_operands_beyond_32_bit_offsets():
+@pytest.mark.parametrize("K", [200, 50556])
+def test_operands_beyond_32_bit_offsets(K):
     # rows 2^31 + 64 bytes apart: far outside 32-bit offsets from the first
     import torch
-    ld, K = (1 << 31) + 64, 200
+    ld = (1 << 31) + 64
     for M in (3, 20):
         a, b = _int8(M, K, 10), _int8(3, K, 11)
-        wide = torch.empty(2 * ld + 4096, dtype=torch.int8, device="cuda:0")
+        wide = torch.empty(2 * ld + (1 << 16), dtype=torch.int8, device="cuda:0")
         bv = wide.as_strided((3, K), (ld, 1))
         bv.copy_(torch.from_numpy(b))
         sa, sb = np.ones(M, np.float32), np.ones(3, np.float32)
@@ -169,7 +172,7 @@ def test_output_beyond_32_bit_offsets():
 def test_cut_products_repeat_and_take_a_workspace():
     # K cut into ranges: the same bits again, over a workspace of any contents
     import torch
-    M, N, K = 64, 515, 8200
+    M, N, K = 40, 515, 40000
     a, b = _int8(M, K, 17), _int8(N, K, 18)
     sa, sb = np.full(M, 0.5, np.float32), np.full(N, 0.125, np.float32)
     n = tw.twell_int8_matmul_workspace_size(M, N, K)
