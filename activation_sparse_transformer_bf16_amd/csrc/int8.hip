@@ -32,20 +32,27 @@ __device__ __forceinline__ float scaled(int acc, float sa, float sb, float bias)
   return (float)acc * sa * sb + bias;
 }
 
+// Rows of y are aligned to the element only; runs of results are stored whole
+// all the same.  8192 x 8191 x 2048 bf16, where few rows are aligned: 131 us,
+// element by element 214.
+typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+
 // Four results of one row from column n on.
 template <Dt D>
 __device__ __forceinline__ void store4(typename DtT<D>::T *row, int n, int N, i32x4_t s, float sa,
-                                       const float (&sb)[4], float bias, bool wide) {
+                                       const float (&sb)[4], float bias) {
   float v[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) v[q] = scaled(s[q], sa, sb[q], bias);
   typename DtT<D>::T *p = row + n;
-  if (wide && n + 4 <= N) {
+  if (n + 4 <= N) {
     if constexpr (D == Dt::BF16)
-      *reinterpret_cast<u32x2_t *>(p) = u32x2_t{(uint32_t)bf16_rne(v[0]) | ((uint32_t)bf16_rne(v[1]) << 16),
-                                               (uint32_t)bf16_rne(v[2]) | ((uint32_t)bf16_rne(v[3]) << 16)};
+      *reinterpret_cast<u32x2_any_t *>(p) = u32x2_any_t{(uint32_t)bf16_rne(v[0]) | ((uint32_t)bf16_rne(v[1]) << 16),
+                                                       (uint32_t)bf16_rne(v[2]) | ((uint32_t)bf16_rne(v[3]) << 16)};
     else
-      *reinterpret_cast<f32x4_t *>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<u32x4_any_t *>(p) = u32x4_any_t{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                       __float_as_uint(v[2]), __float_as_uint(v[3])};
   } else {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -162,18 +169,17 @@ __device__ __forceinline__ int i8_col(int j, int rho) {
   return D == Dt::BF16 ? 32 * (j >> 1) + 8 * (rho >> 2) + 4 * (j & 1) + (rho & 3) : 16 * j + rho;
 }
 
-// 16 bytes of y per lane; a run that is not whole (past N, or rows that are
-// not 16-byte aligned) goes element by element.
+// 16 bytes of y per lane; a run that crosses N goes element by element.
 template <Dt D, bool STREAM>
-__device__ __forceinline__ void store_run(void *row, int n, int N, u32x4_t v, bool wide) {
+__device__ __forceinline__ void store_run(void *row, int n, int N, u32x4_t v) {
   using T = typename DtT<D>::T;
   constexpr int E = 16 / DtT<D>::size;
   T *p = static_cast<T *>(row) + n;
-  if (wide && n + E <= N) {
+  if (n + E <= N) {
     if constexpr (STREAM)
-      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t *>(p));
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any_t *>(p));
     else
-      *reinterpret_cast<u32x4_t *>(p) = v;
+      *reinterpret_cast<u32x4_any_t *>(p) = v;
   } else {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -223,7 +229,7 @@ struct I8Tile {
 // STREAM: the results are stored non-temporally (a template, as the compiler
 // joins the two kinds of store into the ordinary one under a run-time choice).
 template <Dt D, class Cfg, int BN, bool STREAM>
-__global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile(Int8Args a, bool wide, int tiles) {
+__global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile(Int8Args a, int tiles) {
   using T = typename DtT<D>::T;
   using WT = WaveTile<BN, Cfg>;
   using L = I8Tile<Cfg, BN>;
@@ -417,7 +423,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile
       const int r = p * (64 / PER_ROW) + lane / PER_ROW, c = lane % PER_ROW;
       const int m = m0 + row + r, n = n0 + col0 + c * (16 / S);
       const u32x4_t w = *reinterpret_cast<const u32x4_t *>(mine + r * PITCH + c * 16);
-      if (m < a.M && n < a.N) store_run<D, STREAM>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, w, wide);
+      if (m < a.M && n < a.N) store_run<D, STREAM>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, w);
     }
     wave_sync();
   }
@@ -426,7 +432,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_int8_tile
 // The ranges' sums added, scaled and written: 4 columns per thread, a row per
 // blockIdx.y; four ranges' loads in flight at a time.
 template <Dt D>
-__global__ __launch_bounds__(256) void k_int8_join(Int8Args a, int parts, bool wide) {
+__global__ __launch_bounds__(256) void k_int8_join(Int8Args a, int parts) {
   using T = typename DtT<D>::T;
   const int n_pad = (a.N + 3) / 4 * 4;
   const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
@@ -447,7 +453,7 @@ __global__ __launch_bounds__(256) void k_int8_join(Int8Args a, int parts, bool w
       for (int k = 0; k < 4; ++k)
         if (p + k < parts) s += v[k];
     }
-    store4<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, s, sa, sb, bias, wide);
+    store4<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, s, sa, sb, bias);
   }
 }
 
@@ -483,7 +489,7 @@ struct I8Small {
   static_assert(WAVES * FRAGS * 1024 <= LDS && LDS <= 160 * 1024, "the sums take the rings' place");
 };
 template <Dt D, class C>
-__global__ __launch_bounds__(C::THREADS) void k_int8_small(Int8Args a, bool wide, int tiles) {
+__global__ __launch_bounds__(C::THREADS) void k_int8_small(Int8Args a, int tiles) {
   using T = typename DtT<D>::T;
   constexpr int MF = C::MF, NF = C::NF, WAVES = C::WAVES, STAGES = C::STAGES, OPS = C::OPS;
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -585,7 +591,7 @@ __global__ __launch_bounds__(C::THREADS) void k_int8_small(Int8Args a, bool wide
     i32x4_t s = sums[f * 64 + lane];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) s += sums[(w * C::FRAGS + f) * 64 + lane];
-    store4<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, s, sa[p], sb[p], bias[p], wide);
+    store4<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, s, sa[p], sb[p], bias[p]);
   }
 }
 
@@ -676,19 +682,19 @@ size_t int8_matmul_workspace(int M, int N, int K) {
 }
 
 template <Dt D, class Cfg, int BN, bool STREAM = false>
-static hipError_t launch_tile(const Int8Args &a, int parts, bool wide, hipStream_t s) {
+static hipError_t launch_tile(const Int8Args &a, int parts, hipStream_t s) {
   auto kern = k_int8_tile<D, Cfg, BN, STREAM>;
   constexpr int lds = I8Tile<Cfg, BN>::LDS;
   hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   const int64_t tiles = i8_tiles(Cfg::BM, BN, a.M, a.N);
   if (tiles * parts > (int64_t)UINT32_MAX / Cfg::THREADS) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * parts)), dim3(Cfg::THREADS), lds, s, a, wide, (int)tiles);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * parts)), dim3(Cfg::THREADS), lds, s, a, (int)tiles);
   return hipGetLastError();
 }
 
 template <Dt D, int MF, int NF, int WAVES, int STAGES>
-static hipError_t launch_small(const Int8Args &a, bool wide, hipStream_t s) {
+static hipError_t launch_small(const Int8Args &a, hipStream_t s) {
   using C = I8Small<MF, NF, WAVES, STAGES>;
   auto kern = k_int8_small<D, C>;
   if constexpr (C::LDS > 64 * 1024) {
@@ -697,7 +703,7 @@ static hipError_t launch_small(const Int8Args &a, bool wide, hipStream_t s) {
   }
   const int64_t tiles = i8_tiles(C::BM, C::BN, a.M, a.N), wgs = (tiles + 7) / 8 * 8;
   if (wgs > (int64_t)UINT32_MAX / C::THREADS) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(C::THREADS), C::LDS, s, a, wide, (int)tiles);
+  hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(C::THREADS), C::LDS, s, a, (int)tiles);
   return hipGetLastError();
 }
 
@@ -713,16 +719,15 @@ static bool i8_stream(const Int8Args &a) {
 template <Dt D>
 static hipError_t matmul_dt(const Int8Args &args, void *workspace, hipStream_t s) {
   Int8Args a = args;
-  const bool wide = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && (a.ld_y * DtT<D>::size) % 16 == 0;
   I8Plan p = i8_plan(a.M, a.N, a.K);
   if (i8_far(a) && !p.small) p = I8Plan{true, I8_64x64, 1, 0, 0};
   if (p.small) {
     switch (p.shape) {
-      case I8_16x16: return launch_small<D, 1, 1, 8, 2>(a, wide, s);
-      case I8_16x32: return launch_small<D, 1, 2, 4, 2>(a, wide, s);
-      case I8_32x32: return launch_small<D, 2, 2, 4, 2>(a, wide, s);
-      case I8_32x64: return launch_small<D, 2, 4, 8, 1>(a, wide, s);
-      case I8_64x64: return launch_small<D, 4, 4, 8, 1>(a, wide, s);
+      case I8_16x16: return launch_small<D, 1, 1, 8, 2>(a, s);
+      case I8_16x32: return launch_small<D, 1, 2, 4, 2>(a, s);
+      case I8_32x32: return launch_small<D, 2, 2, 4, 2>(a, s);
+      case I8_32x64: return launch_small<D, 2, 4, 8, 1>(a, s);
+      case I8_64x64: return launch_small<D, 4, 4, 8, 1>(a, s);
     }
     return hipErrorInvalidValue;
   }
@@ -731,16 +736,16 @@ static hipError_t matmul_dt(const Int8Args &args, void *workspace, hipStream_t s
   hipError_t e = hipErrorInvalidValue;
   switch (p.shape) {
     case I8_256x256:
-      e = i8_stream<D>(a) ? launch_tile<D, DmaCfg<256, 8, 4>, 256, true>(a, p.parts, wide, s)
-                          : launch_tile<D, DmaCfg<256, 8, 4>, 256>(a, p.parts, wide, s);
+      e = i8_stream<D>(a) ? launch_tile<D, DmaCfg<256, 8, 4>, 256, true>(a, p.parts, s)
+                          : launch_tile<D, DmaCfg<256, 8, 4>, 256>(a, p.parts, s);
       break;
-    case I8_256x128: e = launch_tile<D, DmaCfg<256, 8, 4>, 128>(a, p.parts, wide, s); break;
-    case I8_128x128: e = launch_tile<D, DmaCfg<128, 4, 4>, 128>(a, p.parts, wide, s); break;
-    case I8_64x128: e = launch_tile<D, DmaCfg<64, 4, 4>, 128>(a, p.parts, wide, s); break;
+    case I8_256x128: e = launch_tile<D, DmaCfg<256, 8, 4>, 128>(a, p.parts, s); break;
+    case I8_128x128: e = launch_tile<D, DmaCfg<128, 4, 4>, 128>(a, p.parts, s); break;
+    case I8_64x128: e = launch_tile<D, DmaCfg<64, 4, 4>, 128>(a, p.parts, s); break;
   }
   if (e != hipSuccess || p.parts == 1) return e;
   const dim3 grid((unsigned)((a.N - 1) / 1024 + 1), (unsigned)std::min(a.M, 1 << 15));
-  hipLaunchKernelGGL(k_int8_join<D>, grid, dim3(256), 0, s, a, p.parts, wide);
+  hipLaunchKernelGGL(k_int8_join<D>, grid, dim3(256), 0, s, a, p.parts);
   return hipGetLastError();
 }
 

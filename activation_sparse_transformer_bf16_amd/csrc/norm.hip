@@ -26,10 +26,25 @@ constexpr float Q_MAX = 127.0f;
 constexpr float Q_TINY = 0x1p-100f;
 constexpr uint32_t INF_BITS = 0x7F800000u;
 
-// A row of d elements.  AL: 16-byte aligned and a whole number of 16-byte
-// chunks; it is then read and written through a buffer descriptor of exactly
-// its bytes, so that chunks past its end load zeros and store nothing, with no
-// branch.  Otherwise element by element.  `p` is the same for a whole wave.
+// How a kernel reads and writes its rows, in chunks of 16 bytes.
+enum class Rows {
+  WHOLE,  // all 16-byte aligned and a whole number of chunks
+  ANY,    // aligned to the element only, at least one chunk long
+  TINY,   // shorter than one chunk
+};
+
+// A row of d elements; `p` is the same for a whole wave.
+//
+// WHOLE rows go through a buffer descriptor of exactly their bytes, so that
+// chunks past the end load zeros and store nothing, with no branch.
+//
+// ANY rows go through 16-byte accesses at the element's alignment.  The chunk
+// that crosses the end, and those past it, load the row's last 16 bytes
+// instead; trim() then moves the row's elements into place and zeroes the
+// others.  It is apart from load() because it needs the loaded value: a row's
+// loads are all under way before the first is waited for.  The crossing chunk
+// is stored by elements.  8192 x 2047 bf16 with residual: 30 us (25 at 2048),
+// element by element 84, as each load is waited for by itself.
 //
 // Stores of whole rows (h, y, dx) carry the non-temporal bit: written this way
 // they leave L2 to the inputs (bf16, 8192 x 2048 with residual and 8 bits:
@@ -39,8 +54,13 @@ constexpr uint32_t INF_BITS = 0x7F800000u;
 // (NT) where no other kernel's copy in cache is worth keeping: in the
 // quantiser (36.3 -> 32.8 us) and the gradient (16384 x 4096: 96 -> 89 us);
 // in the norm it costs 4 us, as x and residual come from the kernel before.
+// ANY rows share lines between waves, and the bit drops them in between: the
+// quantiser loads those without it (8192 x 2047 fp32: 16.3 -> 14.1 us; the
+// gradient does not gain, 51.8 -> 55.7), and the gradient stores them without
+// it (16384 x 4095 fp32: 195 -> 168 us; the norm does not gain).
 constexpr int NON_TEMPORAL = 2;
-template <Dt D, bool AL, bool NT = false>
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+template <Dt D, Rows R, bool NT = false>
 struct Row {
   using T = typename DtT<D>::T;
   static constexpr int E = 16 / DtT<D>::size;  // elements per chunk
@@ -50,12 +70,21 @@ struct Row {
 
   __device__ __forceinline__ Row(const void *base, int64_t t, int64_t ld, int d_)
       : p(const_cast<T *>(static_cast<const T *>(base)) + t * ld), d(d_) {
-    if constexpr (AL) rsrc = __builtin_amdgcn_make_buffer_rsrc(p, 0, d * (int)sizeof(T), 0x00020000);
+    if constexpr (R == Rows::WHOLE) rsrc = __builtin_amdgcn_make_buffer_rsrc(p, 0, d * (int)sizeof(T), 0x00020000);
   }
-  // elements e0 .. e0 + E - 1, +0 past the end
+  // elements e0 .. e0 + E - 1, +0 past the end; of ANY rows after trim()
   __device__ __forceinline__ u32x4_t load(int e0) const {
-    if constexpr (AL) {
+    if constexpr (R == Rows::WHOLE) {
       return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rsrc, e0 * (int)sizeof(T), 0, NT ? NON_TEMPORAL : 0));
+    } else if constexpr (R == Rows::ANY) {
+      if (__builtin_amdgcn_readfirstlane(e0) >= d) return u32x4_t{0u, 0u, 0u, 0u};  // nothing for this wave
+      uint32_t at = min((uint32_t)e0, (uint32_t)(d - E)) * (uint32_t)sizeof(T);
+      asm volatile("" : "+v"(at));
+      const u32x4_any_t *q = reinterpret_cast<const u32x4_any_t *>(reinterpret_cast<const char *>(p) + at);
+      if constexpr (NT)
+        return __builtin_nontemporal_load(q);
+      else
+        return *q;
     } else {
       u32x4_t w = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -70,9 +99,39 @@ struct Row {
       return w;
     }
   }
+  __device__ __forceinline__ u32x4_t trim(u32x4_t w, int e0) const {
+    if constexpr (R == Rows::ANY) {
+      if (__builtin_amdgcn_readfirstlane(e0) + 64 * E > d) {  // the wave's chunks reach the end
+        const int n = max(e0 - (d - E), 0) * (int)sizeof(T);  // bytes to move by
+        u32x4_t v = w;
+        if constexpr (sizeof(T) == 2) {
+          const bool half = (n & 2) != 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = half ? (v[i] >> 16) | (i < 3 ? w[i < 3 ? i + 1 : 3] << 16 : 0u) : v[i];
+        }
+        const bool one = (n & 4) != 0, two = (n & 8) != 0, all = n >= 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = one ? (i < 3 ? v[i < 3 ? i + 1 : 3] : 0u) : v[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = two ? (i < 2 ? w[i < 2 ? i + 2 : 3] : 0u) : w[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = all ? 0u : w[i];
+      }
+    }
+    return w;
+  }
+  template <bool NTS = true>
   __device__ __forceinline__ void store(int e0, u32x4_t w) const {
-    if constexpr (AL) {
+    if constexpr (R == Rows::WHOLE) {
       __builtin_amdgcn_raw_buffer_store_b128(w, rsrc, e0 * (int)sizeof(T), 0, NON_TEMPORAL);
+    } else if (R == Rows::ANY && e0 + E <= d) {
+      uint32_t at = (uint32_t)e0 * (uint32_t)sizeof(T);
+      asm volatile("" : "+v"(at));
+      u32x4_any_t *q = reinterpret_cast<u32x4_any_t *>(reinterpret_cast<char *>(p) + at);
+      if constexpr (NTS)
+        __builtin_nontemporal_store(w, q);
+      else
+        *q = w;
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i) {
@@ -124,7 +183,7 @@ __device__ __forceinline__ void keep_packed(u32x4_t &w) { asm volatile("" : "+v"
 // rounds it to a whole number (ties to even) whose low byte is the 8-bit
 // value; the product is rounded by itself first (no fused multiply-add), as
 // the definition says.
-template <int E, bool AL>
+template <int E, Rows R>
 __device__ __forceinline__ void store_q(int8_t *row, int e0, int d, const float (&z)[E], float inv, bool bad) {
 #pragma clang fp contract(off)
   uint32_t w[E / 4];
@@ -140,7 +199,7 @@ __device__ __forceinline__ void store_q(int8_t *row, int e0, int d, const float 
     const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);  // bytes 0, 0, b2, b3
     w[k] = bad ? 0u : (lo | hi);
   }
-  if constexpr (AL) {
+  if constexpr (R == Rows::WHOLE) {
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(row, 0, d, 0x00020000);
     if constexpr (E == 8)
       __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{w[0], w[1]}, rsrc, e0, 0, 0);
@@ -212,7 +271,7 @@ constexpr int row_waves(int W) { return W > 4 ? W : 4; }
 // Memory bound: bf16 8192 x 2048 with residual and 8 bits 23.5 us (151 MB, 6.4
 // TB/s; a plain copy of the card moves 6.1-6.3), the quantiser of 8192 x 8192
 // 32.5 us (201 MB, 6.2 TB/s); one row 2.3 us, launch and one round trip.
-template <Dt D, int W, int NC, bool AL, bool NORM>
+template <Dt D, int W, int NC, Rows R, bool NORM>
 __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
   constexpr int E = 16 / DtT<D>::size;
   constexpr int RB = row_waves(W) / W;
@@ -223,7 +282,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
   const int d = a.d;
   const int first = ((wave % W) * 64 + lane) * E;  // the lane's element of chunk 0
   constexpr int STEP = W * 64 * E;
-  const Row<D, AL> weight(a.weight, 0, 0, d);
+  const Row<D, R> weight(a.weight, 0, 0, d);
   int turn = 0;
   for (int64_t t0 = (int64_t)blockIdx.x * RB; t0 < a.rows; t0 += (int64_t)gridDim.x * RB) {
     const int64_t t = t0 + wave / W;
@@ -232,7 +291,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
     float ss = 0.0f;
     uint32_t top = 0;
     if (live) {
-      const Row<D, AL, !NORM> x(a.x, t, a.ld_x, d);
+      const Row<D, R, !NORM && R == Rows::WHOLE> x(a.x, t, a.ld_x, d);
 #pragma unroll
       for (int c = 0; c < NC; ++c) hv[c] = x.load(first + c * STEP);
       if constexpr (HOLD) {
@@ -240,19 +299,26 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
         for (int c = 0; c < NC; ++c) wv[c] = weight.load(first + c * STEP);
       }
       if (NORM && a.residual != nullptr) {
-        const Row<D, AL> residual(a.residual, t, a.ld_res, d);
+        const Row<D, R> residual(a.residual, t, a.ld_res, d);
         u32x4_t rv[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) rv[c] = residual.load(first + c * STEP);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           float u[E], v[E];
-          unpack<D>(hv[c], u);
-          unpack<D>(rv[c], v);
+          unpack<D>(x.trim(hv[c], first + c * STEP), u);
+          unpack<D>(residual.trim(rv[c], first + c * STEP), v);
 #pragma unroll
           for (int i = 0; i < E; ++i) u[i] += v[i];
           hv[c] = pack_chunk<D>(u);
         }
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) hv[c] = x.trim(hv[c], first + c * STEP);
+      }
+      if constexpr (HOLD) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) wv[c] = weight.trim(wv[c], first + c * STEP);
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -266,7 +332,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
         if (a.q != nullptr) {
           if constexpr (NORM) {
             float w[E];
-            unpack<D>(HOLD ? wv[c] : weight.load(first + c * STEP), w);
+            unpack<D>(HOLD ? wv[c] : weight.trim(weight.load(first + c * STEP), first + c * STEP), w);
 #pragma unroll
             for (int i = 0; i < E; ++i) z[i] = u[i] * w[i];
           }
@@ -287,7 +353,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
     const bool bad = s.top >= INF_BITS;
     const float m = fmaxf(__uint_as_float(s.top), Q_TINY);
     const float inv = Q_MAX / m;
-    const Row<D, AL> h(a.h, t, a.ld_h, d), y(a.y, t, a.ld_y, d);
+    const Row<D, R> h(a.h, t, a.ld_h, d), y(a.y, t, a.ld_y, d);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int e0 = first + c * STEP;
@@ -295,7 +361,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
       unpack<D>(hv[c], u);
       if constexpr (NORM) {
         float w[E];
-        unpack<D>(HOLD ? wv[c] : weight.load(e0), w);
+        unpack<D>(HOLD ? wv[c] : weight.trim(weight.load(e0), e0), w);
         if (a.h != nullptr) h.store(e0, hv[c]);
         if (a.y != nullptr) {
           float v[E];
@@ -306,7 +372,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < E; ++i) u[i] *= w[i];
       }
-      if (a.q != nullptr) store_q<E, AL>(a.q + t * a.ld_q, e0, d, u, inv, bad);
+      if (a.q != nullptr) store_q<E, R>(a.q + t * a.ld_q, e0, d, u, inv, bad);
     }
     if (a.q != nullptr && lane == 0 && wave % W == 0)
       a.scale[t] = bad ? __uint_as_float(0x7FC00000u) : r * (m / Q_MAX);
@@ -326,7 +392,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
 // room to load the next row ahead (1 us); one wave with four chunks spills
 // (40 us), 512 workgroups write twice the partial rows (28 us).
 constexpr int BACK_WAVES = 16;
-template <Dt D, int W, int NC, bool AL>
+template <Dt D, int W, int NC, Rows R>
 __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardArgs a) {
   constexpr int E = 16 / DtT<D>::size;
   constexpr int RB = BACK_WAVES / W;
@@ -340,12 +406,12 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
   const int first = ((wave % W) * 64 + lane) * E;
   constexpr int STEP = W * 64 * E;
   float *out = a.partial + (size_t)blockIdx.x * d;
-  const Row<D, AL> weight(a.weight, 0, 0, d);
+  const Row<D, R> weight(a.weight, 0, 0, d);
   u32x4_t wv[HOLD_W ? NC : 1];
   float dw[HOLD ? NC : 1][E];
   if constexpr (HOLD_W) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) wv[c] = weight.load(first + c * STEP);
+    for (int c = 0; c < NC; ++c) wv[c] = weight.trim(weight.load(first + c * STEP), first + c * STEP);
   }
   if constexpr (HOLD) {
 #pragma unroll
@@ -365,14 +431,14 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
   u32x4_t hv[NC], gv[NC], sv[NC];
   auto load_row = [&](int64_t t) {
     if (t >= a.rows) return;
-    const Row<D, AL, true> h(a.h, t, a.ld_h, d), dy(a.dy, t, a.ld_dy, d);
+    const Row<D, R, true> h(a.h, t, a.ld_h, d), dy(a.dy, t, a.ld_dy, d);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       hv[c] = h.load(first + c * STEP);
       gv[c] = dy.load(first + c * STEP);
     }
     if (AHEAD && a.dh != nullptr) {
-      const Row<D, AL, true> dh(a.dh, t, a.ld_dh, d);
+      const Row<D, R, true> dh(a.dh, t, a.ld_dh, d);
 #pragma unroll
       for (int c = 0; c < NC; ++c) sv[c] = dh.load(first + c * STEP);
     }
@@ -388,9 +454,9 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
     u32x4_t hc[NC], gc[NC], sc[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      hc[c] = hv[c];
-      gc[c] = gv[c];
-      sc[c] = sv[c];
+      hc[c] = weight.trim(hv[c], first + c * STEP);
+      gc[c] = weight.trim(gv[c], first + c * STEP);
+      sc[c] = weight.trim(sv[c], first + c * STEP);
     }
     if (AHEAD) load_row(t + step);
     float ss = 0.0f, dot = 0.0f;
@@ -400,7 +466,7 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
         float h[E], g[E], w[E];
         unpack<D>(hc[c], h);
         unpack<D>(gc[c], g);
-        unpack<D>(HOLD_W ? wv[c] : weight.load(first + c * STEP), w);
+        unpack<D>(HOLD_W ? wv[c] : weight.trim(weight.load(first + c * STEP), first + c * STEP), w);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
           ss += h[i] * h[i];
@@ -419,15 +485,15 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
       }
       const float r = rsqrtf(s.a / (float)d + a.eps);
       const float k = r * r * (s.b / (float)d);
-      const Row<D, AL, true> dh(a.dh, t, a.ld_dh, d), dx(a.dx, t, a.ld_dx, d);
+      const Row<D, R, true> dh(a.dh, t, a.ld_dh, d), dx(a.dx, t, a.ld_dx, d);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int e0 = first + c * STEP;
         float h[E], g[E], w[E], o[E];
         unpack<D>(hc[c], h);
         unpack<D>(gc[c], g);
-        unpack<D>(HOLD_W ? wv[c] : weight.load(e0), w);
-        if (!AHEAD && a.dh != nullptr) sc[c] = dh.load(e0);
+        unpack<D>(HOLD_W ? wv[c] : weight.trim(weight.load(e0), e0), w);
+        if (!AHEAD && a.dh != nullptr) sc[c] = dh.trim(dh.load(e0), e0);
         unpack<D>(sc[c], o);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
@@ -438,7 +504,7 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
             out[e0 + i] += p;
           o[i] += r * (g[i] * w[i] - h[i] * k);
         }
-        dx.store(e0, pack_chunk<D>(o));
+        dx.template store<R == Rows::WHOLE>(e0, pack_chunk<D>(o));
         // one chunk after the other: interleaved, their values do not fit the registers
         if constexpr (NC > 2) __builtin_amdgcn_sched_barrier(0);
       }
@@ -511,21 +577,26 @@ static bool rows16(const void *p, int64_t ld, int s) {
 template <Dt D, int W, int NC, bool NORM>
 static hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
   constexpr int S = DtT<D>::size, RB = row_waves(W) / W;
-  const bool al = (a.d * S) % 16 == 0 && rows16(a.x, a.ld_x, S) && rows16(a.residual, a.ld_res, S) && rows16(a.weight, 0, S) &&
-                  rows16(a.h, a.ld_h, S) && rows16(a.y, a.ld_y, S);
+  const bool whole = (a.d * S) % 16 == 0 && rows16(a.x, a.ld_x, S) && rows16(a.residual, a.ld_res, S) &&
+                     rows16(a.weight, 0, S) && rows16(a.h, a.ld_h, S) && rows16(a.y, a.ld_y, S);
   // at most 2^20 workgroups, which take more rows in turn
   const dim3 grid(std::min((a.rows - 1) / RB + 1, 1 << 20)), block(64 * row_waves(W));
-  if (al)
-    hipLaunchKernelGGL((k_norm_rows<D, W, NC, true, NORM>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((k_norm_rows<D, W, NC, false, NORM>), grid, block, 0, s, a);
+  if (whole) {
+    hipLaunchKernelGGL((k_norm_rows<D, W, NC, Rows::WHOLE, NORM>), grid, block, 0, s, a);
+  } else if (a.d * S >= 16) {
+    hipLaunchKernelGGL((k_norm_rows<D, W, NC, Rows::ANY, NORM>), grid, block, 0, s, a);
+  } else if constexpr (W * NC == 1) {
+    hipLaunchKernelGGL((k_norm_rows<D, W, NC, Rows::TINY, NORM>), grid, block, 0, s, a);
+  }
   return hipGetLastError();
 }
 
 // Chunks of 64 lanes x 16 bytes in a row: a wave each up to 4 of them, then 4
 // waves, 16 from 17 chunks on (measured at 4, 8 and 16 chunks, W = 1 ... 16:
 // fewer waves with more chunks each hold fewer rows in flight, 24.1 against
-// 23.0 us at 8192 x 2048 bf16; more waves pay for the barrier, 27.9 us).
+// 23.0 us at 8192 x 2048 bf16; more waves pay for the barrier, 27.9 us).  16 waves
+// take two chunks each where that is enough (2000 x 8192 fp32 with residual
+// 43.9 -> 40.9 us against four).
 template <Dt D, bool NORM>
 static hipError_t norm_rows_dt(const NormArgs &a, hipStream_t s) {
   const int chunks = norm_chunks(a.d, D);
@@ -534,6 +605,7 @@ static hipError_t norm_rows_dt(const NormArgs &a, hipStream_t s) {
   if (chunks <= 4) return launch_rows<D, 4, 1, NORM>(a, s);
   if (chunks <= 8) return launch_rows<D, 4, 2, NORM>(a, s);
   if (chunks <= 16) return launch_rows<D, 4, 4, NORM>(a, s);
+  if (chunks <= 32) return launch_rows<D, 16, 2, NORM>(a, s);
   if (chunks <= 64) return launch_rows<D, 16, 4, NORM>(a, s);
   if (chunks <= NORM_MAX_CHUNKS) return launch_rows<D, 16, 8, NORM>(a, s);
   return hipErrorInvalidValue;
@@ -549,13 +621,16 @@ hipError_t norm_rows(const NormArgs &a, hipStream_t s) {
 template <Dt D, int W, int NC>
 static hipError_t launch_backward(const NormBackwardArgs &a, hipStream_t s) {
   constexpr int S = DtT<D>::size;
-  const bool al = (a.d * S) % 16 == 0 && rows16(a.dy, a.ld_dy, S) && rows16(a.h, a.ld_h, S) && rows16(a.weight, 0, S) &&
-                  rows16(a.dh, a.ld_dh, S) && rows16(a.dx, a.ld_dx, S);
+  const bool whole = (a.d * S) % 16 == 0 && rows16(a.dy, a.ld_dy, S) && rows16(a.h, a.ld_h, S) &&
+                     rows16(a.weight, 0, S) && rows16(a.dh, a.ld_dh, S) && rows16(a.dx, a.ld_dx, S);
   const dim3 grid(a.n_partial), block(64 * BACK_WAVES);
-  if (al)
-    hipLaunchKernelGGL((k_norm_backward<D, W, NC, true>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((k_norm_backward<D, W, NC, false>), grid, block, 0, s, a);
+  if (whole) {
+    hipLaunchKernelGGL((k_norm_backward<D, W, NC, Rows::WHOLE>), grid, block, 0, s, a);
+  } else if (a.d * S >= 16) {
+    hipLaunchKernelGGL((k_norm_backward<D, W, NC, Rows::ANY>), grid, block, 0, s, a);
+  } else if constexpr (W * NC == 1) {
+    hipLaunchKernelGGL((k_norm_backward<D, W, NC, Rows::TINY>), grid, block, 0, s, a);
+  }
   return hipGetLastError();
 }
 

@@ -157,6 +157,19 @@ def test_operands_beyond_32_bit_offsets(K):
         _check(tw.twell_int8_matmul(bv, _vec(sb), _dev(a), _vec(sa), dtype=torch_dtype("f32")), b, sb, a, sa, None, "f32")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_results_beyond_the_cache(dtype):
+    # over 256 MB of results, in rows of no alignment: sums below 2^24, so that
+    # the fp32 product of the same whole numbers is exact
+    import torch
+    M, N, K = (8200, 16401, 48) if dtype == "bf16" else (4100, 16401, 48)
+    a, b = _dev(_int8(M, K, 19)), _dev(_int8(N, K, 20))
+    one = lambda n: torch.ones(n, device="cuda:0")  # noqa: E731
+    y = tw.twell_int8_matmul(a, one(M), b, one(N), dtype=torch_dtype(dtype))
+    assert y.numel() * y.element_size() > 256 << 20
+    assert torch.equal(y, (a.float() @ b.float().t()).to(y.dtype))
+
+
 def test_output_beyond_32_bit_offsets():
     # y rows 2^31 elements apart
     import torch

@@ -195,6 +195,46 @@ def test_row_strides_and_alignment(dtype, d, ld, off):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [3, 4, 5, 8, 9, 15, 255, 257, 511, 513, 1023, 1025, 2047, 2049, 4095, 4097, 8191, 8193,
+                               16383, 16385, 32767, 65535])
+def test_unaligned_rows_of_every_length(dtype, d):
+    # rows one element apart in a buffer of NaN, so at every alignment, ending
+    # before, at and behind each edge of a lane's, a wave's and a workgroup's
+    # part: nothing around a row may reach its results or change.  The outputs
+    # lie over inputs.
+    import torch
+    if dtype == "f32" and d > 32768:
+        pytest.skip("longer than an fp32 row may be")
+    T = 5
+    x, res, w = _data(T, d, dtype, 31), _data(T, d, dtype, 32), _weight(d, dtype, 33)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+
+    def apart(a):
+        buf = torch.full((T * (d + 1) + 1,), float("nan"), dtype=dt, device="cuda:0")
+        view = buf[1:].view(T, d + 1)[:, :d]
+        view.copy_(to_dev(a, dtype))
+        return buf, view
+
+    wd = apart(np.repeat(w[None], T, 0))[1][1]
+    q, scale = tw.twell_quantize_rows(apart(x)[1])
+    assert_bitwise(q.cpu().numpy(), quantize_rows(x, dtype)[0], "q of the quantiser")
+    (xb, xd), (rb, rd) = apart(x), apart(res)
+    out = tw.twell_rmsnorm(xd, wd, EPS, rd, quantize=True, h=rd, y=xd)
+    _check_norm(out, x, res, w, dtype, True)
+    dy, dh = _data(T, d, dtype, 34), _data(T, d, dtype, 35)
+    h = residual_sum(x, res, dtype)
+    dx64, dw64 = rmsnorm_backward(dy, h, w, EPS, dtype, dh)
+    bx, bw = _bounds_backward(dy, h, w, dh, dtype)
+    for over in ("dh", "dy"):
+        (yb, yd), (gb, gd) = apart(dy), apart(dh)
+        dx, dw = tw.twell_rmsnorm_backward(yd, rd, wd, EPS, dh=gd, dx=gd if over == "dh" else yd)
+        _close(decode(from_dev(dx.contiguous(), dtype), dtype), dx64, bx, dtype, f"dx over {over}")
+        assert np.all(np.abs(dw.cpu().numpy() - dw64) <= bw)
+        for buf in (xb, rb, yb, gb):
+            assert bool(buf[::d + 1].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [200, 4100])
 def test_outputs_over_inputs(dtype, d):
     T = 21
