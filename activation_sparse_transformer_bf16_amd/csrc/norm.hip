@@ -390,7 +390,8 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
 // bf16 8192 x 2048 with dh: 24.7 us (134 MB, 5.4 TB/s) and 4 us for the sums;
 // 16384 x 4096 89 us (6.0 TB/s).  Two waves a row and two chunks a lane leave
 // room to load the next row ahead (1 us); one wave with four chunks spills
-// (40 us), 512 workgroups write twice the partial rows (28 us).
+// (40 us), 512 workgroups write twice the partial rows (28 us), 192 or 128 leave
+// CUs idle (from memory 32.6 and 34.9 against 28.8 us, both kernels).
 constexpr int BACK_WAVES = 16;
 template <Dt D, int W, int NC, Rows R>
 __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardArgs a) {
