@@ -658,6 +658,11 @@ class RmsNormOut(NamedTuple):
 # 2-5 us: the checks below compare first and word the error only when one
 # fails, and outputs made here are not checked again.
 
+# Sizes are 32-bit in the library, and ctypes passes the low 32 bits of a larger
+# number: one that does not fit has to be refused here.
+_MAX_SIZE = (1 << 31) - 1
+
+
 def _bad_rows(t, name, device, dtype, shape):
     """The error of the first check that a 2-D operand fails."""
     if t is None:
@@ -668,6 +673,8 @@ def _bad_rows(t, name, device, dtype, shape):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if max(shape) > _MAX_SIZE:
+        raise ValueError(f"{name}: sizes of {tuple(shape)} exceed {_MAX_SIZE}")
     raise ValueError(f"{name} must have unit stride along its rows")
 
 
@@ -676,6 +683,8 @@ def _rows(t, name, device, dtype, shape) -> int:
     if t is None or t.dtype != dtype or t.device != device or not t.is_cuda or t.shape != shape:
         _bad_rows(t, name, device, dtype, shape)
     rows, cols = shape
+    if rows > _MAX_SIZE or cols > _MAX_SIZE:
+        _bad_rows(t, name, device, dtype, shape)
     if rows == 0:
         return cols
     across, along = t.stride()
@@ -769,6 +778,9 @@ def twell_rmsnorm(x, weight, eps: float = 1e-6, residual=None, quantize: bool = 
 
 @functools.lru_cache(maxsize=4096)
 def twell_rmsnorm_backward_workspace_size(rows: int, d: int, dtype) -> int:
+    """Bytes of the gradient's workspace; 0 for sizes that it does not take."""
+    if max(rows, d) > _MAX_SIZE:
+        return 0
     return int(_lib.twell_rmsnorm_backward_workspace_size(rows, d, _dtype_code(dtype)))
 
 
@@ -828,6 +840,9 @@ def twell_quantize_rows(x, q=None, scale=None):
 
 @functools.lru_cache(maxsize=4096)
 def twell_int8_matmul_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of the product's workspace; 0 where it needs none, and for sizes that it does not take."""
+    if max(M, N, K) > _MAX_SIZE:
+        return 0
     return int(_lib.twell_int8_matmul_workspace_size(M, N, K))
 
 
