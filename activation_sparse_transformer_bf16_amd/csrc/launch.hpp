@@ -300,6 +300,7 @@ struct NormArgs {
   int8_t *q;             // or null
   int64_t ld_q;
   float *scale;          // [rows] with q
+  float unit = 1.0f;     // set by norm_rows: the factor on the squares
 };
 // A row is held in registers: at most NORM_MAX_CHUNKS chunks of 64 lanes x 16 bytes.
 constexpr int NORM_MAX_CHUNKS = 128;
@@ -326,6 +327,7 @@ struct NormBackwardArgs {
   float *dweight;        // [d]
   float *partial;        // [n_partial][d]
   int n_partial;         // norm_backward_partials(): the workgroups of the row kernel
+  float unit = 1.0f;     // set by norm_backward: the factor on the squares and on g h
 };
 constexpr int NORM_BACKWARD_WGS = 256;
 int norm_backward_partials(int rows, int d, Dt dt);

@@ -283,6 +283,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
   const int first = ((wave % W) * 64 + lane) * E;  // the lane's element of chunk 0
   constexpr int STEP = W * 64 * E;
   const Row<D, R> weight(a.weight, 0, 0, d);
+  const float count = (float)d * a.unit;
   int turn = 0;
   for (int64_t t0 = (int64_t)blockIdx.x * RB; t0 < a.rows; t0 += (int64_t)gridDim.x * RB) {
     const int64_t t = t0 + wave / W;
@@ -326,7 +327,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
         unpack<D>(hv[c], u);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          if (NORM) ss += u[i] * u[i];
+          if (NORM) ss += u[i] * a.unit * u[i];
           z[i] = u[i];
         }
         if (a.q != nullptr) {
@@ -349,7 +350,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
       keep_packed(hv[c]);
       if constexpr (HOLD) keep_packed(wv[c]);
     }
-    const float r = NORM ? rsqrtf(s.a / (float)d + a.eps) : 1.0f;
+    const float r = NORM ? rsqrtf(s.a / count + a.eps) : 1.0f;
     const bool bad = s.top >= INF_BITS;
     const float m = fmaxf(__uint_as_float(s.top), Q_TINY);
     const float inv = Q_MAX / m;
@@ -382,10 +383,12 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
 // Gradient: a workgroup of 16 waves walks groups of RB = 16 / W rows, its
 // own, + grid, ...; each wave keeps its columns' dw sums in registers over all
 // its rows, the workgroup adds its row groups in order and writes one row of
-// partial sums.  The weight is held in registers where it fits, and loaded for each
-// row where it does not; with eight chunks per lane the registers hold no sums
-// either: the workgroup, which then takes one row at a time, adds each row to
-// its partial row in memory (every element by the one lane that owns it).
+// partial sums.  The weight is held in registers where it fits (with four chunks
+// per lane beside whole rows only, whose ends take no registers: 2000 x 12287 fp32
+// 154 us, held 200), and loaded for each row where it does not; with eight chunks
+// per lane the registers hold no sums either: the workgroup, which then takes one
+// row at a time, adds each row to its partial row in memory (every element by the
+// one lane that owns it).
 //
 // bf16 8192 x 2048 with dh: 24.7 us (134 MB, 5.4 TB/s) and 4 us for the sums;
 // 16384 x 4096 89 us (6.0 TB/s).  Two waves a row and two chunks a lane leave
@@ -398,7 +401,7 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
   constexpr int E = 16 / DtT<D>::size;
   constexpr int RB = BACK_WAVES / W;
   constexpr bool HOLD = NC <= 4;         // the sums
-  constexpr bool HOLD_W = NC * E <= 16;  // the weight
+  constexpr bool HOLD_W = NC * E <= 16 && (NC <= 2 || R == Rows::WHOLE);  // the weight
   static_assert(HOLD || RB == 1, "sums in memory: one row per workgroup at a time");
   __shared__ RowSums sums[2][BACK_WAVES];
   const int lane = threadIdx.x & 63;
@@ -408,6 +411,7 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
   constexpr int STEP = W * 64 * E;
   float *out = a.partial + (size_t)blockIdx.x * d;
   const Row<D, R> weight(a.weight, 0, 0, d);
+  const float count = (float)d * a.unit;
   u32x4_t wv[HOLD_W ? NC : 1];
   float dw[HOLD ? NC : 1][E];
   if constexpr (HOLD_W) {
@@ -470,8 +474,8 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
         unpack<D>(HOLD_W ? wv[c] : weight.trim(weight.load(first + c * STEP), first + c * STEP), w);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          ss += h[i] * h[i];
-          dot += g[i] * w[i] * h[i];
+          ss += h[i] * a.unit * h[i];
+          dot += g[i] * w[i] * a.unit * h[i];
         }
       }
     }
@@ -484,8 +488,8 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardA
         keep_packed(gc[c]);
         if constexpr (HOLD_W) keep_packed(wv[c]);
       }
-      const float r = rsqrtf(s.a / (float)d + a.eps);
-      const float k = r * r * (s.b / (float)d);
+      const float r = rsqrtf(s.a / count + a.eps);
+      const float k = r * (r * (s.b / count));  // r^2 alone can leave the range of fp32
       const Row<D, R, true> dh(a.dh, t, a.ld_dh, d), dx(a.dx, t, a.ld_dx, d);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -612,8 +616,22 @@ static hipError_t norm_rows_dt(const NormArgs &a, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-hipError_t norm_rows(const NormArgs &a, hipStream_t s) {
-  if (a.rows <= 0) return hipSuccess;
+// The factor on the terms of a row's sums (the squares, and g h), so that a sum
+// stays below 2^128 where its mean does: the power of two at or below 1 / d, which
+// rounds nothing.  But a term below 2^-126 d loses digits to it, and one below
+// 2^-149 d is lost, which counts only beside an eps as small as that: there the
+// terms stay as they are.
+static float norm_unit(int d, float eps) {
+  float unit = 1.0f;
+  if (eps >= 0x1p-100f)
+    while (unit * (float)d > 1.0f) unit *= 0.5f;
+  return unit;
+}
+
+hipError_t norm_rows(const NormArgs &args, hipStream_t s) {
+  if (args.rows <= 0) return hipSuccess;
+  NormArgs a = args;
+  a.unit = norm_unit(a.d, a.eps);
   if (a.weight != nullptr)
     return a.dtype == Dt::BF16 ? norm_rows_dt<Dt::BF16, true>(a, s) : norm_rows_dt<Dt::F32, true>(a, s);
   return a.dtype == Dt::BF16 ? norm_rows_dt<Dt::BF16, false>(a, s) : norm_rows_dt<Dt::F32, false>(a, s);
@@ -659,6 +677,7 @@ int norm_backward_partials(int rows, int d, Dt dt) {
 hipError_t norm_backward(const NormBackwardArgs &args, hipStream_t s) {
   // one workgroup writes dweight itself (zeros with no rows)
   NormBackwardArgs a = args;
+  a.unit = norm_unit(a.d, a.eps);
   if (a.n_partial == 1) a.partial = a.dweight;
   hipError_t e = a.dtype == Dt::BF16 ? backward_dt<Dt::BF16>(a, s) : backward_dt<Dt::F32>(a, s);
   if (e != hipSuccess || a.n_partial == 1) return e;

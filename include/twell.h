@@ -517,8 +517,11 @@ typedef struct {
  *     q_tj = round-to-even(z_tj * (127 / m_t)),  scale_t = r_t * (m_t / 127).
  * q does not depend on r (it cancels), so it is the same to the bit for any
  * order of the sum.  A row with an infinite or NaN z gets q = 0 and scale NaN.
- * Sums are fp32 (the mean square has to stay below 2^128); the norm is of the
- * stored (rounded) h, which is what twell_rmsnorm_backward takes.
+ * Sums are fp32; the norm is of the stored (rounded) h, which is what
+ * twell_rmsnorm_backward takes.  Range: a row whose mean square is 2^128 or more
+ * counts as infinite (r = 0, so y and scale are 0).  With an eps below 2^-100 it is
+ * the sum of the squares that has to stay below 2^128, and their mean at least
+ * 2^-120; with eps = 0 a row of zeros is 0/0 (y NaN, q 0, scale infinite).
  * h, y and q are each optional (NULL: not written), but one of them is needed.
  * h and y may be x or residual themselves (same address and stride): each row
  * is read whole before any of it is written.
@@ -539,7 +542,9 @@ twell_status twell_rmsnorm(const void *x, int64_t ld_x, const void *residual, in
  * dh: the gradient that reaches h along the residual stream, or NULL for none.
  * dx is the gradient of h, and so of x and of the residual alike.  dx may be
  * dy or dh itself (same address and stride).  dweight [d] fp32, overwritten
- * (zeros with rows == 0).  Sums run in a fixed order (deterministic).
+ * (zeros with rows == 0).  Sums run in a fixed order (deterministic).  Range: as
+ * twell_rmsnorm; |dy_tj h_tj| and the row's mean of |dy w h| have to stay below
+ * 2^128 too (the sum of them, with an eps below 2^-100).
  * workspace: >= twell_rmsnorm_backward_workspace_size() bytes, 256-byte
  * aligned (at most 256 rows of d floats).
  * Errors: as twell_rmsnorm, WORKSPACE.
