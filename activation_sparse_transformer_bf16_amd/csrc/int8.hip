@@ -25,7 +25,6 @@
 namespace twell {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
-typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
 // The scaled value of one sum.
 __device__ __forceinline__ float scaled(int acc, float sa, float sb, float bias) {

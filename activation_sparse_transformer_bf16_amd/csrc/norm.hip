@@ -59,6 +59,12 @@ enum class Rows {
 // gradient does not gain, 51.8 -> 55.7), and the gradient stores them without
 // it (16384 x 4095 fp32: 195 -> 168 us; the norm does not gain).
 constexpr int NON_TEMPORAL = 2;
+
+// The offset stays 32-bit and apart from the row's address, which is in scalar
+// registers: the compiler otherwise adds the two first and keeps a 64-bit address
+// per access (up to 19 more vector registers, and spills).
+__device__ __forceinline__ void keep_offset(uint32_t &at) { asm volatile("" : "+v"(at)); }
+
 typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
 template <Dt D, Rows R, bool NT = false>
 struct Row {
@@ -79,7 +85,7 @@ struct Row {
     } else if constexpr (R == Rows::ANY) {
       if (__builtin_amdgcn_readfirstlane(e0) >= d) return u32x4_t{0u, 0u, 0u, 0u};  // nothing for this wave
       uint32_t at = min((uint32_t)e0, (uint32_t)(d - E)) * (uint32_t)sizeof(T);
-      asm volatile("" : "+v"(at));
+      keep_offset(at);
       const u32x4_any_t *q = reinterpret_cast<const u32x4_any_t *>(reinterpret_cast<const char *>(p) + at);
       if constexpr (NT)
         return __builtin_nontemporal_load(q);
@@ -126,7 +132,7 @@ struct Row {
       __builtin_amdgcn_raw_buffer_store_b128(w, rsrc, e0 * (int)sizeof(T), 0, NON_TEMPORAL);
     } else if (R == Rows::ANY && e0 + E <= d) {
       uint32_t at = (uint32_t)e0 * (uint32_t)sizeof(T);
-      asm volatile("" : "+v"(at));
+      keep_offset(at);
       u32x4_any_t *q = reinterpret_cast<u32x4_any_t *>(reinterpret_cast<char *>(p) + at);
       if constexpr (NTS)
         __builtin_nontemporal_store(w, q);
