@@ -214,17 +214,20 @@ struct I8Tile {
 // multiplied the next slab's lower half, each b fragment after its last use;
 // the copies for the slab STAGES ahead go out between the products.
 //
-// Measured (256 x 256 tiles, Gaussian operands, back to back): 8192 x 8192 x
-// 2048 127-131 us, 2.1 POP/s; 8192^3 413 us, 2.66 POP/s; 16384 x 14336 x 4096
-// 762 us, 2.5 POP/s, against 2.0 POP/s of the library's 8-bit product at
-// 8192^3 and 5 POP/s of the specification.  The power of the chip bounds it:
-// operands of zeros take 103, 315 and 597 us.  By parts, at 8192^3 with random
-// operands and 32 x 32 x 32 products: registers only 3.4 POP/s, with the
-// fragment reads 3.0, with the copies into LDS 2.4; the 16 x 16 x 64 form then
-// gained 10%.  The results' stores cost the rest (8192 x 8192 x 2048: 110 us
-// without them); a persistent workgroup that starts the next tile's copies
-// before them gains nothing, nor do 128 x 128 wave tiles on four waves
-// (accumulators in AGPRs, 583 us at 8192^3).
+// Measured (256 x 256 tiles, Gaussian operands, back to back over the same
+// buffers): 8192 x 8192 x 2048 127-131 us, 2.1 POP/s (132-140 over buffers in turn
+// or all in memory; fp32 results, all in memory, 171); 8192^3 413 us, 2.66 POP/s;
+// 16384 x 14336 x 4096 762-783 us, 2.5 POP/s (fp32 results 828), against 2.0 POP/s
+// of the library's 8-bit product at 8192^3, 3.95 from registers alone and 5 of the
+// specification.  Two things bound it.  The power of the chip: operands of zeros
+// take 103, 315 and 597 us; by parts, at 8192^3 with random operands and 32 x 32 x 32
+// products, registers only 3.4 POP/s, with the fragment reads 3.0, with the copies
+// into LDS 2.4; the 16 x 16 x 64 form then gained 10%.  And what each tile spends
+// before its first and after its last product, which a short K does not hide: with
+// zeros 2.67 POP/s at K = 2048, 3.49 at 8192; the results' stores alone are 20 us of
+// 8192 x 8192 x 2048 (110 us without them).  A persistent workgroup that starts the
+// next tile's copies before them gains nothing, nor do 128 x 128 wave tiles on four
+// waves (accumulators in AGPRs, 583 us at 8192^3).
 // STREAM: the results are stored non-temporally (a template, as the compiler
 // joins the two kinds of store into the ordinary one under a run-time choice).
 template <Dt D, class Cfg, int BN, bool STREAM>

@@ -18,6 +18,9 @@
 // stores (NC chunks of 16 bytes per lane, in storage bits), so every input is
 // read and every output written once; an output may be the same buffer as an
 // input of the same row, since all of a row's loads come before its stores.
+// Above 32 KB a row the registers do not hold everything in each variant, and some
+// of it goes through scratch; which variants, and their times, is said at each
+// kernel.
 #include "launch.hpp"
 
 namespace twell {
@@ -274,9 +277,17 @@ constexpr int row_waves(int W) { return W > 4 ? W : 4; }
 // the plain quantiser (h = x, no weight, r = 1).  With eight chunks per lane
 // the weight is loaded again where it is used instead of being held.
 //
-// Memory bound: bf16 8192 x 2048 with residual and 8 bits 23.5 us (151 MB, 6.4
-// TB/s; a plain copy of the card moves 6.1-6.3), the quantiser of 8192 x 8192
-// 32.5 us (201 MB, 6.2 TB/s); one row 2.3 us, launch and one round trip.
+// Memory bound: bf16 8192 x 2048 with residual and 8 bits 23.7 us over three sets
+// of operands in turn (151 MB, 6.4 TB/s; a plain copy of the card moves 6.1-6.3),
+// 28.2 with all of them in memory, the quantiser of 8192 x 8192 32.8 us (201 MB, 6.1
+// TB/s); one row 2.1 us, launch and one round trip.
+//
+// Long rows with residual, all in memory (us): 2000 x 12288 fp32 70, 2000 x 24576
+// bf16 73, 1000 x 24576 fp32 73 (393 MB, 5.4 TB/s each), 1000 x 40000 bf16 63 (320 MB,
+// 5.1).  Rows of no alignment need registers for their ends, and beyond 64 KB (16
+// waves, 8 chunks) 97 to 139 of them are spilled, in the quantiser 20 to 61: 1000 x
+// 39999 bf16 212, 1000 x 24575 fp32 185 (quantiser 85 and 38, whole rows 23 and 22).
+// Of 32 to 64 KB only bf16 spills (24): 2000 x 24575 138 us, 2000 x 12287 fp32 79.
 template <Dt D, int W, int NC, Rows R, bool NORM>
 __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
   constexpr int E = 16 / DtT<D>::size;
@@ -396,11 +407,23 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
 // row at a time, adds each row to its partial row in memory (every element by the
 // one lane that owns it).
 //
-// bf16 8192 x 2048 with dh: 24.7 us (134 MB, 5.4 TB/s) and 4 us for the sums;
-// 16384 x 4096 89 us (6.0 TB/s).  Two waves a row and two chunks a lane leave
-// room to load the next row ahead (1 us); one wave with four chunks spills
-// (40 us), 512 workgroups write twice the partial rows (28 us), 192 or 128 leave
-// CUs idle (from memory 32.6 and 34.9 against 28.8 us, both kernels).
+// bf16 8192 x 2048 with dh: 26.0 us (134 MB, 5.2 TB/s) and 4 us for the sums, both
+// together back to back 27.8; 16384 x 4096 89 us (6.0 TB/s).  Two waves a row and
+// two chunks a lane leave room to load the next row ahead (1 us); one wave with
+// four chunks spills (40 us), 512 workgroups write twice the partial rows (28 us),
+// 192 or 128 leave CUs idle (from memory 32.6 and 34.9 against 28.8 us, both kernels).
+//
+// Away from that shape, bf16 with dh, both kernels, all in memory (us, and the bytes'
+// time at 6.2 TB/s): 64 x 2048 8.3 (0.2) and 300 x 2048 8.9 (0.8): two launches, and
+// groups of rows for 8 and 38 of the 256 CUs; 1024 x 4096 13.1 (5.4); 4096 x 5120 39
+// (27), 2000 x 8192 31 (21), 1000 x 14336 38 (18), 500 x 16000 31 (10): the 256 partial
+// rows, 16 to 33 MB written and read again, beside 64 to 168 MB of rows.
+//
+// Above 32 KB a row registers are spilled in every variant: 18 to 84 with four
+// chunks per lane, 117 to 376 with eight, more for rows of no alignment.  2000 x
+// 12288 fp32 93 (63), 12287 154; 2000 x 24576 bf16 114 (63), 24575 261; 1000 x 24576
+// fp32 265 (63), 24575 459; 1000 x 40000 bf16 409 (52), 39999 690: there the sums in
+// memory are read and written for each row as well.
 constexpr int BACK_WAVES = 16;
 template <Dt D, int W, int NC, Rows R>
 __global__ __launch_bounds__(64 * BACK_WAVES) void k_norm_backward(NormBackwardArgs a) {

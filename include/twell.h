@@ -489,8 +489,8 @@ twell_status twell_ffn_backward(const twell_hybrid *h, const void *x, const void
  * They take any sizes and row strides: ld_* is a row's distance from the next
  * in ELEMENTS, at least its length; rows are [rows][d] with unit stride along
  * d.  Buffers need the alignment of their element type only; the norm and its
- * gradient are up to a fifth faster on rows that are 16-byte aligned (base,
- * stride and length).  The general rules
+ * gradient are about a fifth faster on rows that are 16-byte aligned (base, stride
+ * and length), and up to three times on rows of more than 32 KB.  The general rules
  * above (streams, no allocation, host validation) apply, but not their limits
  * on d and F and their 16-byte alignment.
  *
