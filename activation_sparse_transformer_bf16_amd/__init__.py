@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 from typing import NamedTuple, Optional, Tuple
 
@@ -61,6 +62,35 @@ class TwellInt8C(ctypes.Structure):
     ]
 
 
+class TwellMx4C(ctypes.Structure):
+    """Mirror of ``twell_mx4`` (include/twell.h)."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("ld", ctypes.c_int64), ("q", ctypes.c_void_p),
+        ("ld_scale", ctypes.c_int64), ("scale", ctypes.c_void_p), ("factor", ctypes.c_void_p),
+    ]
+
+
+class TwellAdamWTensorC(ctypes.Structure):
+    """Mirror of ``twell_adamw_tensor`` (include/twell.h)."""
+
+    _fields_ = [
+        ("n", ctypes.c_int64), ("weight", ctypes.c_void_p), ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+        ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int), ("weight_decay", ctypes.c_float),
+    ]
+
+
+class TwellAdamWC(ctypes.Structure):
+    """Mirror of ``twell_adamw`` (include/twell.h)."""
+
+    _fields_ = [
+        ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint64), ("lr_device", ctypes.c_void_p),
+        ("step_device", ctypes.c_void_p),
+    ]
+
+
 class TwellError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{message} (status {status})")
@@ -82,6 +112,7 @@ def _load():
     P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     L, R = ctypes.c_int64, ctypes.c_float
     M, Q = ctypes.POINTER(TwellMatrixC), ctypes.POINTER(TwellInt8C)
+    X = ctypes.POINTER(TwellMx4C)
     sig = {
         "twell_abi_version": (I, []),
         "twell_status_str": (ctypes.c_char_p, [I]),
@@ -113,6 +144,15 @@ def _load():
         "twell_quantize_rows": (I, [P, L, I, Q, P]),
         "twell_int8_matmul_workspace_size": (Z, [I, I, I]),
         "twell_int8_matmul": (I, [Q, Q, P, I, P, L, P, Z, P]),
+        "twell_quantize_mx4": (I, [P, L, I, X, P]),
+        "twell_dequantize_mx4": (I, [X, I, P, L, P]),
+        "twell_rmsnorm_mx4": (I, [P, L, P, L, P, R, I, I, I, P, L, P, L, X, P]),
+        "twell_mx4_matmul_workspace_size": (Z, [I, I, I]),
+        "twell_mx4_matmul": (I, [X, X, P, I, P, L, P, Z, P]),
+        "twell_grad_norm_workspace_size": (Z, [P, I]),
+        "twell_grad_norm": (I, [P, I, R, P, P, Z, P]),
+        "twell_adamw_step": (I, [P, I, ctypes.POINTER(TwellAdamWC), P, P]),
+        "twell_adamw_states": (I, [P, I, I, P, P, P]),
     }
     # Private function objects: changing argtypes on the public handle (lib())
     # cannot make this binding pass truncated pointers.
@@ -136,7 +176,8 @@ _lib = _Fns(_private)
 import torch as _t  # noqa: E402  (loaded by _load, before the library)
 
 _torch_c = _t._C
-_INT8, _FLOAT32, _BFLOAT16 = _t.int8, _t.float32, _t.bfloat16
+_INT8, _UINT8, _INT64 = _t.int8, _t.uint8, _t.int64
+_FLOAT32, _BFLOAT16 = _t.float32, _t.bfloat16
 _CODES = {_FLOAT32: TWELL_F32, _BFLOAT16: TWELL_BF16}
 _CONTIGUOUS = _t.contiguous_format
 
@@ -150,7 +191,10 @@ EXPORTS = ("twell_abi_version", "twell_status_str", "twell_last_error", "twell_p
            "twell_stream_probe", "twell_mfma_probe", "twell_ffn_forward_noalloc", "twell_sparse_ffn_grouped",
            "twell_sparse_ffn_grouped_workspace_size",
            "twell_rmsnorm", "twell_rmsnorm_backward_workspace_size", "twell_rmsnorm_backward",
-           "twell_quantize_rows", "twell_int8_matmul_workspace_size", "twell_int8_matmul")
+           "twell_quantize_rows", "twell_int8_matmul_workspace_size", "twell_int8_matmul",
+           "twell_quantize_mx4", "twell_dequantize_mx4", "twell_rmsnorm_mx4", "twell_mx4_matmul_workspace_size",
+           "twell_mx4_matmul", "twell_grad_norm_workspace_size", "twell_grad_norm", "twell_adamw_step",
+           "twell_adamw_states")
 
 # Size of the static device scratch behind twell_ffn_forward_noalloc
 # (TWELL_NOALLOC_SCRATCH_BYTES in include/twell.h).
@@ -875,6 +919,369 @@ def twell_int8_matmul(a, a_scale, b, b_scale, row_bias=None, dtype=None, y=None,
     if st:
         _check(st)
     return y
+
+
+# --------------------------------------------------------------------------- microscaled rows
+
+def _launch(device, fn, *args):
+    """Calls an entry point on the device's current stream, with the device current."""
+    if _torch_c._cuda_getDevice() == device.index:
+        st = fn(*args, _raw_stream(device))
+    else:
+        with _t.cuda.device(device):
+            st = fn(*args, _raw_stream(device))
+    if st:
+        _check(st)
+
+
+class Mx4Rows(NamedTuple):
+    """Rows of microscaled 4-bit floats (``twell_mx4`` in include/twell.h), as
+    ``twell_quantize_mx4`` lays them out; a row slice of each tensor is one of
+    fewer rows."""
+
+    q: object              # uint8 [rows, ceil(cols / 2)], rows 16-byte aligned
+    scale: object          # uint8 [rows, ceil(cols / 32) rounded up to 16]
+    cols: int
+    factor: object = None  # float32 [rows] or None
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device, factor: bool = False) -> "Mx4Rows":
+        ld, lds = _mx4_strides(cols)
+        q = _t.empty((rows, ld), dtype=_UINT8, device=device)
+        n = (cols + 1) // 2
+        return cls(q if n == ld else q[:, :n], _t.empty((rows, lds), dtype=_UINT8, device=device), cols,
+                   _t.empty((rows,), dtype=_FLOAT32, device=device) if factor else None)
+
+
+def _mx4_strides(cols):
+    return (cols + 31) // 32 * 16, (cols + 511) // 512 * 16
+
+
+def _new_mx4(x, factor):
+    """Rows for those of x, and their descriptor."""
+    rows, cols = x.shape
+    ld, lds = _mx4_strides(cols)
+    q = x.new_empty((rows, ld), dtype=_UINT8)
+    scale = x.new_empty((rows, lds), dtype=_UINT8)
+    f = x.new_empty((rows,), dtype=_FLOAT32) if factor else None
+    desc = TwellMx4C(rows, cols, ld, q.data_ptr(), lds, scale.data_ptr(), None if f is None else f.data_ptr())
+    n = (cols + 1) // 2
+    return Mx4Rows(q if n == ld else q[:, :n], scale, cols, f), desc
+
+
+def _mx4_rows(r, name, device, shape) -> TwellMx4C:
+    """The descriptor of 4-bit rows given as tensors: every row 16-byte aligned,
+    with its last 16-byte chunk inside the tensor's storage."""
+    if not isinstance(r, Mx4Rows):
+        raise TypeError(f"{name} must be Mx4Rows, got {type(r).__name__}")
+    rows, cols = shape
+    if r.cols != cols or cols <= 0:
+        raise ValueError(f"{name} must have {cols} columns (at least 1), got {r.cols}")
+    if cols > _MAX_SIZE:
+        raise ValueError(f"{name}: {cols} columns exceed {_MAX_SIZE}")
+    n, (wide, lds) = (cols + 1) // 2, _mx4_strides(cols)
+    ld = _rows(r.q, f"{name}.q", device, _UINT8, (rows, n))
+    ld_scale = _rows(r.scale, f"{name}.scale", device, _UINT8, (rows, lds))
+    fp = None if r.factor is None else _vec(r.factor, f"{name}.factor", device, _FLOAT32, rows)
+    if rows <= 1:
+        ld, ld_scale = wide, lds
+    elif ld % 16 or ld_scale % 16:
+        raise ValueError(f"{name}: row strides {ld} and {ld_scale} are not multiples of 16 (lay rows out as "
+                         "twell_quantize_mx4 does)")
+    end = (n + 15) // 16 * 16
+    if end != n and rows and r.q.storage_offset() + (rows - 1) * ld + end > r.q.untyped_storage().nbytes():
+        raise ValueError(f"{name}: the last row's 16-byte chunks run past the tensor's storage")
+    return TwellMx4C(rows, cols, ld, r.q.data_ptr(), ld_scale, r.scale.data_ptr(), fp)
+
+
+def twell_quantize_mx4(x, out: Optional[Mx4Rows] = None) -> Mx4Rows:
+    """Rows of x [rows, cols] in microscaled 4-bit floats."""
+    device, dtype, shape = x.device, x.dtype, x.shape
+    code = _CODES[dtype] if dtype in _CODES else _dtype_code(dtype)
+    if len(shape) != 2:
+        raise ValueError(f"x must be 2-D [rows, cols], got shape {tuple(shape)}")
+    ld_x = _rows(x, "x", device, dtype, shape)
+    if out is None:
+        out, desc = _new_mx4(x, False)
+    else:
+        desc = _mx4_rows(out, "out", device, shape)
+    _launch(device, _lib.twell_quantize_mx4, x.data_ptr(), ld_x, code, desc)
+    return out
+
+
+def twell_dequantize_mx4(rows: Mx4Rows, dtype=None, y=None):
+    """The values of 4-bit rows, [rows, cols] in ``dtype`` (default bfloat16, or
+    that of a given ``y``)."""
+    if not isinstance(rows, Mx4Rows):
+        raise TypeError(f"rows must be Mx4Rows, got {type(rows).__name__}")
+    device = rows.q.device
+    shape = (rows.q.shape[0], rows.cols)
+    desc = _mx4_rows(rows, "rows", device, shape)
+    if dtype is None:
+        dtype = _BFLOAT16 if y is None else y.dtype
+    code = _CODES[dtype] if dtype in _CODES else _dtype_code(dtype)
+    ld_y = shape[1]
+    if y is None:
+        y = rows.q.new_empty(shape, dtype=dtype)
+    else:
+        ld_y = _rows(y, "y", device, dtype, shape)
+    _launch(device, _lib.twell_dequantize_mx4, desc, code, y.data_ptr(), ld_y)
+    return y
+
+
+class RmsNormMx4Out(NamedTuple):
+    """What ``twell_rmsnorm_mx4`` wrote (None: not asked for); ``h`` is x itself without a residual."""
+
+    y: object    # dtype [rows, d]
+    h: object    # dtype [rows, d]
+    q: Mx4Rows   # with a factor per row
+
+
+def twell_rmsnorm_mx4(x, weight, eps: float = 1e-6, residual=None, h=None, y=None, q: Optional[Mx4Rows] = None,
+                      want_y: bool = True) -> RmsNormMx4Out:
+    """``twell_rmsnorm`` with the normed rows in microscaled 4-bit floats.
+
+    x, residual, h, y: [rows, d] with unit stride along d (any row stride).  ``h``
+    and ``y`` may be ``x`` or ``residual`` themselves.  ``want_y=False`` writes the
+    4 bits alone."""
+    device, dtype, shape = x.device, x.dtype, x.shape
+    code = _CODES[dtype] if dtype in _CODES else _dtype_code(dtype)
+    if len(shape) != 2:
+        raise ValueError(f"x must be 2-D [rows, d], got shape {tuple(shape)}")
+    rows, d = shape
+    ld_x = _rows(x, "x", device, dtype, shape)
+    wp = _vec(weight, "weight", device, dtype, d)
+    ld_r = ld_h = ld_y = d
+    rp = hp = yp = None
+    if residual is not None:
+        ld_r = _rows(residual, "residual", device, dtype, shape)
+        rp = residual.data_ptr()
+    if h is not None:
+        ld_h = _rows(h, "h", device, dtype, shape)
+        hp = h.data_ptr()
+    elif residual is not None:
+        h = _t.empty_like(x, memory_format=_CONTIGUOUS)
+        hp = h.data_ptr()
+    if y is not None:
+        ld_y = _rows(y, "y", device, dtype, shape)
+        yp = y.data_ptr()
+    elif want_y:
+        y = _t.empty_like(x, memory_format=_CONTIGUOUS)
+        yp = y.data_ptr()
+    if q is None:
+        q, qd = _new_mx4(x, True)
+    else:
+        qd = _mx4_rows(q, "q", device, shape)
+    _launch(device, _lib.twell_rmsnorm_mx4, x.data_ptr(), ld_x, rp, ld_r, wp, eps, rows, d, code, hp, ld_h, yp, ld_y,
+            qd)
+    return RmsNormMx4Out(y, x if h is None else h, q)
+
+
+@functools.lru_cache(maxsize=4096)
+def twell_mx4_matmul_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of the product's workspace; 0 where it needs none, and for sizes that it does not take."""
+    if max(M, N, K) > _MAX_SIZE:
+        return 0
+    return int(_lib.twell_mx4_matmul_workspace_size(M, N, K))
+
+
+def twell_mx4_matmul(a: Mx4Rows, b: Mx4Rows, row_bias=None, dtype=None, y=None, workspace=None):
+    """y[m, n] = sum_k a[m, k] b[n, k] (+ row_bias[m]) for 4-bit rows a [M, K], b [N, K]
+    with their factors; y [M, N] in ``dtype`` (default bfloat16, or that of a
+    given ``y``)."""
+    if not isinstance(a, Mx4Rows) or not isinstance(b, Mx4Rows):
+        raise TypeError(f"a and b must be Mx4Rows, got {type(a).__name__} and {type(b).__name__}")
+    device = a.q.device
+    M, N, K = a.q.shape[0], b.q.shape[0], a.cols
+    ad = _mx4_rows(a, "a", device, (M, K))
+    bd = _mx4_rows(b, "b", device, (N, K))
+    bp = None if row_bias is None else _vec(row_bias, "row_bias", device, _FLOAT32, M)
+    if dtype is None:
+        dtype = _BFLOAT16 if y is None else y.dtype
+    code = _CODES[dtype] if dtype in _CODES else _dtype_code(dtype)
+    ld_y = N
+    if y is None:
+        y = a.q.new_empty((M, N), dtype=dtype)
+    else:
+        ld_y = _rows(y, "y", device, dtype, (M, N))
+    nbytes = twell_mx4_matmul_workspace_size(M, N, K)
+    ws, wn = None, 0
+    if nbytes:
+        workspace = _workspace(nbytes, device, workspace)
+        ws, wn = workspace.data_ptr(), workspace.numel()
+    _launch(device, _lib.twell_mx4_matmul, ad, bd, bp, code, y.data_ptr(), ld_y, ws, wn)
+    return y
+
+
+# --------------------------------------------------------------------------- the optimiser
+
+@functools.lru_cache(maxsize=64)
+def _adamw_struct(count: int) -> struct.Struct:
+    """A list of ``count`` twell_adamw_tensor."""
+    one = struct.calcsize("@q7P2if") + 4
+    assert one == ctypes.sizeof(TwellAdamWTensorC)
+    return struct.Struct("@" + "q7P2if4x" * count)
+
+
+def _grad_list(grads):
+    """(the C list, device) of gradients alone."""
+    flat = []
+    device = grads[0].device if grads else None
+    for i, g in enumerate(grads):
+        if g.device != device or not g.is_cuda or not g.is_contiguous():
+            _need(g, f"grads[{i}]", device)
+        code = _CODES[g.dtype] if g.dtype in _CODES else _dtype_code(g.dtype)
+        flat += (g.numel(), 0, 0, g.data_ptr(), 0, 0, 0, 0, 0, code, 0.0)
+    return _adamw_struct(len(grads)).pack(*flat), device
+
+
+def twell_grad_norm(grads, max_norm: float = float("inf"), out=None, workspace=None):
+    """The norm of all gradients together and the factor that clips them to
+    ``max_norm``: float32 [2], as ``twell_adamw_step`` takes it for ``clip``."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads is empty")
+    table, device = _grad_list(grads)
+    if out is None:
+        out = _t.empty((2,), dtype=_FLOAT32, device=device)
+    else:
+        _vec(out, "out", device, _FLOAT32, 2)
+    ws = _workspace(int(_lib.twell_grad_norm_workspace_size(table, len(grads))), device, workspace)
+    _launch(device, _lib.twell_grad_norm, table, len(grads), max_norm, out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+class TwellAdamW:
+    """Weights and optimiser states of ``twell_adamw_step``: lists with an entry
+    per weight tensor (``twell_adamw_tensor`` in include/twell.h).
+
+    m, v: float32 like the weights, or uint8 codes [numel] with ``m_scale`` and
+    ``v_scale`` uint8 [ceil(numel / 32)] (None for a tensor with 32-bit states).
+    master: float32 copies of bfloat16 weights, or None (for all, or for a
+    tensor).  weight_decay: one number, or one per tensor."""
+
+    def __init__(self, weights, m, v, m_scale=None, v_scale=None, master=None, weight_decay=0.0):
+        n = len(weights)
+        self.weights, self.m, self.v = list(weights), list(m), list(v)
+        self.m_scale = [None] * n if m_scale is None else list(m_scale)
+        self.v_scale = [None] * n if v_scale is None else list(v_scale)
+        self.master = [None] * n if master is None else list(master)
+        self.weight_decay = ([float(weight_decay)] * n if isinstance(weight_decay, (int, float))
+                             else [float(d) for d in weight_decay])
+        if not n:
+            raise ValueError("no weights")
+        self.device = self.weights[0].device
+        self.validate()
+
+    @classmethod
+    def zeros(cls, weights, bits: int = 32, master: bool = False, weight_decay=0.0) -> "TwellAdamW":
+        """States before the first step, with ``bits`` 32 or 8; ``master``: keep
+        float32 copies of the bfloat16 weights."""
+        if bits not in (8, 32):
+            raise ValueError(f"states have 8 or 32 bits, not {bits}")
+
+        def states():
+            if bits == 32:
+                return [_t.zeros_like(w, dtype=_FLOAT32, memory_format=_CONTIGUOUS) for w in weights]
+            return [_t.zeros((w.numel(),), dtype=_UINT8, device=w.device) for w in weights]
+
+        def scales():
+            if bits == 32:
+                return None
+            return [_t.zeros(((w.numel() + 31) // 32,), dtype=_UINT8, device=w.device) for w in weights]
+
+        copies = [w.detach().float() if w.dtype == _BFLOAT16 else None for w in weights] if master else None
+        return cls(weights, states(), states(), scales(), scales(), copies, weight_decay)
+
+    def validate(self) -> None:
+        """Check every buffer before its pointers reach the library."""
+        n, device = len(self.weights), self.device
+        for name in ("m", "v", "m_scale", "v_scale", "master", "weight_decay"):
+            if len(getattr(self, name)) != n:
+                raise ValueError(f"{name}: {len(getattr(self, name))} entries, {n} weights")
+        for i, w in enumerate(self.weights):
+            _need(w, f"weights[{i}]", device)
+            _dtype_code(w.dtype)
+            if (self.m_scale[i] is None) != (self.v_scale[i] is None):
+                raise ValueError(f"m_scale[{i}] and v_scale[{i}] go together")
+            blocks = ((w.numel() + 31) // 32,)
+            for name in ("m", "v"):
+                scale = getattr(self, f"{name}_scale")[i]
+                if scale is None:
+                    _need(getattr(self, name)[i], f"{name}[{i}]", device, _FLOAT32, w.shape)
+                else:
+                    _need(getattr(self, name)[i], f"{name}[{i}]", device, _UINT8, (w.numel(),))
+                    _need(scale, f"{name}_scale[{i}]", device, _UINT8, blocks)
+            if self.master[i] is not None:
+                if w.dtype == _FLOAT32:
+                    raise ValueError(f"master[{i}]: float32 weights have no float32 copy")
+                _need(self.master[i], f"master[{i}]", device, _FLOAT32, w.shape)
+
+    def c_list(self, grads=None) -> bytes:
+        """The C list with this step's gradients (None: a list for reading the states)."""
+        flat = []
+        for i, w in enumerate(self.weights):
+            gp, gc = 0, 0
+            if grads is not None:
+                g = grads[i]
+                if g is None or g.device != self.device or g.shape != w.shape or not g.is_contiguous():
+                    _need(g, f"grads[{i}]", self.device, None, w.shape)
+                gp, gc = g.data_ptr(), _CODES[g.dtype] if g.dtype in _CODES else _dtype_code(g.dtype)
+            ms, vs, x = self.m_scale[i], self.v_scale[i], self.master[i]
+            flat += (w.numel(), w.data_ptr(), 0 if x is None else x.data_ptr(), gp, self.m[i].data_ptr(),
+                     self.v[i].data_ptr(), 0 if ms is None else ms.data_ptr(), 0 if vs is None else vs.data_ptr(),
+                     _CODES[w.dtype], gc, self.weight_decay[i])
+        return _adamw_struct(len(self.weights)).pack(*flat)
+
+
+def twell_adamw_step(opt: TwellAdamW, grads, lr, step, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                     clip=None, seed: int = 0) -> None:
+    """One AdamW step over all of ``opt``'s tensors, in place, with ``grads``
+    (float32 or bfloat16) like the weights.
+
+    ``step`` counts from 1; it or ``lr`` may be a tensor of one element on the GPU
+    (int64, float32), read when the step runs.  ``clip``: what ``twell_grad_norm``
+    returned (a factor that is not finite leaves the step out).  ``seed``: of the
+    random roundings of 8-bit states and of bfloat16 weights without a copy."""
+    device = opt.device
+    grads = list(grads)
+    if len(grads) != len(opt.weights):
+        raise ValueError(f"{len(grads)} gradients, {len(opt.weights)} weights")
+    table = opt.c_list(grads)
+    lp = sp = cp = None
+    if isinstance(lr, _t.Tensor):
+        lp, lr = _one(lr, "lr", device, _FLOAT32), 0.0
+    if isinstance(step, _t.Tensor):
+        sp, step = _one(step, "step", device, _INT64), 1
+    elif not 1 <= step < 1 << 63:
+        raise ValueError(f"steps count from 1, got {step}")
+    if clip is not None:
+        cp = _vec(clip, "clip", device, _FLOAT32, 2)
+    args = TwellAdamWC(lr, beta1, beta2, eps, step, seed & 0xFFFFFFFFFFFFFFFF, lp, sp)
+    _launch(device, _lib.twell_adamw_step, table, len(grads), args, cp)
+
+
+def _one(t, name, device, dtype) -> int:
+    if t.numel() != 1:
+        raise ValueError(f"{name} must have one element, got {t.numel()}")
+    _need(t, name, device, dtype)
+    return t.data_ptr()
+
+
+def twell_adamw_states(opt: TwellAdamW, dtype=None):
+    """The values of ``opt``'s 8-bit states, (m, v): lists of tensors like the weights
+    in ``dtype`` (default bfloat16, which holds them exactly)."""
+    dtype = _BFLOAT16 if dtype is None else dtype
+    code = _dtype_code(dtype)
+    if any(s is None for s in opt.m_scale):
+        raise ValueError("states of 32 bits need no reading")
+    n = len(opt.weights)
+    m = [_t.empty_like(w, dtype=dtype, memory_format=_CONTIGUOUS) for w in opt.weights]
+    v = [_t.empty_like(w, dtype=dtype, memory_format=_CONTIGUOUS) for w in opt.weights]
+    pointers = ctypes.c_void_p * n
+    _launch(opt.device, _lib.twell_adamw_states, opt.c_list(), n, code, pointers(*[t.data_ptr() for t in m]),
+            pointers(*[t.data_ptr() for t in v]))
+    return m, v
 
 
 def twell_stream_probe(src, dst, mode: int) -> None:

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "launch.hpp"
+#include "mx4.hpp"
 #include "twell.h"
 
 using namespace twell;
@@ -946,6 +947,276 @@ twell_status twell_int8_matmul(const twell_int8 *a, const twell_int8 *b, const f
   Int8Args ia{to_dt(dtype), a->rows, b->rows, a->cols, a->q, a->ld, a->scale, b->q, b->ld, b->scale, row_bias, y,
               ld_y};
   TW_TRY(int8_matmul(ia, workspace, static_cast<hipStream_t>(stream)), "8-bit product");
+  return TWELL_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t ADAMW_MAX_N = (int64_t)1 << 40;
+
+twell_status check_mx4(const char *name, const twell_mx4 *q) {
+  if (q == nullptr) return fail(TWELL_ERR_INVALID_ARG, "null %s", name);
+  if (q->rows < 0 || q->cols <= 0) return fail(TWELL_ERR_INVALID_ARG, "%s: need rows >= 0 and cols > 0", name);
+  const int codes = q->cols / 2 + q->cols % 2, blocks = (q->cols - 1) / MX4_BLOCK + 1;
+  twell_status st = check_rows(name, q->q, q->ld, codes, 1, q->rows);
+  if (st != TWELL_OK) return st;
+  if (q->ld_scale < blocks || q->ld_scale > ((int64_t)1 << 40))
+    return fail(TWELL_ERR_INVALID_ARG, "%s: scale stride %lld with %d blocks a row", name, (long long)q->ld_scale, blocks);
+  if (q->rows > 0 && q->scale == nullptr) return fail(TWELL_ERR_INVALID_ARG, "%s: null scale", name);
+  if (!aligned(q->q, 16) || q->ld % 16 != 0)
+    return fail(TWELL_ERR_UNSUPPORTED, "%s: rows must be 16-byte aligned (base and stride)", name);
+  if (!aligned(q->scale, 16) || q->ld_scale % 16 != 0)
+    return fail(TWELL_ERR_UNSUPPORTED, "%s: rows of scales must be 16-byte aligned (base and stride)", name);
+  if (!aligned(q->factor, 4)) return fail(TWELL_ERR_UNSUPPORTED, "%s: misaligned factor", name);
+  return TWELL_OK;
+}
+
+twell_status check_list(const twell_adamw_tensor *t, int count) {
+  if (count < 0) return fail(TWELL_ERR_INVALID_ARG, "need count >= 0");
+  if (count > 0 && t == nullptr) return fail(TWELL_ERR_INVALID_ARG, "null tensors");
+  for (int i = 0; i < count; ++i) {
+    if (t[i].n < 0) return fail(TWELL_ERR_INVALID_ARG, "tensor %d: negative size", i);
+    if (t[i].n > ADAMW_MAX_N) return fail(TWELL_ERR_UNSUPPORTED, "tensor %d: %lld elements", i, (long long)t[i].n);
+  }
+  return TWELL_OK;
+}
+
+twell_status check_grads(const twell_adamw_tensor *t, int count) {
+  twell_status st = check_list(t, count);
+  for (int i = 0; st == TWELL_OK && i < count; ++i) {
+    if (!valid_dtype((int)t[i].grad_dtype))
+      st = fail(TWELL_ERR_INVALID_ARG, "tensor %d: unknown grad_dtype %d", i, (int)t[i].grad_dtype);
+    else if (t[i].n > 0 && t[i].grad == nullptr)
+      st = fail(TWELL_ERR_INVALID_ARG, "tensor %d: null grad", i);
+    else if (!aligned(t[i].grad, dt_size(t[i].grad_dtype)))
+      st = fail(TWELL_ERR_UNSUPPORTED, "tensor %d: misaligned grad", i);
+  }
+  return st;
+}
+
+twell_status check_states(const twell_adamw_tensor &t, int i) {
+  if ((t.m_scale == nullptr) != (t.v_scale == nullptr))
+    return fail(TWELL_ERR_INVALID_ARG, "tensor %d: m_scale and v_scale go together", i);
+  if (t.n > 0 && (t.m == nullptr || t.v == nullptr)) return fail(TWELL_ERR_INVALID_ARG, "tensor %d: null m or v", i);
+  if (t.m_scale == nullptr && (!aligned(t.m, 4) || !aligned(t.v, 4)))
+    return fail(TWELL_ERR_UNSUPPORTED, "tensor %d: misaligned m or v", i);
+  return TWELL_OK;
+}
+
+// The gradients of tensors i ... in one launch's list; returns how many.
+int grad_batch(const twell_adamw_tensor *t, int i, int count, GradRef (&g)[GRAD_LIST]) {
+  int n = 0;
+  for (; n < GRAD_LIST && i + n < count; ++n) g[n] = GradRef{t[i + n].grad, t[i + n].n, to_dt(t[i + n].grad_dtype)};
+  return n;
+}
+
+size_t grad_norm_ws(const twell_adamw_tensor *t, int count) {
+  size_t wgs = 0;
+  for (int i = 0; i < count;) {
+    GradRef g[GRAD_LIST];
+    const int n = grad_batch(t, i, count, g);
+    wgs += (size_t)grad_wgs(g, n);
+    i += n;
+  }
+  return align_up(std::max<size_t>(wgs, 1) * sizeof(double), ALIGN_WS);
+}
+
+}  // namespace
+
+extern "C" {
+
+twell_status twell_quantize_mx4(const void *x, int64_t ld_x, twell_dtype dtype, const twell_mx4 *out, void *stream) {
+  g_err[0] = 0;
+  twell_status st = check_mx4("out", out);
+  if (st != TWELL_OK) return st;
+  if (!valid_dtype((int)dtype)) return fail(TWELL_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  if (out->factor != nullptr) return fail(TWELL_ERR_INVALID_ARG, "out: the quantiser writes no factor");
+  if ((st = check_rows("x", x, ld_x, out->cols, dt_size(dtype), out->rows)) != TWELL_OK) return st;
+  if (out->rows == 0) return TWELL_OK;
+  Mx4Args a{to_dt(dtype), out->rows, out->cols, x, ld_x, out->q, out->ld, out->scale, out->ld_scale, nullptr, nullptr, 0};
+  TW_TRY(mx4_rows(a, false, static_cast<hipStream_t>(stream)), "4-bit quantiser");
+  return TWELL_OK;
+}
+
+twell_status twell_dequantize_mx4(const twell_mx4 *in, twell_dtype dtype, void *y, int64_t ld_y, void *stream) {
+  g_err[0] = 0;
+  twell_status st = check_mx4("in", in);
+  if (st != TWELL_OK) return st;
+  if (!valid_dtype((int)dtype)) return fail(TWELL_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  if ((st = check_rows("y", y, ld_y, in->cols, dt_size(dtype), in->rows)) != TWELL_OK) return st;
+  if (in->rows == 0) return TWELL_OK;
+  Mx4Args a{to_dt(dtype), in->rows, in->cols, nullptr, 0, in->q, in->ld, in->scale, in->ld_scale, in->factor, y, ld_y};
+  TW_TRY(mx4_rows(a, true, static_cast<hipStream_t>(stream)), "4-bit reader");
+  return TWELL_OK;
+}
+
+twell_status twell_rmsnorm_mx4(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual,
+                               const void *weight, float eps, int rows, int d, twell_dtype dtype, void *h,
+                               int64_t ld_h, void *y, int64_t ld_y, const twell_mx4 *q, void *stream) {
+  g_err[0] = 0;
+  twell_status st = check_norm_shape(rows, d, (int)dtype);
+  if (st != TWELL_OK) return st;
+  if ((st = check_eps(eps)) != TWELL_OK) return st;
+  const int e = dt_size(dtype);
+  if ((st = check_rows("x", x, ld_x, d, e, rows)) != TWELL_OK) return st;
+  if (residual != nullptr && (st = check_rows("residual", residual, ld_residual, d, e, rows)) != TWELL_OK) return st;
+  if (h != nullptr && (st = check_rows("h", h, ld_h, d, e, rows)) != TWELL_OK) return st;
+  if (y != nullptr && (st = check_rows("y", y, ld_y, d, e, rows)) != TWELL_OK) return st;
+  if ((st = check_mx4("q", q)) != TWELL_OK) return st;
+  if (q->rows != rows || q->cols != d)
+    return fail(TWELL_ERR_INVALID_ARG, "q is %d x %d, the rows are %d x %d", q->rows, q->cols, rows, d);
+  if (rows == 0) return TWELL_OK;
+  if (q->factor == nullptr) return fail(TWELL_ERR_INVALID_ARG, "q: null factor");
+  if (weight == nullptr) return fail(TWELL_ERR_INVALID_ARG, "null weight");
+  if (!aligned(weight, e)) return fail(TWELL_ERR_UNSUPPORTED, "misaligned weight");
+  NormArgs a{to_dt(dtype), rows, d, x, ld_x, residual, ld_residual, weight, eps, h, ld_h, y, ld_y, nullptr, 0, nullptr};
+  a.q4 = q->q;
+  a.ld_q4 = q->ld;
+  a.q4_scale = q->scale;
+  a.ld_q4_scale = q->ld_scale;
+  a.q4_factor = q->factor;
+  TW_TRY(norm_rows(a, static_cast<hipStream_t>(stream)), "RMS norm to 4 bits");
+  return TWELL_OK;
+}
+
+size_t twell_mx4_matmul_workspace_size(int M, int N, int K) {
+  return M < 0 || N < 0 || M > MX4_MAX_ROWS || N > MX4_MAX_ROWS || K <= 0 || K > MX4_MAX_K ? 0 : mx4_matmul_workspace(M, N, K);
+}
+
+twell_status twell_mx4_matmul(const twell_mx4 *a, const twell_mx4 *b, const float *row_bias, twell_dtype dtype,
+                              void *y, int64_t ld_y, void *workspace, size_t ws_bytes, void *stream) {
+  g_err[0] = 0;
+  if (!valid_dtype((int)dtype)) return fail(TWELL_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  twell_status st = check_mx4("a", a);
+  if (st != TWELL_OK) return st;
+  if ((st = check_mx4("b", b)) != TWELL_OK) return st;
+  if (a->cols != b->cols) return fail(TWELL_ERR_INVALID_ARG, "a has %d columns, b %d", a->cols, b->cols);
+  if (a->cols > MX4_MAX_K) return fail(TWELL_ERR_UNSUPPORTED, "%d columns not built (at most %d)", a->cols, MX4_MAX_K);
+  if (a->rows > MX4_MAX_ROWS || b->rows > MX4_MAX_ROWS)
+    return fail(TWELL_ERR_UNSUPPORTED, "%d x %d results not built (at most %d each way)", a->rows, b->rows, MX4_MAX_ROWS);
+  if ((st = check_rows("y", y, ld_y, b->rows, dt_size(dtype), a->rows > 0 && b->rows > 0)) != TWELL_OK) return st;
+  if (!aligned(row_bias, 4)) return fail(TWELL_ERR_UNSUPPORTED, "misaligned row_bias");
+  if (a->rows == 0 || b->rows == 0) return TWELL_OK;
+  const size_t need = mx4_matmul_workspace(a->rows, b->rows, a->cols);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need))
+    return fail(TWELL_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? ws_bytes : 0);
+  if (!aligned(workspace, ALIGN_WS)) return fail(TWELL_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
+  Mx4MatmulArgs ma{to_dt(dtype), a->rows, b->rows, a->cols, a->q, a->ld, a->scale, a->ld_scale, a->factor,
+                   b->q, b->ld, b->scale, b->ld_scale, b->factor, row_bias, y, ld_y};
+  TW_TRY(mx4_matmul(ma, workspace, static_cast<hipStream_t>(stream)), "4-bit product");
+  return TWELL_OK;
+}
+
+size_t twell_grad_norm_workspace_size(const twell_adamw_tensor *tensors, int count) {
+  char saved[sizeof(g_err)];
+  memcpy(saved, g_err, sizeof(g_err));
+  const twell_status st = check_list(tensors, count);
+  memcpy(g_err, saved, sizeof(g_err));
+  return st == TWELL_OK ? grad_norm_ws(tensors, count) : 0;
+}
+
+twell_status twell_grad_norm(const twell_adamw_tensor *tensors, int count, float max_norm, float *out,
+                             void *workspace, size_t ws_bytes, void *stream) {
+  g_err[0] = 0;
+  twell_status st = check_grads(tensors, count);
+  if (st != TWELL_OK) return st;
+  if (!(max_norm > 0.0f)) return fail(TWELL_ERR_INVALID_ARG, "max_norm must be > 0");
+  if (out == nullptr) return fail(TWELL_ERR_INVALID_ARG, "null out");
+  if (!aligned(out, 4)) return fail(TWELL_ERR_UNSUPPORTED, "misaligned out");
+  const size_t need = grad_norm_ws(tensors, count);
+  if (workspace == nullptr || ws_bytes < need)
+    return fail(TWELL_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? ws_bytes : 0);
+  if (!aligned(workspace, ALIGN_WS)) return fail(TWELL_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
+  double *partial = static_cast<double *>(workspace);
+  int used = 0;
+  for (int i = 0; i < count;) {
+    GradRef g[GRAD_LIST];
+    const int n = grad_batch(tensors, i, count, g);
+    TW_TRY(grad_squares(g, n, partial + used, static_cast<hipStream_t>(stream)), "gradient squares");
+    used += grad_wgs(g, n);
+    i += n;
+  }
+  TW_TRY(grad_norm(partial, used, max_norm, out, static_cast<hipStream_t>(stream)), "gradient norm");
+  return TWELL_OK;
+}
+
+twell_status twell_adamw_step(const twell_adamw_tensor *tensors, int count, const twell_adamw *args,
+                              const float *clip, void *stream) {
+  g_err[0] = 0;
+  twell_status st = check_grads(tensors, count);
+  if (st != TWELL_OK) return st;
+  if (args == nullptr) return fail(TWELL_ERR_INVALID_ARG, "null args");
+  const twell_adamw &h = *args;
+  if (!(h.lr >= 0.0 && h.lr <= 3.0e38)) return fail(TWELL_ERR_INVALID_ARG, "lr must be finite and >= 0");
+  if (!(h.eps >= 0.0 && h.eps <= 3.0e38)) return fail(TWELL_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!(h.beta1 >= 0.0 && h.beta1 < 1.0 && h.beta2 >= 0.0 && h.beta2 < 1.0))
+    return fail(TWELL_ERR_INVALID_ARG, "betas must lie in [0, 1)");
+  if (h.step_device == nullptr && h.step < 1) return fail(TWELL_ERR_INVALID_ARG, "steps count from 1");
+  if (!aligned(h.lr_device, 4) || !aligned(h.step_device, 8) || !aligned(clip, 4))
+    return fail(TWELL_ERR_UNSUPPORTED, "misaligned lr_device, step_device or clip");
+  for (int i = 0; i < count; ++i) {
+    const twell_adamw_tensor &t = tensors[i];
+    if (!valid_dtype((int)t.dtype)) return fail(TWELL_ERR_INVALID_ARG, "tensor %d: unknown dtype %d", i, (int)t.dtype);
+    if ((st = check_states(t, i)) != TWELL_OK) return st;
+    if (t.n > 0 && t.weight == nullptr) return fail(TWELL_ERR_INVALID_ARG, "tensor %d: null weight", i);
+    if (t.master != nullptr && t.dtype == TWELL_F32)
+      return fail(TWELL_ERR_INVALID_ARG, "tensor %d: an fp32 copy of fp32 weights", i);
+    if (!(t.weight_decay >= -3.0e38f && t.weight_decay <= 3.0e38f))
+      return fail(TWELL_ERR_INVALID_ARG, "tensor %d: weight_decay must be finite", i);
+    if (!aligned(t.weight, dt_size(t.dtype)) || !aligned(t.master, 4))
+      return fail(TWELL_ERR_UNSUPPORTED, "tensor %d: misaligned weight or master", i);
+  }
+  const AdamWArgs a{h.lr, h.beta1, h.beta2, h.eps, h.step, h.seed, h.lr_device, h.step_device, clip};
+  // tensors of one kind share a launch; bits of a kind: bf16 weights, bf16 gradients, 8-bit states, master
+  for (int kind = 0; kind < 16; ++kind) {
+    AdamWTensor list[ADAMW_LIST];
+    int n = 0;
+    for (int i = 0; i <= count; ++i) {
+      if (n == ADAMW_LIST || (i == count && n > 0)) {
+        TW_TRY(adamw_step(list, n, kind & 1 ? Dt::BF16 : Dt::F32, kind & 2 ? Dt::BF16 : Dt::F32, (kind & 4) != 0, a,
+                          static_cast<hipStream_t>(stream)),
+               "AdamW step");
+        n = 0;
+      }
+      if (i == count) break;
+      const twell_adamw_tensor &t = tensors[i];
+      const int is = (t.dtype == TWELL_BF16 ? 1 : 0) | (t.grad_dtype == TWELL_BF16 ? 2 : 0) | (t.m_scale ? 4 : 0) |
+                     (t.master ? 8 : 0);
+      if (is == kind && t.n > 0)
+        list[n++] = AdamWTensor{t.n, t.weight, t.master, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.weight_decay, i};
+    }
+  }
+  return TWELL_OK;
+}
+
+twell_status twell_adamw_states(const twell_adamw_tensor *tensors, int count, twell_dtype dtype, void *const *m,
+                                void *const *v, void *stream) {
+  g_err[0] = 0;
+  if (!valid_dtype((int)dtype)) return fail(TWELL_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  twell_status st = check_list(tensors, count);
+  if (st != TWELL_OK) return st;
+  for (int i = 0; i < count; ++i) {
+    const twell_adamw_tensor &t = tensors[i];
+    if ((st = check_states(t, i)) != TWELL_OK) return st;
+    if (t.n > 0 && t.m_scale == nullptr) return fail(TWELL_ERR_INVALID_ARG, "tensor %d: states of 32 bits", i);
+    if (!aligned(m ? m[i] : nullptr, dt_size(dtype)) || !aligned(v ? v[i] : nullptr, dt_size(dtype)))
+      return fail(TWELL_ERR_UNSUPPORTED, "tensor %d: misaligned output", i);
+  }
+  StateRead list[STATE_LIST];
+  int n = 0;
+  for (int64_t i = 0; i < 2 * (int64_t)count; ++i) {
+    const twell_adamw_tensor &t = tensors[i / 2];
+    void *out = i % 2 == 0 ? (m ? m[i / 2] : nullptr) : (v ? v[i / 2] : nullptr);
+    if (out != nullptr && t.n > 0)
+      list[n++] = i % 2 == 0 ? StateRead{t.n, static_cast<const uint8_t *>(t.m), t.m_scale, out, 1}
+                             : StateRead{t.n, static_cast<const uint8_t *>(t.v), t.v_scale, out, 0};
+    if (n == STATE_LIST || (i == 2 * (int64_t)count - 1 && n > 0)) {
+      TW_TRY(state_read(list, n, to_dt(dtype), static_cast<hipStream_t>(stream)), "8-bit states");
+      n = 0;
+    }
+  }
   return TWELL_OK;
 }
 

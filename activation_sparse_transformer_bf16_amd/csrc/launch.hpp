@@ -301,6 +301,11 @@ struct NormArgs {
   int64_t ld_q;
   float *scale;          // [rows] with q
   float unit = 1.0f;     // set by norm_rows: the factor on the squares
+  uint8_t *q4 = nullptr;        // 4-bit rows (mx4.hpp) in place of q, or null
+  int64_t ld_q4 = 0;
+  uint8_t *q4_scale = nullptr;  // [rows][ld_q4_scale]
+  int64_t ld_q4_scale = 0;
+  float *q4_factor = nullptr;   // [rows]: r
 };
 // A row is held in registers: at most NORM_MAX_CHUNKS chunks of 64 lanes x 16 bytes.
 constexpr int NORM_MAX_CHUNKS = 128;
@@ -354,6 +359,92 @@ struct Int8Args {
 };
 size_t int8_matmul_workspace(int M, int N, int K);
 hipError_t int8_matmul(const Int8Args &a, void *workspace, hipStream_t s);
+
+// Rows of microscaled 4-bit floats (mx4.hpp): x -> q and scale, or q, scale and
+// factor -> y.
+struct Mx4Args {
+  Dt dtype;              // of x, y
+  int rows, cols;
+  const void *x;
+  int64_t ld_x;
+  uint8_t *q;            // [rows][ld_q]
+  int64_t ld_q;
+  uint8_t *scale;        // [rows][ld_scale]
+  int64_t ld_scale;
+  const float *factor;   // [rows] or null
+  void *y;
+  int64_t ld_y;
+};
+hipError_t mx4_rows(const Mx4Args &a, bool read, hipStream_t s);
+
+// Product of such rows (mx4_matmul.hip): a [M][K], b [N][K], rows 16-byte aligned
+// with whole readable 16-byte chunks, of the scales too; y [M][N].
+constexpr int MX4_MAX_K = 1 << 20;
+constexpr int MX4_MAX_ROWS = 1 << 26;  // of a and of b
+struct Mx4MatmulArgs {
+  Dt dtype;              // of y
+  int M, N, K;
+  const uint8_t *a;
+  int64_t ld_a;
+  const uint8_t *a_scale;
+  int64_t ld_sa;
+  const float *a_factor;  // [M] or null
+  const uint8_t *b;
+  int64_t ld_b;
+  const uint8_t *b_scale;
+  int64_t ld_sb;
+  const float *b_factor;  // [N] or null
+  const float *bias;      // [M] or null
+  void *y;
+  int64_t ld_y;
+};
+size_t mx4_matmul_workspace(int M, int N, int K);
+hipError_t mx4_matmul(const Mx4MatmulArgs &a, void *workspace, hipStream_t s);
+
+// One tensor of the optimiser's step, as the C ABI describes it.
+struct AdamWTensor {
+  int64_t n;
+  void *weight;
+  float *master;         // or null
+  const void *grad;
+  void *m, *v;           // fp32, or 8-bit codes with their scale bytes
+  uint8_t *m_scale, *v_scale;
+  float decay;
+  int place;             // in the call's list
+};
+struct AdamWArgs {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  uint64_t seed;
+  const float *lr_device;     // or null
+  const int64_t *step_device; // or null
+  const float *clip;          // [2]: norm, factor; or null
+};
+// At most ADAMW_LIST tensors of one kind: weights and gradients of these types,
+// states in 8 bits or fp32, with or without fp32 copies of the weights.
+constexpr int ADAMW_LIST = 40;
+hipError_t adamw_step(const AdamWTensor *t, int count, Dt weight, Dt grad, bool bits8, const AdamWArgs &a,
+                      hipStream_t s);
+// The values of at most STATE_LIST 8-bit states.
+struct StateRead {
+  int64_t n;
+  const uint8_t *code, *scale;
+  void *out;             // [n]
+  int is_signed;         // m; v is not
+};
+constexpr int STATE_LIST = 64;
+hipError_t state_read(const StateRead *r, int count, Dt dtype, hipStream_t s);
+// Squares of at most GRAD_LIST gradients: grad_wgs() partial sums; then the root of
+// n of them in out[0] and min(1, max_norm / norm) in out[1].
+struct GradRef {
+  const void *p;
+  int64_t n;
+  Dt dtype;
+};
+constexpr int GRAD_LIST = 96;
+int grad_wgs(const GradRef *g, int count);
+hipError_t grad_squares(const GradRef *g, int count, double *partial, hipStream_t s);
+hipError_t grad_norm(const double *partial, int n, float max_norm, float *out, hipStream_t s);
 
 // *p = 0 with a one-thread kernel (safe under stream capture).
 hipError_t zero_int(int *p, hipStream_t s);

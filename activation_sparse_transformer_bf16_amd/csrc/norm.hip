@@ -7,6 +7,9 @@
 //   gradient: g = dy w,  dx = round(dh + r (g - h r^2 mean(g h))),
 //             dw_j = sum_t dy_tj h_tj r_t
 //
+// The rows in 4 bits (mx4.hpp) are those of z too, and r is their row's factor: a
+// block's scale is a power of two, which r is not.
+//
 // The row's factor r cancels between a value and the row's largest one, so q
 // is formed from z alone: it holds no sum, and is the same to the bit however
 // the row is split over lanes.  Only scale carries r.  m_t is kept above
@@ -22,165 +25,14 @@
 // of it goes through scratch; which variants, and their times, is said at each
 // kernel.
 #include "launch.hpp"
+#include "mx4.hpp"
+#include "rows.hpp"
 
 namespace twell {
 
 constexpr float Q_MAX = 127.0f;
 constexpr float Q_TINY = 0x1p-100f;
 constexpr uint32_t INF_BITS = 0x7F800000u;
-
-// How a kernel reads and writes its rows, in chunks of 16 bytes.
-enum class Rows {
-  WHOLE,  // all 16-byte aligned and a whole number of chunks
-  ANY,    // aligned to the element only, at least one chunk long
-  TINY,   // shorter than one chunk
-};
-
-// A row of d elements; `p` is the same for a whole wave.
-//
-// WHOLE rows go through a buffer descriptor of exactly their bytes, so that
-// chunks past the end load zeros and store nothing, with no branch.
-//
-// ANY rows go through 16-byte accesses at the element's alignment.  The chunk
-// that crosses the end, and those past it, load the row's last 16 bytes
-// instead; trim() then moves the row's elements into place and zeroes the
-// others.  It is apart from load() because it needs the loaded value: a row's
-// loads are all under way before the first is waited for.  The crossing chunk
-// is stored by elements.  8192 x 2047 bf16 with residual: 30 us (25 at 2048),
-// element by element 84, as each load is waited for by itself.
-//
-// Stores of whole rows (h, y, dx) carry the non-temporal bit: written this way
-// they leave L2 to the inputs (bf16, 8192 x 2048 with residual and 8 bits:
-// 29.6 -> 23.4 us, and no slower with the product that reads them behind it).
-// Stores of q do not: its reader then misses (the quantiser of 8192 x 8192
-// and the 8-bit product together 151 against 160 us).  Loads carry the bit
-// (NT) where no other kernel's copy in cache is worth keeping: in the
-// quantiser (36.3 -> 32.8 us) and the gradient (16384 x 4096: 96 -> 89 us);
-// in the norm it costs 4 us, as x and residual come from the kernel before.
-// ANY rows share lines between waves, and the bit drops them in between: the
-// quantiser loads those without it (8192 x 2047 fp32: 16.3 -> 14.1 us; the
-// gradient does not gain, 51.8 -> 55.7), and the gradient stores them without
-// it (16384 x 4095 fp32: 195 -> 168 us; the norm does not gain).
-constexpr int NON_TEMPORAL = 2;
-
-// The offset stays 32-bit and apart from the row's address, which is in scalar
-// registers: the compiler otherwise adds the two first and keeps a 64-bit address
-// per access (up to 19 more vector registers, and spills).
-__device__ __forceinline__ void keep_offset(uint32_t &at) { asm volatile("" : "+v"(at)); }
-
-typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
-template <Dt D, Rows R, bool NT = false>
-struct Row {
-  using T = typename DtT<D>::T;
-  static constexpr int E = 16 / DtT<D>::size;  // elements per chunk
-  __amdgpu_buffer_rsrc_t rsrc;
-  T *p;
-  int d;
-
-  __device__ __forceinline__ Row(const void *base, int64_t t, int64_t ld, int d_)
-      : p(const_cast<T *>(static_cast<const T *>(base)) + t * ld), d(d_) {
-    if constexpr (R == Rows::WHOLE) rsrc = __builtin_amdgcn_make_buffer_rsrc(p, 0, d * (int)sizeof(T), 0x00020000);
-  }
-  // elements e0 .. e0 + E - 1, +0 past the end; of ANY rows after trim()
-  __device__ __forceinline__ u32x4_t load(int e0) const {
-    if constexpr (R == Rows::WHOLE) {
-      return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rsrc, e0 * (int)sizeof(T), 0, NT ? NON_TEMPORAL : 0));
-    } else if constexpr (R == Rows::ANY) {
-      if (__builtin_amdgcn_readfirstlane(e0) >= d) return u32x4_t{0u, 0u, 0u, 0u};  // nothing for this wave
-      uint32_t at = min((uint32_t)e0, (uint32_t)(d - E)) * (uint32_t)sizeof(T);
-      keep_offset(at);
-      const u32x4_any_t *q = reinterpret_cast<const u32x4_any_t *>(reinterpret_cast<const char *>(p) + at);
-      if constexpr (NT)
-        return __builtin_nontemporal_load(q);
-      else
-        return *q;
-    } else {
-      u32x4_t w = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (e0 + i < d) {
-          if constexpr (D == Dt::BF16)
-            w[i / 2] |= (uint32_t)p[e0 + i] << (16 * (i % 2));
-          else
-            w[i] = __float_as_uint(p[e0 + i]);
-        }
-      }
-      return w;
-    }
-  }
-  __device__ __forceinline__ u32x4_t trim(u32x4_t w, int e0) const {
-    if constexpr (R == Rows::ANY) {
-      if (__builtin_amdgcn_readfirstlane(e0) + 64 * E > d) {  // the wave's chunks reach the end
-        const int n = max(e0 - (d - E), 0) * (int)sizeof(T);  // bytes to move by
-        u32x4_t v = w;
-        if constexpr (sizeof(T) == 2) {
-          const bool half = (n & 2) != 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = half ? (v[i] >> 16) | (i < 3 ? w[i < 3 ? i + 1 : 3] << 16 : 0u) : v[i];
-        }
-        const bool one = (n & 4) != 0, two = (n & 8) != 0, all = n >= 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = one ? (i < 3 ? v[i < 3 ? i + 1 : 3] : 0u) : v[i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = two ? (i < 2 ? w[i < 2 ? i + 2 : 3] : 0u) : w[i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = all ? 0u : w[i];
-      }
-    }
-    return w;
-  }
-  template <bool NTS = true>
-  __device__ __forceinline__ void store(int e0, u32x4_t w) const {
-    if constexpr (R == Rows::WHOLE) {
-      __builtin_amdgcn_raw_buffer_store_b128(w, rsrc, e0 * (int)sizeof(T), 0, NON_TEMPORAL);
-    } else if (R == Rows::ANY && e0 + E <= d) {
-      uint32_t at = (uint32_t)e0 * (uint32_t)sizeof(T);
-      keep_offset(at);
-      u32x4_any_t *q = reinterpret_cast<u32x4_any_t *>(reinterpret_cast<char *>(p) + at);
-      if constexpr (NTS)
-        __builtin_nontemporal_store(w, q);
-      else
-        *q = w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (e0 + i < d) {
-          if constexpr (D == Dt::BF16)
-            p[e0 + i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
-          else
-            p[e0 + i] = __uint_as_float(w[i]);
-        }
-      }
-    }
-  }
-};
-
-template <Dt D>
-__device__ __forceinline__ void unpack(u32x4_t w, float (&v)[16 / DtT<D>::size]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (D == Dt::BF16) {
-      v[2 * i] = bf16lo(w[i]);
-      v[2 * i + 1] = bf16hi(w[i]);
-    } else {
-      v[i] = __uint_as_float(w[i]);
-    }
-  }
-}
-
-// Rounds to the storage type.
-template <Dt D>
-__device__ __forceinline__ u32x4_t pack_chunk(const float (&v)[16 / DtT<D>::size]) {
-  u32x4_t w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (D == Dt::BF16)
-      w[i] = (uint32_t)bf16_rne(v[2 * i]) | ((uint32_t)bf16_rne(v[2 * i + 1]) << 16);
-    else
-      w[i] = __float_as_uint(v[i]);
-  }
-  return w;
-}
 
 // The chunk's bits only from here on: without this the compiler keeps the
 // unpacked values of the first pass over a row alive for the second, twice the
@@ -288,8 +140,9 @@ constexpr int row_waves(int W) { return W > 4 ? W : 4; }
 // waves, 8 chunks) 97 to 139 of them are spilled, in the quantiser 20 to 61: 1000 x
 // 39999 bf16 212, 1000 x 24575 fp32 185 (quantiser 85 and 38, whole rows 23 and 22).
 // Of 32 to 64 KB only bf16 spills (24): 2000 x 24575 138 us, 2000 x 12287 fp32 79.
-template <Dt D, int W, int NC, Rows R, bool NORM>
+template <Dt D, int W, int NC, Rows R, bool NORM, bool Q4>
 __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
+  static_assert(NORM || !Q4, "rows in 4 bits without a norm: mx4.hip");
   constexpr int E = 16 / DtT<D>::size;
   constexpr int RB = row_waves(W) / W;
   constexpr bool HOLD = NORM && NC <= 4;
@@ -347,7 +200,7 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
           if (NORM) ss += u[i] * a.unit * u[i];
           z[i] = u[i];
         }
-        if (a.q != nullptr) {
+        if (!Q4 && a.q != nullptr) {
           if constexpr (NORM) {
             float w[E];
             unpack<D>(HOLD ? wv[c] : weight.trim(weight.load(first + c * STEP), first + c * STEP), w);
@@ -390,9 +243,16 @@ __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < E; ++i) u[i] *= w[i];
       }
-      if (a.q != nullptr) store_q<E, R>(a.q + t * a.ld_q, e0, d, u, inv, bad);
+      if constexpr (Q4) {
+        uint32_t byte;
+        const uint32_t codes = mx4_codes<E>(u, byte);
+        mx4_store<E>(a.q4 + t * a.ld_q4, a.q4_scale + t * a.ld_q4_scale, e0, d, codes, byte);
+      } else if (a.q != nullptr) {
+        store_q<E, R>(a.q + t * a.ld_q, e0, d, u, inv, bad);
+      }
     }
-    if (a.q != nullptr && lane == 0 && wave % W == 0)
+    if (Q4 && lane == 0 && wave % W == 0) a.q4_factor[t] = r;
+    if (!Q4 && a.q != nullptr && lane == 0 && wave % W == 0)
       a.scale[t] = bad ? __uint_as_float(0x7FC00000u) : r * (m / Q_MAX);
   }
 }
@@ -608,7 +468,7 @@ static bool rows16(const void *p, int64_t ld, int s) {
   return p == nullptr || ((reinterpret_cast<uintptr_t>(p) % 16) == 0 && (ld * s) % 16 == 0);
 }
 
-template <Dt D, int W, int NC, bool NORM>
+template <Dt D, int W, int NC, bool NORM, bool Q4>
 static hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
   constexpr int S = DtT<D>::size, RB = row_waves(W) / W;
   const bool whole = (a.d * S) % 16 == 0 && rows16(a.x, a.ld_x, S) && rows16(a.residual, a.ld_res, S) &&
@@ -616,11 +476,11 @@ static hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
   // at most 2^20 workgroups, which take more rows in turn
   const dim3 grid(std::min((a.rows - 1) / RB + 1, 1 << 20)), block(64 * row_waves(W));
   if (whole) {
-    hipLaunchKernelGGL((k_norm_rows<D, W, NC, Rows::WHOLE, NORM>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_norm_rows<D, W, NC, Rows::WHOLE, NORM, Q4>), grid, block, 0, s, a);
   } else if (a.d * S >= 16) {
-    hipLaunchKernelGGL((k_norm_rows<D, W, NC, Rows::ANY, NORM>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_norm_rows<D, W, NC, Rows::ANY, NORM, Q4>), grid, block, 0, s, a);
   } else if constexpr (W * NC == 1) {
-    hipLaunchKernelGGL((k_norm_rows<D, W, NC, Rows::TINY, NORM>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_norm_rows<D, W, NC, Rows::TINY, NORM, Q4>), grid, block, 0, s, a);
   }
   return hipGetLastError();
 }
@@ -631,17 +491,17 @@ static hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
 // 23.0 us at 8192 x 2048 bf16; more waves pay for the barrier, 27.9 us).  16 waves
 // take two chunks each where that is enough (2000 x 8192 fp32 with residual
 // 43.9 -> 40.9 us against four).
-template <Dt D, bool NORM>
+template <Dt D, bool NORM, bool Q4>
 static hipError_t norm_rows_dt(const NormArgs &a, hipStream_t s) {
   const int chunks = norm_chunks(a.d, D);
-  if (chunks <= 1) return launch_rows<D, 1, 1, NORM>(a, s);
-  if (chunks <= 2) return launch_rows<D, 2, 1, NORM>(a, s);
-  if (chunks <= 4) return launch_rows<D, 4, 1, NORM>(a, s);
-  if (chunks <= 8) return launch_rows<D, 4, 2, NORM>(a, s);
-  if (chunks <= 16) return launch_rows<D, 4, 4, NORM>(a, s);
-  if (chunks <= 32) return launch_rows<D, 16, 2, NORM>(a, s);
-  if (chunks <= 64) return launch_rows<D, 16, 4, NORM>(a, s);
-  if (chunks <= NORM_MAX_CHUNKS) return launch_rows<D, 16, 8, NORM>(a, s);
+  if (chunks <= 1) return launch_rows<D, 1, 1, NORM, Q4>(a, s);
+  if (chunks <= 2) return launch_rows<D, 2, 1, NORM, Q4>(a, s);
+  if (chunks <= 4) return launch_rows<D, 4, 1, NORM, Q4>(a, s);
+  if (chunks <= 8) return launch_rows<D, 4, 2, NORM, Q4>(a, s);
+  if (chunks <= 16) return launch_rows<D, 4, 4, NORM, Q4>(a, s);
+  if (chunks <= 32) return launch_rows<D, 16, 2, NORM, Q4>(a, s);
+  if (chunks <= 64) return launch_rows<D, 16, 4, NORM, Q4>(a, s);
+  if (chunks <= NORM_MAX_CHUNKS) return launch_rows<D, 16, 8, NORM, Q4>(a, s);
   return hipErrorInvalidValue;
 }
 
@@ -661,9 +521,11 @@ hipError_t norm_rows(const NormArgs &args, hipStream_t s) {
   if (args.rows <= 0) return hipSuccess;
   NormArgs a = args;
   a.unit = norm_unit(a.d, a.eps);
+  if (a.q4 != nullptr)
+    return a.dtype == Dt::BF16 ? norm_rows_dt<Dt::BF16, true, true>(a, s) : norm_rows_dt<Dt::F32, true, true>(a, s);
   if (a.weight != nullptr)
-    return a.dtype == Dt::BF16 ? norm_rows_dt<Dt::BF16, true>(a, s) : norm_rows_dt<Dt::F32, true>(a, s);
-  return a.dtype == Dt::BF16 ? norm_rows_dt<Dt::BF16, false>(a, s) : norm_rows_dt<Dt::F32, false>(a, s);
+    return a.dtype == Dt::BF16 ? norm_rows_dt<Dt::BF16, true, false>(a, s) : norm_rows_dt<Dt::F32, true, false>(a, s);
+  return a.dtype == Dt::BF16 ? norm_rows_dt<Dt::BF16, false, false>(a, s) : norm_rows_dt<Dt::F32, false, false>(a, s);
 }
 
 template <Dt D, int W, int NC>

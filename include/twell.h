@@ -586,6 +586,170 @@ twell_status twell_int8_matmul(const twell_int8 *a, const twell_int8 *b, const f
                                void *stream);
 
 /*
+ * twell_mx4 -- rows of microscaled 4-bit floats.  Blocks of 32 elements along a row
+ * share a scale 2^e; an element is 0, 0.5, 1, 1.5, 2, 3, 4 or 6 (codes 0 ... 7) times
+ * 2^e, with a sign in bit 3 of its code.  A byte holds two elements, the even one in
+ * its low half: element (t, j) is in q[t * ld + j / 2].
+ * Scale bytes are e + 127 (1 ... 253; 255: every value of the block is NaN).  The byte
+ * of block b of row t is scale[t * ld_scale + b / 16 * 16 + b % 4 * 4 + b / 4 % 4]:
+ * groups of 16 bytes, each transposed as a 4 x 4 matrix, which is how the matrix
+ * cores read them.
+ * factor: one fp32 value per row that multiplies all of it, or NULL for 1.
+ * q and scale are 16-byte aligned, ld and ld_scale multiples of 16; the bytes up
+ * to the next multiple of 16 behind a row's codes and scales are READABLE
+ * (buffers of rows * ld and rows * ld_scale bytes are enough).  Those past
+ * ceil(cols / 2) codes and past the last block's scale hold anything: no operator
+ * writes them, and they reach no result.  Of an odd row's last byte the high half
+ * is written as 0 and not read.
+ */
+typedef struct {
+  int32_t rows, cols;
+  int64_t ld;           /* bytes from row to row of q: a multiple of 16, >= ceil(cols / 2) */
+  uint8_t *q;           /* [rows][ld] */
+  int64_t ld_scale;     /* and of scale: a multiple of 16, >= ceil(cols / 32) */
+  uint8_t *scale;       /* [rows][ld_scale] */
+  float *factor;        /* [rows] or NULL */
+} twell_mx4;
+
+/*
+ * twell_quantize_mx4 -- x [out->rows][out->cols] to 4 bits: for each block, e is
+ * the smallest whole number (-126 ... 126) with max |x| <= 7 * 2^e, and each element
+ * the nearest of the values above times 2^e, ties to the even code.  So no element is
+ * further off than half the step at its size (the largest, between 6 and 7, too).
+ * A block with an infinite or NaN element gets codes 0 and the scale byte 255.
+ * (Elements over 3.5 * 2^126 have 2^128 as their nearest value, which is read as
+ * infinite.)  out->factor has to be NULL.
+ * Errors: INVALID_ARG (NULL pointers, sizes, strides, a factor), UNSUPPORTED
+ * (alignment), HIP.
+ */
+twell_status twell_quantize_mx4(const void *x, int64_t ld_x, twell_dtype dtype, const twell_mx4 *out, void *stream);
+
+/*
+ * twell_dequantize_mx4 -- the values of in's elements, factor included (one fp32
+ * product), rounded to dtype: y [in->rows][in->cols].
+ * Errors: as twell_quantize_mx4.
+ */
+twell_status twell_dequantize_mx4(const twell_mx4 *in, twell_dtype dtype, void *y, int64_t ld_y, void *stream);
+
+/*
+ * twell_rmsnorm_mx4 -- twell_rmsnorm with the normed rows in 4 bits: q's codes and
+ * scales are those of z = h * weight (one fp32 product), and its factors r_t, so
+ * that the values are h_tj * r_t * weight_j as y's are, without its rounding.  The
+ * bits do not depend on r and are the same for any order of the sum.  q is needed,
+ * with a factor; h and y are optional.  Everything else as twell_rmsnorm.
+ * Errors: as twell_rmsnorm.
+ */
+twell_status twell_rmsnorm_mx4(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual,
+                               const void *weight, float eps, int rows, int d, twell_dtype dtype, void *h,
+                               int64_t ld_h, void *y, int64_t ld_y, const twell_mx4 *q, void *stream);
+
+/*
+ * twell_mx4_matmul -- the product of 4-bit rows:
+ *     y_mn = round((sum_k a_mk b_nk) * a->factor_m * b->factor_n + row_bias_m)
+ * on the matrix cores, which apply the blocks' scales; the sums in fp32 in a fixed
+ * order.  y [a->rows][b->rows] in dtype; row_bias: one fp32 value per row of a, or
+ * NULL.  a->cols == b->cols, at most 2^20; at most 2^26 rows each.  y may not
+ * overlap the inputs.
+ * workspace: >= twell_mx4_matmul_workspace_size(a->rows, b->rows, a->cols) bytes,
+ * 256-byte aligned; NULL where that is 0.  Products with too few output tiles for the
+ * GPU cut K into ranges and keep their sums there (at most 64 MB).
+ * Errors: INVALID_ARG (NULL pointers, sizes, strides, different cols),
+ * UNSUPPORTED (cols, rows, alignment, a stride that is not a multiple of 16),
+ * WORKSPACE, HIP.
+ */
+size_t twell_mx4_matmul_workspace_size(int M, int N, int K);
+twell_status twell_mx4_matmul(const twell_mx4 *a, const twell_mx4 *b, const float *row_bias, twell_dtype dtype,
+                              void *y, int64_t ld_y, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * twell_adamw_tensor -- one tensor of the optimiser's step: n elements that lie
+ * together, each buffer aligned to its own element type.  Lists of them are HOST memory.
+ * States are fp32 (m_scale and v_scale NULL), or 8 bits with one scale byte per 32
+ * elements (of m and of v; ceil(n / 32) bytes each).  All-zero buffers are the states
+ * before the first step in either form.
+ *
+ * 8 bits: a block of 32 elements shares 2^E, E the smallest whole number (-87 ... 113)
+ * with max <= 1.875 * 2^E; its scale byte is E + 127, lower bytes count as 40 (E = -87),
+ * and 241 ... 255 make the block NaN (255 is what is written for one that is not finite,
+ * or too large).  A code's fields are, from the top: m a sign, 4 bits of exponent
+ * and 3 of mantissa, v 5 and 3; the topmost exponent stands for 2^E, exponent 0 for
+ * the subnormal numbers below the lowest.
+ */
+typedef struct {
+  int64_t n;             /* elements, 0 ... 2^40 */
+  void *weight;          /* [n], dtype */
+  float *master;         /* [n] fp32 copy of bf16 weights, or NULL for none */
+  const void *grad;      /* [n], grad_dtype */
+  void *m, *v;           /* [n] fp32, or uint8_t codes */
+  uint8_t *m_scale, *v_scale;  /* [ceil(n / 32)], or both NULL */
+  twell_dtype dtype, grad_dtype;
+  float weight_decay;
+} twell_adamw_tensor;
+
+/*
+ * twell_grad_norm -- out[0] = the root of the sum of the squares of all gradients
+ * of the list, out[1] = min(1, max_norm / out[0]), the factor that clips them to
+ * max_norm (NaN where the norm is infinite or NaN).  Only n, grad and grad_dtype of
+ * the tensors are read.  Squares and sums are fp64, in a fixed order.  max_norm > 0
+ * (infinity: the factor is 1).  With no element the norm is 0 and the factor 1.
+ * workspace: >= twell_grad_norm_workspace_size(tensors, count) bytes, 256-byte
+ * aligned (0 for a list that is refused).
+ * Errors: INVALID_ARG (a NULL list, output or gradient, a negative size, dtype,
+ * max_norm), UNSUPPORTED (alignment, n), WORKSPACE, HIP.
+ */
+size_t twell_grad_norm_workspace_size(const twell_adamw_tensor *tensors, int count);
+twell_status twell_grad_norm(const twell_adamw_tensor *tensors, int count, float max_norm, float *out,
+                             void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * twell_adamw_step -- one step of AdamW over all tensors of a list, in place:
+ *     g = grad * clip[1]
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + ((1 - beta2) g) g
+ *     w = (1 - lr weight_decay) w - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32, with one rounding per operation in g, m and v (w: the fp32 copy where there
+ * is one, which the weight is then rounded from; the weight itself otherwise).  w
+ * takes m and v before they are rounded to 8 bits.
+ * 8-bit states, and bf16 weights without an fp32 copy, are rounded up or down by 16
+ * random bits each, up as often as the value lies near the upper neighbour: a step is
+ * mostly far smaller than half the distance to the next value and would be lost
+ * otherwise.  v > 0 is not rounded to 0.  The bits are a hash of seed + t, the
+ * tensor's place in the list and the element's index: the same call gives the same
+ * results.
+ * v below 2^-126 may count as 0 in the root.  eps = 0 with m = v = 0 is 0/0 (NaN).
+ *
+ * step: t, from 1 on.  step_device, lr_device: where not NULL, t and lr are read from
+ * the GPU when the step runs, so that a captured graph of it can be replayed with
+ * other values; a t below 1 there leaves the step out.
+ * clip: [2] as twell_grad_norm writes it, or NULL.  A factor that is not finite (an
+ * infinite or NaN gradient) leaves the step out: nothing is written.
+ * No tensor's buffers may overlap another's that is written, or each other.
+ * Errors: INVALID_ARG (NULL pointers, a negative n, dtypes, one scale without the
+ * other, an fp32 copy of fp32 weights, betas outside [0, 1), a negative or not finite
+ * lr or eps, a weight_decay that is not finite, step < 1), UNSUPPORTED (alignment,
+ * n), HIP.
+ */
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  uint64_t seed;
+  const float *lr_device;      /* [1] or NULL */
+  const int64_t *step_device;  /* [1] or NULL */
+} twell_adamw;
+twell_status twell_adamw_step(const twell_adamw_tensor *tensors, int count, const twell_adamw *args,
+                              const float *clip, void *stream);
+
+/*
+ * twell_adamw_states -- the values of the list's 8-bit states: m[i], v[i] [n] in dtype
+ * (bf16 holds them exactly but for values below 2^-126).  m and v are HOST arrays of
+ * count pointers; either may be NULL, and so may any of their entries (not read).
+ * Only n, m, v and their scales are read of the tensors.
+ * Errors: INVALID_ARG (NULL list or states, no scales, dtype, sizes), UNSUPPORTED
+ * (alignment, n), HIP.
+ */
+twell_status twell_adamw_states(const twell_adamw_tensor *tensors, int count, twell_dtype dtype, void *const *m,
+                                void *const *v, void *stream);
+
+/*
  * twell_stream_probe -- streaming HBM probe (a measurement aid, not part of
  * the layer's computation; the pages define no such operation).
  *
