@@ -397,6 +397,8 @@ struct Mx4MatmulArgs {
   const float *bias;      // [M] or null
   void *y;
   int64_t ld_y;
+  float *partial = nullptr;  // set by mx4_matmul: sums of the K ranges, [ranges][M][N rounded up to 4]
+  int k_part = 0;            // and the ranges' length
 };
 size_t mx4_matmul_workspace(int M, int N, int K);
 hipError_t mx4_matmul(const Mx4MatmulArgs &a, void *workspace, hipStream_t s);

@@ -3,25 +3,39 @@
 //   y_mn = round((sum_k a_mk b_nk) fa_m fb_n + bias_m)
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 rows of 128 elements of both
-// sides and applies the scales: lane 16 h + r holds elements 32 h ... 32 h + 31 of
-// row r (16 bytes) and that block's scale byte.
+// sides and applies the blocks' scales: lane 16 h + r holds elements 32 h ... 32 h + 31
+// of row r (16 bytes) and, in one byte of a dword, that block's scale.  The byte is
+// chosen by the instruction, so a dword serves four steps of 128 elements: a group
+// of 512, whose 16 scale bytes lie in a row as mx4_place says.
+//
+// K need not fill the last group: codes of a past K are zeroed and scales past the
+// last block set to 2^-127 on both sides (what lies there may be NaN).  Nothing
+// outside the operands is read, and results past M and N are not stored.
+//
+// Three kernels, as for 8-bit rows (int8.hip), whose tiles have the same bytes:
+//  * k_mx4_tile: tiles of BM x BN outputs, operands through a ring of LDS stages;
+//    where the tiles are too few for the chip, K is cut into ranges whose sums go
+//    to the workspace,
+//  * k_mx4_join, which adds them in order and writes the results.
+//  * k_mx4_small: products too small to fill the chip with such tiles: 16 to 64
+//    rows and columns per workgroup, whose waves split K.
 #include "launch.hpp"
 #include "mx4.hpp"
+#include "narrow.hpp"
 
 namespace twell {
 
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
-// acc += a b^T over 128 elements; S: the byte of the two scale dwords.
+// acc += b a^T over 128 elements; S: the byte of the scale dwords.
 template <int S>
-__device__ __forceinline__ f32x4_t mx4_mfma(u32x4_t a, u32x4_t b, f32x4_t acc, uint32_t sa, uint32_t sb) {
-  const i32x8_t x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  const i32x8_t y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 4, 4, S, (int)sa, S, (int)sb);
+__device__ __forceinline__ f32x4_t mx4_mfma(u32x4_t b, u32x4_t a, f32x4_t acc, uint32_t sb, uint32_t sa) {
+  const i32x8_t x = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  const i32x8_t y = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 4, 4, S, (int)sb, S, (int)sa);
 }
 
-// Keeps the first `left` elements of a 32-element chunk.
+// The first `left` elements of a 32-element chunk, zeros for the others.
 __device__ __forceinline__ u32x4_t mx4_keep(u32x4_t v, int left) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -31,53 +45,631 @@ __device__ __forceinline__ u32x4_t mx4_keep(u32x4_t v, int left) {
   return v;
 }
 
-// One wave per 16 x 16 results.
+// Which bytes of a lane's scale dword are blocks of the row: byte s is block 4 s + h
+// of a group with `left` elements.
+__device__ __forceinline__ uint32_t mx4_scale_mask(int left, int h) {
+  const int n = min(max((left - MX4_BLOCK * h + 127) / 128, 0), 4);
+  return n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+}
+
+__device__ __forceinline__ float mx4_result(float acc, float fa, float fb, float bias) { return acc * fa * fb + bias; }
+
+// Four results of one row from column n on.
 template <Dt D>
-__global__ __launch_bounds__(64) void k_mx4_simple(Mx4MatmulArgs a) {
-  const int lane = threadIdx.x, rho = lane & 15, h = lane >> 4;
-  const int tiles_n = (a.N + 15) / 16;
-  const int m0 = blockIdx.x / tiles_n * 16, n0 = blockIdx.x % tiles_n * 16;
-  const int m = min(m0 + rho, a.M - 1), n = min(n0 + rho, a.N - 1);
-  const uint8_t *pa = a.a + (int64_t)m * a.ld_a, *pb = a.b + (int64_t)n * a.ld_b;
-  const uint8_t *sa = a.a_scale + (int64_t)m * a.ld_sa, *sb = a.b_scale + (int64_t)n * a.ld_sb;
-  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  const u32x4_t zero = {0u, 0u, 0u, 0u};
-  for (int k = 0; k < a.K; k += 128) {
-    const int e = k + 32 * h;
-    u32x4_t x = zero, y = zero;
-    uint32_t s = 0, t = 0;
-    if (e < a.K) {
-      x = mx4_keep(*reinterpret_cast<const u32x4_t *>(pa + e / 2), a.K - e);
-      y = *reinterpret_cast<const u32x4_t *>(pb + e / 2);
-      s = sa[mx4_place(e / 32)];
-      t = sb[mx4_place(e / 32)];
-    }
-    acc = mx4_mfma<0>(y, x, acc, t, s);
-  }
-  using T = typename DtT<D>::T;
-  const int row = m0 + rho;
-  if (row >= a.M) return;
-  const float fa = a.a_factor ? a.a_factor[row] : 1.0f, bias = a.bias ? a.bias[row] : 0.0f;
+__device__ __forceinline__ void mx4_store4(typename DtT<D>::T *row, int n, int N, f32x4_t s, float fa,
+                                           const float (&fb)[4], float bias) {
+  float v[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int col = n0 + 4 * h + q;
-    if (col < a.N)
-      static_cast<T *>(a.y)[(int64_t)row * a.ld_y + col] =
-          from_f32<D>(acc[q] * fa * (a.b_factor ? a.b_factor[col] : 1.0f) + bias);
+  for (int q = 0; q < 4; ++q) v[q] = mx4_result(s[q], fa, fb[q], bias);
+  typename DtT<D>::T *p = row + n;
+  if (n + 4 <= N) {
+    if constexpr (D == Dt::BF16)
+      *reinterpret_cast<u32x2_any_t *>(p) = u32x2_any_t{(uint32_t)bf16_rne(v[0]) | ((uint32_t)bf16_rne(v[1]) << 16),
+                                                       (uint32_t)bf16_rne(v[2]) | ((uint32_t)bf16_rne(v[3]) << 16)};
+    else
+      *reinterpret_cast<u32x4_any_t *>(p) = u32x4_any_t{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                       __float_as_uint(v[2]), __float_as_uint(v[3])};
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < N) p[q] = from_f32<D>(v[q]);
   }
 }
 
-size_t mx4_matmul_workspace(int M, int N, int K) { return 0; }
+// ---- tiles ----------------------------------------------------------------------
+
+// LDS: the ring of four stages (a group), two groups' scales (16 bytes per row),
+// then fa, bias and fb of the tile (fp32).
+template <class Cfg, int BN>
+struct Mx4Tile {
+  static constexpr int RING = gemm_dma_ring_bytes<Cfg>(BN);
+  static constexpr int ROWS = Cfg::BM + BN;
+  static constexpr int SCALES = ROWS * 16;
+  static constexpr int VALS = 2 * Cfg::BM + BN;
+  static_assert(Cfg::BM % 64 == 0 && BN % 64 == 0, "copied 64 at a time");
+  static_assert(ROWS / 64 <= Cfg::WAVES, "one copy of scales per wave and group");
+  static_assert(Cfg::STAGES == 4, "the ring is a group");
+  static constexpr int LDS = RING + 2 * SCALES + VALS * 4;
+};
+
+// Tiles as k_int8_tile's (int8.hip): a wave owns 64 columns (4 b fragments) and 2 H
+// 16-row blocks of a, taken in two halves; fragments and scales are read from LDS
+// half a slab ahead.  A slab is 64 bytes of each row, 128 elements.  The loop goes by
+// groups of four slabs, one for each byte of the scale dwords, and the ring holds a
+// group, so every LDS address is fixed.
+template <Dt D, class Cfg, int BN, bool STREAM>
+__global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(Mx4MatmulArgs a, int tiles) {
+  using T = typename DtT<D>::T;
+  using WT = WaveTile<BN, Cfg>;
+  using L = Mx4Tile<Cfg, BN>;
+  constexpr int BM = Cfg::BM, WAVES = Cfg::WAVES, STAGES = Cfg::STAGES;
+  constexpr int H = WT::NWM, NB = 4;
+  constexpr int STAGE = (BM + BN) * SLAB;
+  constexpr int SB = D == Dt::BF16 ? 3 : 2;  // b's swizzle: the rows of a fragment are 8 (4) apart in groups of 4
+  using RowsA = I8Rows<BM, WAVES, 2>;
+  using RowsB = I8Rows<BN, WAVES, SB>;
+  constexpr int OPS = RowsA::PER_WAVE + RowsB::PER_WAVE;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row0 = WT::row0(wave), col0 = WT::col0(wave);
+  int tm, tn;
+  tile_coords(blockIdx.x % tiles, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN, tm, tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  // this workgroup's range of K (whole groups): from here on the operands begin and end with it
+  const int part = blockIdx.x / tiles;
+  const int k0 = part * a.k_part;
+  a.a += k0 / 2;
+  a.b += k0 / 2;
+  a.a_scale += k0 / 32;
+  a.b_scale += k0 / 32;
+  a.K = min(a.K - k0, a.k_part);
+  const int groups = (a.K + MX4_GROUP - 1) / MX4_GROUP;
+  const uint32_t base = lds_address(smem);
+
+  // factors and biases, 64 at a time, and scales; issued before the stages, so that
+  // the stage waits below cover them (loads complete in order)
+#pragma unroll
+  for (int g = 0; g < L::VALS / 64; ++g) {
+    if (g % WAVES != wave) continue;
+    const float *src = g < BM / 64       ? (a.a_factor ? a.a_factor + min(m0 + 64 * g + lane, a.M - 1) : nullptr)
+                       : g < 2 * BM / 64 ? (a.bias ? a.bias + min(m0 + 64 * (g - BM / 64) + lane, a.M - 1) : nullptr)
+                                         : (a.b_factor ? a.b_factor + min(n0 + 64 * (g - 2 * BM / 64) + lane, a.N - 1) : nullptr);
+    const bool some = g < BM / 64 ? a.a_factor != nullptr : g < 2 * BM / 64 ? a.bias != nullptr : a.b_factor != nullptr;
+    if (some) copy4(src, __builtin_amdgcn_readfirstlane((int)(base + L::RING + 2 * L::SCALES + 256 * g)));
+  }
+  // the wave's 64 rows of scales, 16 bytes of each per group
+  const int srow = 64 * wave + lane;
+  const uint8_t *scales = srow < BM ? a.a_scale + (int64_t)min(m0 + srow, a.M - 1) * a.ld_sa
+                                    : a.b_scale + (int64_t)min(n0 + srow - BM, a.N - 1) * a.ld_sb;
+  const bool has_scales = 64 * wave < L::ROWS;
+  auto copy_scales = [&](int g) {
+    if (has_scales)
+      copy16(scales + (int64_t)g * 16,
+             __builtin_amdgcn_readfirstlane((int)(base + L::RING + (g & 1) * L::SCALES + 1024 * wave)));
+  };
+  copy_scales(0);
+  if (groups > 1) copy_scales(1);
+  RowsA da;
+  RowsB db;
+  const int bytes = (a.K + 1) / 2;
+  da.init(wave, lane, 0, reinterpret_cast<const int8_t *>(a.a), a.ld_a, m0, a.M, bytes);
+  db.init(wave, lane, BM * SLAB, reinterpret_cast<const int8_t *>(a.b), a.ld_b, n0, a.N, bytes);
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) {
+    da.template issue_all<true>(base + s * STAGE);
+    db.template issue_all<true>(base + s * STAGE);
+  }
+  f32x4_t acc[2 * H][NB];
+#pragma unroll
+  for (int i = 0; i < 2 * H; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int rho = lane & 15, h = lane >> 4;
+  u32x4_t alo[H], ahi[H], b[NB];
+  uint32_t salo[H], sahi[H], sb[NB];
+  auto read_a = [&](u32x4_t(&f)[H], int slot, int half) {
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+      f[i] = __builtin_bit_cast(u32x4_t, read_i8<2>(smem + slot * STAGE, row0 + 16 * (half * H + i) + rho, lane));
+  };
+  auto read_b = [&](int j, int slot) {
+    b[j] = __builtin_bit_cast(u32x4_t, read_i8<SB>(smem + slot * STAGE + BM * SLAB, col0 + i8_col<D>(j, rho), lane));
+  };
+  // scale dwords of group g: the lane's row, its quarter of the 16 bytes
+  auto scale_at = [&](int g, int row) {
+    return *reinterpret_cast<const uint32_t *>(smem + L::RING + (g & 1) * L::SCALES + row * 16 + 4 * h);
+  };
+  auto read_sa = [&](uint32_t(&f)[H], int g, int half) {
+#pragma unroll
+    for (int i = 0; i < H; ++i) f[i] = scale_at(g, row0 + 16 * (half * H + i) + rho);
+  };
+  auto read_sb = [&](int j, int g) { sb[j] = scale_at(g, BM + col0 + i8_col<D>(j, rho)); };
+  auto multiply = [&](auto step, const u32x4_t(&f)[H], const uint32_t(&sf)[H], int half, int j) {
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+      acc[half * H + i][j] = mx4_mfma<decltype(step)::value>(b[j], f[i], acc[half * H + i][j], sb[j], sf[i]);
+  };
+  wait_vmcnt<(STAGES - 1) * OPS>();
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    read_b(j, 0);
+    read_sb(j, 0);
+  }
+  read_a(alo, 0, 0);
+  read_sa(salo, 0, 0);
+  // slab S of group g; the next group follows
+  auto slab = [&](auto step, int g) {
+    constexpr int S = decltype(step)::value;
+    constexpr int next = (S + 1) % STAGES;
+    read_a(ahi, S, 1);
+    if constexpr (S == 0) read_sa(sahi, g, 1);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) multiply(step, alo, salo, 0, j);
+    __builtin_amdgcn_sched_barrier(0);
+    // every wave has read all of this slab (the barrier waits for its LDS reads) and
+    // the next slab has landed for every wave, and the scales before it
+    wait_vmcnt<(STAGES - 2) * OPS>();
+    __syncthreads();
+    if constexpr (S == 0) {
+      if (g + 2 < groups) copy_scales(g + 2);
+    }
+    read_a(alo, next, 0);
+    if constexpr (S == 3) read_sa(salo, g + 1, 0);
+    // the loads of the slab a group ahead among the products, not in one block
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      multiply(step, ahi, sahi, 1, j);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int q = j; q < OPS; q += NB) {
+        if (q < RowsA::PER_WAVE)
+          da.issue(q, base + S * STAGE);
+        else
+          db.issue(q - RowsA::PER_WAVE, base + S * STAGE);
+      }
+      read_b(j, next);
+      if constexpr (S == 3) read_sb(j, g + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    da.template advance<true>();
+    db.template advance<true>();
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
+  for (int g = 0; g < groups - 1; ++g) {
+    slab(I0(), g);
+    slab(I1(), g);
+    slab(I2(), g);
+    slab(I3(), g);
+  }
+  // the last group: all of it is in the ring or on its way
+  wait_vmcnt<0>();
+  __syncthreads();
+  const int left = a.K - (groups - 1) * MX4_GROUP;
+  read_sa(sahi, groups - 1, 1);
+  if (left < MX4_GROUP) {
+    const uint32_t mask = mx4_scale_mask(left, h);
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      salo[i] &= mask;
+      sahi[i] &= mask;
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) sb[j] &= mask;
+  }
+  auto last = [&](auto step) {
+    constexpr int S = decltype(step)::value;
+    if (S * 128 >= left) return;
+    if constexpr (S > 0) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) read_b(j, S);
+      read_a(alo, S, 0);
+    }
+    read_a(ahi, S, 1);
+    if (left < (S + 1) * 128) {
+      const int n = left - S * 128 - 32 * h;
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        alo[i] = mx4_keep(alo[i], n);
+        ahi[i] = mx4_keep(ahi[i], n);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      multiply(step, alo, salo, 0, j);
+      multiply(step, ahi, sahi, 1, j);
+    }
+  };
+  last(I0());
+  last(I1());
+  last(I2());
+  last(I3());
+
+  if (a.partial != nullptr) {
+    // the range's sums, 4 columns per lane; rows of n_pad (a multiple of 4)
+    const int n_pad = (a.N + 3) / 4 * 4;
+#pragma unroll
+    for (int i = 0; i < 2 * H; ++i) {
+      const int m = m0 + row0 + 16 * i + rho;
+      if (m >= a.M) continue;
+      float *row = a.partial + ((int64_t)part * a.M + m) * n_pad;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int n = n0 + col0 + i8_col<D>(j, 4 * h);
+        if (n < a.N) *reinterpret_cast<f32x4_t *>(row + n) = acc[i][j];
+      }
+    }
+    return;
+  }
+  __syncthreads();  // every wave has read its last fragments: the ring is free
+
+  // Results, 16 rows of 64 columns at a time through the wave's own LDS rows,
+  // so that a store covers whole 128-byte lines.
+  constexpr int S = DtT<D>::size;
+  constexpr int PITCH = 64 * S + 16, PER_ROW = 64 * S / 16;  // bytes of a staged row, lanes that store it
+  static_assert(WAVES * 16 * PITCH <= L::RING, "the staged rows fit the ring");
+  char *mine = smem + wave * 16 * PITCH;
+  const float *va = reinterpret_cast<const float *>(smem + L::RING + 2 * L::SCALES), *vbias = va + BM, *vb = va + 2 * BM;
+  f32x4_t fb[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+    fb[j] = a.b_factor ? *reinterpret_cast<const f32x4_t *>(vb + col0 + i8_col<D>(j, 4 * h)) : f32x4_t{1.0f, 1.0f, 1.0f, 1.0f};
+#pragma unroll
+  for (int i = 0; i < 2 * H; ++i) {
+    const int row = row0 + 16 * i;
+    const float fa = a.a_factor ? va[row + rho] : 1.0f;
+    const float bias = a.bias ? vbias[row + rho] : 0.0f;
+    float v[NB][4];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[j][q] = mx4_result(acc[i][j][q], fa, fb[j][q], bias);
+#pragma unroll
+    for (int j = 0; j < NB; j += D == Dt::BF16 ? 2 : 1) {
+      u32x4_t w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (D == Dt::BF16)
+          w[k] = (uint32_t)bf16_rne(v[j + k / 2][2 * (k % 2)]) | ((uint32_t)bf16_rne(v[j + k / 2][2 * (k % 2) + 1]) << 16);
+        else
+          w[k] = __float_as_uint(v[j][k]);
+      }
+      *reinterpret_cast<u32x4_t *>(mine + rho * PITCH + i8_col<D>(j, 4 * h) * S) = w;
+    }
+    wave_sync();
+#pragma unroll
+    for (int p = 0; p < PER_ROW / 4; ++p) {
+      const int r = p * (64 / PER_ROW) + lane / PER_ROW, c = lane % PER_ROW;
+      const int m = m0 + row + r, n = n0 + col0 + c * (16 / S);
+      const u32x4_t w = *reinterpret_cast<const u32x4_t *>(mine + r * PITCH + c * 16);
+      if (m < a.M && n < a.N) store_run<D, STREAM>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, w);
+    }
+    wave_sync();
+  }
+}
+
+// The ranges' sums added in order, scaled and written: 4 columns per thread, a row
+// per blockIdx.y; four ranges' loads in flight at a time.
+template <Dt D>
+__global__ __launch_bounds__(256) void k_mx4_join(Mx4MatmulArgs a, int parts) {
+  using T = typename DtT<D>::T;
+  const int n_pad = (a.N + 3) / 4 * 4;
+  const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (n >= a.N) return;
+  float fb[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) fb[q] = a.b_factor ? a.b_factor[min(n + q, a.N - 1)] : 1.0f;
+  for (int m = blockIdx.y; m < a.M; m += gridDim.y) {
+    const float fa = a.a_factor ? a.a_factor[m] : 1.0f, bias = a.bias ? a.bias[m] : 0.0f;
+    const float *src = a.partial + (int64_t)m * n_pad + n;
+    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 0; p < parts; p += 4) {
+      f32x4_t v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = *reinterpret_cast<const f32x4_t *>(src + (int64_t)min(p + k, parts - 1) * a.M * n_pad);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (p + k < parts) s += v[k];
+    }
+    mx4_store4<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, s, fa, fb, bias);
+  }
+}
+
+// ---- small products ----------------------------------------------------------------
+
+// Tiles of 16 MF x 16 NF results as k_int8_small's: the WAVES waves take slabs of 128
+// bytes of K (256 elements, two steps) in turn, each through a ring of its own in LDS,
+// and add their sums through LDS at the end.  A slab's copies are 8 rows of 128 bytes
+// each, chunk c of row r kept at c ^ (r / 2 % 8), then a dword of scales for each lane
+// of each fragment, of which the slab uses two bytes.
+template <int MF_, int NF_, int WAVES_, int STAGES_>
+struct Mx4Small {
+  static constexpr int MF = MF_, NF = NF_, WAVES = WAVES_, STAGES = STAGES_;
+  static constexpr int BM = 16 * MF, BN = 16 * NF, THREADS = 64 * WAVES;
+  static constexpr int ROW = 128, CODES = (BM + BN) * ROW, STAGE = CODES + (MF + NF) * 256;
+  static constexpr int COPIES = CODES / 1024, OPS = COPIES + MF + NF;
+  static constexpr int FRAGS = MF * NF, PER = (FRAGS + WAVES - 1) / WAVES;  // fragments of the results, and of one wave
+  static constexpr int LDS = WAVES * STAGES * STAGE;
+  static_assert(WAVES * FRAGS * 1024 <= LDS && LDS <= 160 * 1024, "the sums take the rings' place");
+};
+template <Dt D, class C>
+__global__ __launch_bounds__(C::THREADS) void k_mx4_small(Mx4MatmulArgs a, int tiles) {
+  using T = typename DtT<D>::T;
+  constexpr int MF = C::MF, NF = C::NF, WAVES = C::WAVES, STAGES = C::STAGES, COPIES = C::COPIES;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rho = lane & 15, h = lane >> 4;
+  // an eighth of the tiles, column of tiles after column, for each XCD
+  // (workgroups go to the 8 in turn), whose L2 then keeps their rows of b
+  const int tiles_m = (a.M - 1) / C::BM + 1, each = gridDim.x / 8;
+  const int tile = blockIdx.x % 8 * each + blockIdx.x / 8;
+  const int n0 = tile / tiles_m * C::BN, m0 = tile % tiles_m * C::BM;
+  if (tile >= tiles) return;
+
+  // the factors of the results that this wave writes, loaded before the sums
+  float fa[C::PER], bias[C::PER], fb[C::PER][4];
+#pragma unroll
+  for (int p = 0; p < C::PER; ++p) {
+    const int f = min(wave + p * WAVES, C::FRAGS - 1);
+    const int m = min(m0 + 16 * (f / NF) + rho, a.M - 1), n = n0 + 16 * (f % NF) + 4 * h;
+    fa[p] = a.a_factor ? a.a_factor[m] : 1.0f;
+    bias[p] = a.bias ? a.bias[m] : 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) fb[p][q] = a.b_factor ? a.b_factor[min(n + q, a.N - 1)] : 1.0f;
+  }
+
+  // copy j: rows 8 j .. 8 j + 7 of the stage, a's first, 128 bytes each
+  const uint8_t *row[COPIES], *scales[MF + NF];
+#pragma unroll
+  for (int j = 0; j < COPIES; ++j) {
+    const int r = 8 * j + (lane >> 3);
+    row[j] = 8 * j < C::BM ? a.a + (int64_t)min(m0 + r, a.M - 1) * a.ld_a
+                           : a.b + (int64_t)min(n0 + r - C::BM, a.N - 1) * a.ld_b;
+  }
+#pragma unroll
+  for (int f = 0; f < MF + NF; ++f)
+    scales[f] = 4 * h + (f < MF ? a.a_scale + (int64_t)min(m0 + 16 * f + rho, a.M - 1) * a.ld_sa
+                                : a.b_scale + (int64_t)min(n0 + 16 * (f - MF) + rho, a.N - 1) * a.ld_sb);
+  int chunk[2];  // the lane's, by the parity of j
+#pragma unroll
+  for (int p = 0; p < 2; ++p) chunk[p] = ((lane & 7) ^ (4 * p + (lane >> 4))) * 16;
+  const int bytes = (a.K + 1) / 2, last = (bytes - 1) / 16 * 16;
+  const int slabs = (bytes + C::ROW - 1) / C::ROW;
+  const int mine = slabs > wave ? (slabs - wave - 1) / WAVES + 1 : 0;
+  char *ring = smem + wave * (STAGES * C::STAGE);
+  const uint32_t base = lds_address(ring);
+  auto issue = [&](int i) {
+    const int slab = wave + i * WAVES;
+    const uint32_t stage = base + (uint32_t)(i % STAGES * C::STAGE);
+#pragma unroll
+    for (int j = 0; j < COPIES; ++j)
+      copy16(row[j] + min(slab * C::ROW + chunk[j & 1], last), __builtin_amdgcn_readfirstlane((int)(stage + 1024 * j)));
+#pragma unroll
+    for (int f = 0; f < MF + NF; ++f)
+      copy4(scales[f] + slab / 2 * 16, __builtin_amdgcn_readfirstlane((int)(stage + C::CODES + 256 * f)));
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i)
+    if (i < mine) issue(i);
+  f32x4_t acc[MF][NF];
+#pragma unroll
+  for (int x = 0; x < MF; ++x)
+#pragma unroll
+    for (int y = 0; y < NF; ++y) acc[x][y] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < mine; ++i) {
+    wait_stages<C::OPS>(min(mine - 1 - i, STAGES - 1));
+    const char *stage = ring + i % STAGES * C::STAGE;
+    u32x4_t xa[2][MF], xb[2][NF];
+    uint32_t sa[MF], sb[NF];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int at = rho * C::ROW + ((4 * s + h) ^ (rho >> 1)) * 16;
+#pragma unroll
+      for (int x = 0; x < MF; ++x) xa[s][x] = *reinterpret_cast<const u32x4_t *>(stage + x * 16 * C::ROW + at);
+#pragma unroll
+      for (int y = 0; y < NF; ++y) xb[s][y] = *reinterpret_cast<const u32x4_t *>(stage + (MF + y) * 16 * C::ROW + at);
+    }
+    const int slab = wave + i * WAVES;
+    const int down = slab % 2 * 16;  // an odd slab's two bytes are the upper ones
+#pragma unroll
+    for (int x = 0; x < MF; ++x) sa[x] = *reinterpret_cast<const uint32_t *>(stage + C::CODES + 256 * x + 4 * lane) >> down;
+#pragma unroll
+    for (int y = 0; y < NF; ++y) sb[y] = *reinterpret_cast<const uint32_t *>(stage + C::CODES + 256 * (MF + y) + 4 * lane) >> down;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage is read, and may be written again
+    if (i + STAGES < mine) issue(i + STAGES);
+    const int left = a.K - slab * 2 * C::ROW;
+    if (left < 2 * C::ROW) {
+      const uint32_t mask = mx4_scale_mask(left, h);
+#pragma unroll
+      for (int x = 0; x < MF; ++x) {
+        sa[x] &= mask;
+        xa[0][x] = mx4_keep(xa[0][x], left - 32 * h);
+        xa[1][x] = mx4_keep(xa[1][x], left - 128 - 32 * h);
+      }
+#pragma unroll
+      for (int y = 0; y < NF; ++y) sb[y] &= mask;
+    }
+#pragma unroll
+    for (int x = 0; x < MF; ++x)
+#pragma unroll
+      for (int y = 0; y < NF; ++y) acc[x][y] = mx4_mfma<0>(xb[0][y], xa[0][x], acc[x][y], sb[y], sa[x]);
+#pragma unroll
+    for (int x = 0; x < MF; ++x)
+#pragma unroll
+      for (int y = 0; y < NF; ++y) acc[x][y] = mx4_mfma<1>(xb[1][y], xa[1][x], acc[x][y], sb[y], sa[x]);
+  }
+  __syncthreads();  // every wave has read its stages
+  f32x4_t *sums = reinterpret_cast<f32x4_t *>(smem);
+#pragma unroll
+  for (int x = 0; x < MF; ++x)
+#pragma unroll
+    for (int y = 0; y < NF; ++y) sums[(wave * C::FRAGS + x * NF + y) * 64 + lane] = acc[x][y];
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < C::PER; ++p) {
+    const int f = wave + p * WAVES;
+    const int m = m0 + 16 * (f / NF) + rho, n = n0 + 16 * (f % NF) + 4 * h;
+    if (f >= C::FRAGS || m >= a.M || n >= a.N) continue;
+    f32x4_t s = sums[f * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) s += sums[(w * C::FRAGS + f) * 64 + lane];
+    mx4_store4<D>(static_cast<T *>(a.y) + (int64_t)m * a.ld_y, n, a.N, s, fa[p], fb[p], bias[p]);
+  }
+}
+
+// ---- launch -----------------------------------------------------------------------
+
+// The tile shapes of k_mx4_tile: rows, columns, and the time of one slab (128 elements
+// of K) per tile on a CU, in units of 10 ns.
+enum Mx4Shape { MX4_256x256, MX4_256x128, MX4_128x128, MX4_64x128, MX4_SHAPES };
+struct Mx4ShapeCost {
+  int bm, bn, slab;
+};
+constexpr Mx4ShapeCost MX4_COST[MX4_SHAPES] = {{256, 256, 80}, {256, 128, 53}, {128, 128, 30}, {64, 128, 19}};
+constexpr int MX4_TILE_COST = 250;   // of a tile besides its slabs: start, ring fill, results
+constexpr int MX4_JOIN_COST = 250;   // of the second launch
+constexpr int MX4_MAX_PARTS = 16;
+constexpr size_t MX4_MAX_PARTIAL = (size_t)64 << 20;
+
+// Those of k_mx4_small: rows, columns, workgroups that a CU holds, and the time
+// besides the loads, once and for each round of workgroups.
+enum Mx4SmallShape { MX4_16x16, MX4_16x32, MX4_32x32, MX4_32x64, MX4_64x64, MX4_SMALL_SHAPES };
+struct Mx4SmallCost {
+  int bm, bn, held, start, round;
+};
+constexpr Mx4SmallCost MX4_SMALL[MX4_SMALL_SHAPES] = {
+    {16, 16, 2, 155, 85}, {16, 32, 3, 200, 40}, {32, 32, 2, 140, 115}, {32, 64, 1, 40, 235}, {64, 64, 1, 0, 380}};
+constexpr int MX4_SMALL_RATE = 1050;  // bytes a CU loads in 10 ns
+
+struct Mx4Plan {
+  bool small;         // `shape` is an Mx4SmallShape
+  int shape;
+  int parts, k_part;  // k_mx4_tile: the ranges of K
+  size_t bytes;       // of the workspace: 0 with one range
+};
+
+static int64_t mx4_tiles(int bm, int bn, int M, int N) { return (int64_t)((M - 1) / bm + 1) * ((N - 1) / bn + 1); }
+
+// The kernel, shape and number of K ranges with the least estimated time: 256
+// CUs take the tiles in rounds; the ranges' sums are written and read once (4
+// bytes each way at about 4 TB/s), the operands read at 5 TB/s at most.
+static Mx4Plan mx4_plan(int M, int N, int K) {
+  const int ng = (K + MX4_GROUP - 1) / MX4_GROUP, row = (K + 1) / 2;
+  Mx4Plan best{false, MX4_256x256, 1, ng * MX4_GROUP, 0};
+  int64_t least = INT64_MAX;
+  const int64_t bytes = ((int64_t)M + N) * row;
+  for (int shape = 0; shape < MX4_SMALL_SHAPES; ++shape) {
+    const Mx4SmallCost &c = MX4_SMALL[shape];
+    const int64_t tiles = mx4_tiles(c.bm, c.bn, M, N);
+    const int64_t per_cu = (tiles + 255) / 256, rounds = (tiles + 256 * c.held - 1) / (256 * c.held);
+    const int64_t cost =
+        c.start + rounds * c.round + per_cu * ((int64_t)(c.bm + c.bn) * row / MX4_SMALL_RATE) + bytes / 140000;
+    if (cost < least) {
+      least = cost;
+      best = Mx4Plan{true, shape, 1, ng * MX4_GROUP, 0};
+    }
+  }
+  for (int shape = 0; shape < MX4_SHAPES; ++shape) {
+    const int64_t tiles = mx4_tiles(MX4_COST[shape].bm, MX4_COST[shape].bn, M, N);
+    for (int want = 1; want <= MX4_MAX_PARTS; want *= 2) {
+      const int per = (ng + want - 1) / want, parts = (ng + per - 1) / per;
+      const size_t sums = (size_t)parts * M * ((N + 3) / 4 * 4);
+      if (want > 1 && (parts < want || sums * 4 > MX4_MAX_PARTIAL)) break;
+      const int64_t rounds = (tiles * parts + 255) / 256;
+      const int64_t cost = std::max(rounds * (4 * per * MX4_COST[shape].slab + MX4_TILE_COST), bytes / 50000 + MX4_TILE_COST) +
+                           (parts > 1 ? MX4_JOIN_COST + (int64_t)(sums / 5000) : 0);
+      if (cost < least) {
+        least = cost;
+        best = Mx4Plan{false, shape, parts, per * MX4_GROUP, parts > 1 ? (sums * 4 + 255) / 256 * 256 : 0};
+      }
+    }
+  }
+  return best;
+}
+
+// Rows too far apart for 32-bit offsets within a tile: k_mx4_small, which has
+// 64-bit addresses, takes those.
+static bool mx4_far(const Mx4MatmulArgs &a) {
+  return std::max(a.ld_a, a.ld_b) > ((int64_t)1 << 31) / 256 - MX4_MAX_K / 2;
+}
+
+size_t mx4_matmul_workspace(int M, int N, int K) { return M <= 0 || N <= 0 ? 0 : mx4_plan(M, N, K).bytes; }
+
+template <Dt D, class Cfg, int BN, bool STREAM = false>
+static hipError_t launch_tile(const Mx4MatmulArgs &a, int parts, hipStream_t s) {
+  auto kern = k_mx4_tile<D, Cfg, BN, STREAM>;
+  constexpr int lds = Mx4Tile<Cfg, BN>::LDS;
+  hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  const int64_t tiles = mx4_tiles(Cfg::BM, BN, a.M, a.N);
+  if (tiles * parts > (int64_t)UINT32_MAX / Cfg::THREADS) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * parts)), dim3(Cfg::THREADS), lds, s, a, (int)tiles);
+  return hipGetLastError();
+}
+
+template <Dt D, int MF, int NF, int WAVES, int STAGES>
+static hipError_t launch_small(const Mx4MatmulArgs &a, hipStream_t s) {
+  using C = Mx4Small<MF, NF, WAVES, STAGES>;
+  auto kern = k_mx4_small<D, C>;
+  if constexpr (C::LDS > 64 * 1024) {
+    hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t tiles = mx4_tiles(C::BM, C::BN, a.M, a.N), wgs = (tiles + 7) / 8 * 8;
+  if (wgs > (int64_t)UINT32_MAX / C::THREADS) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(C::THREADS), C::LDS, s, a, (int)tiles);
+  return hipGetLastError();
+}
+
+// Results beyond the Infinity Cache (256 MB) are stored non-temporally, as those of
+// the 8-bit product.
+template <Dt D>
+static bool mx4_stream(const Mx4MatmulArgs &a) {
+  return (size_t)a.M * a.N * DtT<D>::size > ((size_t)256 << 20);
+}
+
+template <Dt D>
+static hipError_t matmul_dt(const Mx4MatmulArgs &args, void *workspace, hipStream_t s) {
+  Mx4MatmulArgs a = args;
+  Mx4Plan p = mx4_plan(a.M, a.N, a.K);
+  if (mx4_far(a) && !p.small) p = Mx4Plan{true, MX4_64x64, 1, 0, 0};
+  if (p.small) {
+    switch (p.shape) {
+      case MX4_16x16: return launch_small<D, 1, 1, 8, 2>(a, s);
+      case MX4_16x32: return launch_small<D, 1, 2, 4, 2>(a, s);
+      case MX4_32x32: return launch_small<D, 2, 2, 4, 2>(a, s);
+      case MX4_32x64: return launch_small<D, 2, 4, 8, 1>(a, s);
+      case MX4_64x64: return launch_small<D, 4, 4, 8, 1>(a, s);
+    }
+    return hipErrorInvalidValue;
+  }
+  a.k_part = p.k_part;
+  a.partial = p.parts > 1 ? static_cast<float *>(workspace) : nullptr;
+  hipError_t e = hipErrorInvalidValue;
+  switch (p.shape) {
+    case MX4_256x256:
+      e = mx4_stream<D>(a) ? launch_tile<D, DmaCfg<256, 8, 4>, 256, true>(a, p.parts, s)
+                           : launch_tile<D, DmaCfg<256, 8, 4>, 256>(a, p.parts, s);
+      break;
+    case MX4_256x128: e = launch_tile<D, DmaCfg<256, 8, 4>, 128>(a, p.parts, s); break;
+    case MX4_128x128: e = launch_tile<D, DmaCfg<128, 4, 4>, 128>(a, p.parts, s); break;
+    case MX4_64x128: e = launch_tile<D, DmaCfg<64, 4, 4>, 128>(a, p.parts, s); break;
+  }
+  if (e != hipSuccess || p.parts == 1) return e;
+  const dim3 grid((unsigned)((a.N - 1) / 1024 + 1), (unsigned)std::min(a.M, 1 << 15));
+  hipLaunchKernelGGL(k_mx4_join<D>, grid, dim3(256), 0, s, a, p.parts);
+  return hipGetLastError();
+}
 
 hipError_t mx4_matmul(const Mx4MatmulArgs &a, void *workspace, hipStream_t s) {
   if (a.M <= 0 || a.N <= 0) return hipSuccess;
-  const int64_t tiles = (int64_t)((a.M - 1) / 16 + 1) * ((a.N - 1) / 16 + 1);
-  if (tiles > (int64_t)UINT32_MAX / 64) return hipErrorInvalidValue;
-  if (a.dtype == Dt::BF16)
-    hipLaunchKernelGGL(k_mx4_simple<Dt::BF16>, dim3((unsigned)tiles), dim3(64), 0, s, a);
-  else
-    hipLaunchKernelGGL(k_mx4_simple<Dt::F32>, dim3((unsigned)tiles), dim3(64), 0, s, a);
-  return hipGetLastError();
+  return a.dtype == Dt::BF16 ? matmul_dt<Dt::BF16>(a, workspace, s) : matmul_dt<Dt::F32>(a, workspace, s);
 }
 
 }  // namespace twell

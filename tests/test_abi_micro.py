@@ -127,6 +127,15 @@ def test_product_workspace():
     for M, N, K in [(0, 5, 5), (5, 0, 5), (5, 5, 0), (-1, 5, 5), (5, 5, (1 << 20) + 1), ((1 << 26) + 1, 1, 32),
                     (1 << 40, 5, 5)]:
         assert size(M, N, K) == 0
+    # some product is cut into ranges of K, and refuses less
+    M, N, K = next((m, n, k) for m in (512, 1024, 256, 300) for n in (512, 1024, 300) for k in (65536, 1 << 18, 1 << 20)
+                   if size(m, n, k) > 0)
+    a, b = _q(rows=M, cols=K, ld=K // 2, ld_scale=K // 32), _q(rows=N, cols=K, ld=K // 2, ld_scale=K // 32)
+    need = size(M, N, K)
+    assert need % 256 == 0 and need <= 64 << 20
+    assert product(a, b, ld_y=N, n=need - 1) == WORKSPACE
+    assert product(a, b, ld_y=N, ws=None) == WORKSPACE
+    assert product(a, b, ld_y=N, ws=FAKE + 16, n=need) == UNSUPPORTED
 
 
 def _t(n=100, weight=FAKE, master=None, grad=FAKE, m=FAKE, v=FAKE, ms=None, vs=None, dtype=F32, gdtype=F32, decay=0.1):
