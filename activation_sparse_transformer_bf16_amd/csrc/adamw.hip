@@ -72,8 +72,9 @@ __device__ __forceinline__ uint32_t quad_top(uint32_t v) {
 
 // ---- lists of tensors -----------------------------------------------------------
 
-constexpr int STEP_WAVES = 4, STEP_EACH = 8;                 // elements per lane
-constexpr int STEP_CHUNK = 64 * STEP_WAVES * STEP_EACH;      // elements per workgroup
+constexpr int STEP_WAVES = 4, STEP_EACH = 8;             // waves of a workgroup, elements of a lane
+constexpr int STEP_CHUNK = 64 * STEP_WAVES * STEP_EACH;  // elements of a workgroup
+constexpr int STEP_WGS = 2048;                           // eight workgroups per CU, which take chunks in turn
 
 // Tensors of one launch and the number of their first chunk; by value, so that
 // nothing has to be copied to the GPU before it.
@@ -85,21 +86,99 @@ struct List {
   T t[MAX];
 };
 
-// The tensor that holds chunk c.
+// The list's first chunks, one per lane: which tensor a chunk belongs to is then one
+// comparison for all of them, with no walk through memory.
 template <class T, int MAX>
-__device__ __forceinline__ int list_find(const List<T, MAX> &l, int64_t c) {
-  int i = 0;
-  while (i + 1 < l.count && l.first[i + 1] <= c) ++i;
-  return i;
-}
+struct Finder {
+  static constexpr int N = (MAX + 63) / 64;
+  int64_t first[N];
+  __device__ __forceinline__ explicit Finder(const List<T, MAX> &l) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 0; k < N; ++k) first[k] = lane + 64 * k < l.count ? l.first[min(lane + 64 * k, MAX - 1)] : INT64_MAX;
+  }
+  // The last tensor that starts at or before chunk c: of several without an element,
+  // all of which start there, the one that has some.
+  __device__ __forceinline__ int operator()(int64_t c) const {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) n += popc64(ballot(first[k] <= c));
+    return __builtin_amdgcn_readfirstlane(n - 1);
+  }
+};
 
-// E elements from p on, of which `left` are the tensor's; aligned to the element only.
-template <Dt D, int E>
-__device__ __forceinline__ void load_elements(const void *p, int64_t at, int64_t left, float (&v)[E]) {
+// 16 bytes at any alignment.
+typedef uint32_t u32x4_free_t __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_free_t __attribute__((ext_vector_type(2), aligned(1)));
+
+// 8 elements from p + at on.  WHOLE: all there are the tensor's; otherwise `left` of
+// them, and zeros.
+template <Dt D, bool WHOLE>
+__device__ __forceinline__ void load8(const void *p, int64_t at, int64_t left, float (&v)[8]) {
   using T = typename DtT<D>::T;
   const T *q = static_cast<const T *>(p) + at;
+  if constexpr (!WHOLE) {
 #pragma unroll
-  for (int i = 0; i < E; ++i) v[i] = i < left ? to_f32(q[i]) : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(q[i]) : 0.0f;
+  } else if constexpr (D == Dt::BF16) {
+    const u32x4_t w = *reinterpret_cast<const u32x4_free_t *>(q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i % 2 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+  } else {
+    const u32x4_t a = *reinterpret_cast<const u32x4_free_t *>(q), b = *reinterpret_cast<const u32x4_free_t *>(q + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i < 4 ? a[i] : b[i - 4]);
+  }
+}
+template <bool WHOLE>
+__device__ __forceinline__ u32x2_t load8_codes(const uint8_t *p, int64_t left) {
+  if constexpr (WHOLE) return *reinterpret_cast<const u32x2_free_t *>(p);
+  u32x2_t c = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < left) c[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+  return c;
+}
+// 8 elements' bits: fp32, or bf16 in the low halves.
+template <Dt D, bool WHOLE>
+__device__ __forceinline__ void store8(void *p, int64_t at, int64_t left, const uint32_t (&v)[8]) {
+  using T = typename DtT<D>::T;
+  T *q = static_cast<T *>(p) + at;
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= left) break;
+      if constexpr (D == Dt::BF16)
+        q[i] = (uint16_t)v[i];
+      else
+        q[i] = __uint_as_float(v[i]);
+    }
+  } else if constexpr (D == Dt::BF16) {
+    u32x4_t w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x05040100u);
+    *reinterpret_cast<u32x4_free_t *>(q) = w;
+  } else {
+    *reinterpret_cast<u32x4_free_t *>(q) = u32x4_t{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<u32x4_free_t *>(q + 4) = u32x4_t{v[4], v[5], v[6], v[7]};
+  }
+}
+template <Dt D, bool WHOLE>
+__device__ __forceinline__ void store8_f32(void *p, int64_t at, int64_t left, const float (&v)[8]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = D == Dt::BF16 ? (uint32_t)bf16_rne(v[i]) : __float_as_uint(v[i]);
+  store8<D, WHOLE>(p, at, left, w);
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store8_codes(uint8_t *p, int64_t left, u32x2_t c) {
+  if constexpr (WHOLE) {
+    *reinterpret_cast<u32x2_free_t *>(p) = c;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = (uint8_t)(c[i / 4] >> (8 * (i % 4)));
+  }
 }
 
 // ---- the step ----------------------------------------------------------------------
@@ -116,105 +195,129 @@ struct StepScalars {
 
 using StepList = List<AdamWTensor, ADAMW_LIST>;
 
-template <Dt W, Dt G, bool BITS8, bool MASTER>
-__global__ __launch_bounds__(64 * STEP_WAVES) void k_adamw(StepList list, StepScalars c) {
+// A step's numbers, the same for all tensors.
+struct StepNow {
+  float factor, rate, root;
+  double lr;
+  uint32_t key;
+};
+
+// One lane's 8 elements.
+template <Dt W, Dt G, bool BITS8, bool MASTER, bool WHOLE>
+__device__ __forceinline__ void step8(const AdamWTensor &t, int64_t e0, const StepScalars &c, const StepNow &now) {
 #pragma clang fp contract(off)
-  constexpr int E = STEP_EACH;
-  using T = typename DtT<W>::T;
-  const float factor = c.clip != nullptr ? c.clip[1] : 1.0f;
-  if (!(fabsf(factor) <= 3.0e38f)) return;  // gradients with inf or NaN: the step is left out
-  const int64_t step = c.step_device != nullptr ? *c.step_device : c.step;
-  if (step < 1) return;
-  const double lr = c.lr_device != nullptr ? (double)*c.lr_device : c.lr;
-  const float rate = (float)(lr / -expm1((double)step * c.log1));
-  const float root = (float)(1.0 / sqrt(-expm1((double)step * c.log2)));
-  const uint64_t seed = c.seed + (uint64_t)step;
-  const uint32_t key0 = mix32((uint32_t)seed ^ mix32((uint32_t)(seed >> 32)));
-  for (int64_t chunk = blockIdx.x; chunk < list.chunks; chunk += gridDim.x) {
-    const int at = list_find(list, chunk);
-    const AdamWTensor &t = list.t[at];
-    const int64_t e0 = (chunk - list.first[at]) * STEP_CHUNK + threadIdx.x * E;
-    const int64_t left = t.n - e0;
-    const uint64_t group = (uint64_t)e0 / 8;
-    const uint32_t key = mix32(key0 + (uint32_t)t.place) + (uint32_t)(group >> 32) * 0x9E3779B1u;
-    const uint32_t base = mix32((uint32_t)group + key);
-    float g[E], m[E], v[E], w[E];
-    uint32_t random[E];
-    load_elements<G>(t.grad, e0, left, g);
-    if (MASTER)
-      load_elements<Dt::F32>(t.master, e0, left, w);
-    else
-      load_elements<W>(t.weight, e0, left, w);
-    if constexpr (BITS8) {
-      const uint8_t *mc = static_cast<const uint8_t *>(t.m) + e0, *vc = static_cast<const uint8_t *>(t.v) + e0;
-      const float mu = left > 0 ? state_unit(t.m_scale[e0 / STATE_BLOCK], M_TOP) : 0.0f;
-      const float vu = left > 0 ? state_unit(t.v_scale[e0 / STATE_BLOCK], V_TOP) : 0.0f;
+  const int64_t left = t.n - e0;
+  float g[8], m[8], v[8], w[8];
+  load8<G, WHOLE>(t.grad, e0, left, g);
+  if constexpr (MASTER)
+    load8<Dt::F32, WHOLE>(t.master, e0, left, w);
+  else
+    load8<W, WHOLE>(t.weight, e0, left, w);
+  uint8_t *mc = static_cast<uint8_t *>(t.m) + e0, *vc = static_cast<uint8_t *>(t.v) + e0;
+  const int64_t block = e0 / STATE_BLOCK;
+  if constexpr (BITS8) {
+    const u32x2_t a = load8_codes<WHOLE>(mc, left), b = load8_codes<WHOLE>(vc, left);
+    const bool some = WHOLE || left > 0;
+    const float mu = state_unit(some ? t.m_scale[block] : 0u, M_TOP), vu = state_unit(some ? t.v_scale[block] : 0u, V_TOP);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const uint32_t a = i < left ? mc[i] : 0u, b = i < left ? vc[i] : 0u;
-        const float x = state_value(a & 127u, mu);
-        m[i] = a & 128u ? -x : x;
-        v[i] = state_value(b, vu);
-      }
-    } else {
-      load_elements<Dt::F32>(t.m, e0, left, m);
-      load_elements<Dt::F32>(t.v, e0, left, v);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x = a[i / 4] >> (8 * (i % 4));
+      m[i] = state_value(x & 127u, mu);
+      m[i] = __uint_as_float(__float_as_uint(m[i]) | (x & 128u) << 24);
+      v[i] = state_value(b[i / 4] >> (8 * (i % 4)) & 255u, vu);
     }
-    const float keep = (float)(1.0 - lr * (double)t.decay);
+  } else {
+    load8<Dt::F32, WHOLE>(t.m, e0, left, m);
+    load8<Dt::F32, WHOLE>(t.v, e0, left, v);
+  }
+  const float keep = (float)(1.0 - now.lr * (double)t.decay);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float x = g[i] * factor;
-      m[i] = m[i] * c.beta1 + x * c.rest1;
-      v[i] = v[i] * c.beta2 + (x * c.rest2) * x;
-      const float denom = sqrtf(v[i]) * root + c.eps;
-      w[i] = w[i] * keep - rate * (m[i] / denom);
+  for (int i = 0; i < 8; ++i) {
+    const float x = g[i] * now.factor;
+    m[i] = m[i] * c.beta1 + x * c.rest1;
+    v[i] = v[i] * c.beta2 + (x * c.rest2) * x;
+    // the root and the reciprocal to 1 ulp each, as the instructions give them
+    const float denom = __builtin_amdgcn_sqrtf(v[i]) * now.root + c.eps;
+    w[i] = w[i] * keep - now.rate * (m[i] * __builtin_amdgcn_rcpf(denom));
+  }
+  uint32_t random[8];
+  if constexpr (BITS8 || (W == Dt::BF16 && !MASTER)) {
+    const uint64_t group = (uint64_t)e0 / 8;
+    const uint32_t key = mix32(now.key + (uint32_t)t.place) + (uint32_t)(group >> 32) * 0x9E3779B1u;
+    const uint32_t base = mix32((uint32_t)group + key);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
       random[i] = (base + (uint32_t)i * 0x9E3779B9u) * 0x85EBCA6Bu;
       random[i] ^= random[i] >> 16;
     }
-    if constexpr (BITS8) {
-      uint32_t mt = 0, vt = 0;
+  }
+  if constexpr (BITS8) {
+    uint32_t mt = 0, vt = 0;
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (i >= left) continue;
-        mt = max(mt, __float_as_uint(m[i]) & 0x7FFFFFFFu);
-        vt = max(vt, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-      }
-      const uint32_t ms = state_scale(quad_top(mt)), vs = state_scale(quad_top(vt));
-      const float md = pow2(M_TOP + 100 - min((int)ms, E_MAX)), vd = pow2(V_TOP + 100 - min((int)vs, E_MAX));
-      uint8_t *mc = static_cast<uint8_t *>(t.m) + e0, *vc = static_cast<uint8_t *>(t.v) + e0;
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (i >= left) break;
-        const uint32_t a = state_code(fabsf(m[i]), md, random[i] & 0xFFFFu);
-        const uint32_t b = max(state_code(v[i], vd, random[i] >> 16), v[i] > 0.0f ? 1u : 0u);
-        mc[i] = ms == 255u ? 0 : (uint8_t)(a | (__float_as_uint(m[i]) >> 31) << 7);
-        vc[i] = vs == 255u ? 0 : (uint8_t)b;
-      }
-      if (threadIdx.x % 4 == 0 && left > 0) {
-        t.m_scale[e0 / STATE_BLOCK] = (uint8_t)ms;
-        t.v_scale[e0 / STATE_BLOCK] = (uint8_t)vs;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (i >= left) break;
-        static_cast<float *>(t.m)[e0 + i] = m[i];
-        static_cast<float *>(t.v)[e0 + i] = v[i];
-      }
+    for (int i = 0; i < 8; ++i) {
+      mt = max(mt, __float_as_uint(m[i]) & 0x7FFFFFFFu);
+      vt = max(vt, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     }
+    const uint32_t ms = state_scale(quad_top(mt)), vs = state_scale(quad_top(vt));
+    const float md = pow2(M_TOP + 100 - min((int)ms, E_MAX)), vd = pow2(V_TOP + 100 - min((int)vs, E_MAX));
+    u32x2_t a = {0u, 0u}, b = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      if (i >= left) break;
-      if (MASTER) t.master[e0 + i] = w[i];
-      if constexpr (W == Dt::BF16 && !MASTER) {
-        const uint32_t bits = __float_as_uint(w[i]);
-        const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
-        static_cast<T *>(t.weight)[e0 + i] =
-            finite ? (uint16_t)((bits + ((random[i] >> 8) & 0xFFFFu)) >> 16) : from_f32<W>(w[i]);
-      } else {
-        static_cast<T *>(t.weight)[e0 + i] = from_f32<W>(w[i]);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x = state_code(fabsf(m[i]), md, random[i] & 0xFFFFu) | (__float_as_uint(m[i]) >> 31) << 7;
+      const uint32_t y = max(state_code(v[i], vd, random[i] >> 16), v[i] > 0.0f ? 1u : 0u);
+      a[i / 4] |= x << (8 * (i % 4));
+      b[i / 4] |= y << (8 * (i % 4));
     }
+    if (ms == 255u) a = u32x2_t{0u, 0u};
+    if (vs == 255u) b = u32x2_t{0u, 0u};
+    store8_codes<WHOLE>(mc, left, a);
+    store8_codes<WHOLE>(vc, left, b);
+    if (threadIdx.x % 4 == 0 && (WHOLE || left > 0)) {
+      t.m_scale[block] = (uint8_t)ms;
+      t.v_scale[block] = (uint8_t)vs;
+    }
+  } else {
+    store8_f32<Dt::F32, WHOLE>(t.m, e0, left, m);
+    store8_f32<Dt::F32, WHOLE>(t.v, e0, left, v);
+  }
+  if constexpr (MASTER) store8_f32<Dt::F32, WHOLE>(t.master, e0, left, w);
+  if constexpr (W == Dt::BF16 && !MASTER) {
+    uint32_t bits[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      bits[i] = __float_as_uint(w[i]);
+      // infinities and NaN as they are: the addition would carry through them
+      const bool finite = (bits[i] & 0x7F800000u) != 0x7F800000u;
+      bits[i] = finite ? (bits[i] + (random[i] >> 8 & 0xFFFFu)) >> 16 : (uint32_t)bf16_rne(w[i]);
+    }
+    store8<W, WHOLE>(t.weight, e0, left, bits);
+  } else {
+    store8_f32<W, WHOLE>(t.weight, e0, left, w);
+  }
+}
+
+template <Dt W, Dt G, bool BITS8, bool MASTER>
+__global__ __launch_bounds__(64 * STEP_WAVES) void k_adamw(StepList list, StepScalars c) {
+  StepNow now;
+  now.factor = c.clip != nullptr ? c.clip[1] : 1.0f;
+  if (!(fabsf(now.factor) <= 3.0e38f)) return;  // gradients with inf or NaN: the step is left out
+  const int64_t step = c.step_device != nullptr ? *c.step_device : c.step;
+  if (step < 1) return;
+  now.lr = c.lr_device != nullptr ? (double)*c.lr_device : c.lr;
+  now.rate = (float)(now.lr / -expm1((double)step * c.log1));
+  now.root = (float)(1.0 / sqrt(-expm1((double)step * c.log2)));
+  const uint64_t seed = c.seed + (uint64_t)step;
+  now.key = mix32((uint32_t)seed ^ mix32((uint32_t)(seed >> 32)));
+  const Finder<AdamWTensor, ADAMW_LIST> find(list);
+  for (int64_t chunk = blockIdx.x; chunk < list.chunks; chunk += gridDim.x) {
+    const int at = find(chunk);
+    const AdamWTensor &t = list.t[at];
+    const int64_t start = (chunk - list.first[at]) * STEP_CHUNK;
+    const int64_t e0 = start + threadIdx.x * STEP_EACH;
+    if (start + STEP_CHUNK <= t.n)
+      step8<W, G, BITS8, MASTER, true>(t, e0, c, now);
+    else
+      step8<W, G, BITS8, MASTER, false>(t, e0, c, now);
   }
 }
 
@@ -234,7 +337,7 @@ template <Dt W, Dt G, bool BITS8, bool MASTER>
 static hipError_t launch_step(const AdamWTensor *t, int count, const StepScalars &c, hipStream_t s) {
   StepList l{};
   if (list_fill(l, t, count, STEP_CHUNK, [](const AdamWTensor &x) { return x.n; }) == 0) return hipSuccess;
-  const dim3 grid((unsigned)std::min<int64_t>(l.chunks, 1 << 20));
+  const dim3 grid((unsigned)std::min<int64_t>(l.chunks, STEP_WGS));
   hipLaunchKernelGGL((k_adamw<W, G, BITS8, MASTER>), grid, dim3(64 * STEP_WAVES), 0, s, l, c);
   return hipGetLastError();
 }
@@ -267,20 +370,28 @@ using ReadList = List<StateRead, STATE_LIST>;
 
 template <Dt D>
 __global__ __launch_bounds__(64 * STEP_WAVES) void k_state_read(ReadList list) {
+  const Finder<StateRead, STATE_LIST> find(list);
   for (int64_t chunk = blockIdx.x; chunk < list.chunks; chunk += gridDim.x) {
-    const int at = list_find(list, chunk);
+    const int at = find(chunk);
     const StateRead &t = list.t[at];
-    const int64_t e0 = (chunk - list.first[at]) * STEP_CHUNK + threadIdx.x * STEP_EACH;
-    const int64_t left = t.n - e0;
+    const int64_t start = (chunk - list.first[at]) * STEP_CHUNK;
+    const int64_t e0 = start + threadIdx.x * STEP_EACH, left = t.n - e0;
     if (left <= 0) continue;
+    const bool whole = start + STEP_CHUNK <= t.n;
     const float unit = state_unit(t.scale[e0 / STATE_BLOCK], t.is_signed ? M_TOP : V_TOP);
+    const uint32_t sign = t.is_signed ? 128u : 0u;
+    const u32x2_t c = whole ? load8_codes<true>(t.code + e0, left) : load8_codes<false>(t.code + e0, left);
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < STEP_EACH; ++i) {
-      if (i >= left) break;
-      const uint32_t c = t.code[e0 + i];
-      const float x = state_value(t.is_signed ? c & 127u : c, unit);
-      static_cast<typename DtT<D>::T *>(t.out)[e0 + i] = from_f32<D>(t.is_signed && (c & 128u) ? -x : x);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = c[i / 4] >> (8 * (i % 4)) & 255u;
+      x[i] = state_value(b & ~sign, unit);
+      x[i] = __uint_as_float(__float_as_uint(x[i]) | (b & sign) << 24);
     }
+    if (whole)
+      store8_f32<D, true>(t.out, e0, left, x);
+    else
+      store8_f32<D, false>(t.out, e0, left, x);
   }
 }
 
@@ -289,7 +400,7 @@ hipError_t state_read(const StateRead *r, int count, Dt dtype, hipStream_t s) {
   ReadList l{};
   const int64_t chunks = list_fill(l, r, count, STEP_CHUNK, [](const StateRead &x) { return x.n; });
   if (chunks == 0) return hipSuccess;
-  const dim3 grid((unsigned)std::min<int64_t>(chunks, 1 << 20)), block(64 * STEP_WAVES);
+  const dim3 grid((unsigned)std::min<int64_t>(chunks, STEP_WGS)), block(64 * STEP_WAVES);
   if (dtype == Dt::BF16)
     hipLaunchKernelGGL(k_state_read<Dt::BF16>, grid, block, 0, s, l);
   else
@@ -317,20 +428,35 @@ __device__ __forceinline__ double block_sum(double v, double *buf) {
   return v;
 }
 
+template <Dt D, bool WHOLE>
+__device__ __forceinline__ double squares8(const void *p, int64_t at, int64_t left) {
+  float x[8];
+  load8<D, WHOLE>(p, at, left, x);
+  double s[2] = {0.0, 0.0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i % 2] = fma((double)x[i], (double)x[i], s[i % 2]);
+  return s[0] + s[1];
+}
+
 __global__ __launch_bounds__(64 * STEP_WAVES) void k_grad_squares(GradList list, double *partial) {
   __shared__ double buf[STEP_WAVES];
+  const Finder<GradRef, GRAD_LIST> find(list);
   double sum = 0.0;
   for (int64_t chunk = blockIdx.x; chunk < list.chunks; chunk += gridDim.x) {
-    const int at = list_find(list, chunk);
+    const int at = find(chunk);
     const GradRef &t = list.t[at];
-    const int64_t e0 = (chunk - list.first[at]) * GRAD_CHUNK + threadIdx.x * 16;
+    const int64_t start = (chunk - list.first[at]) * GRAD_CHUNK;
+    const int64_t e0 = start + threadIdx.x * 8;
+    double s[2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (e0 + i >= t.n) break;
-      const double x = t.dtype == Dt::BF16 ? (double)to_f32(static_cast<const uint16_t *>(t.p)[e0 + i])
-                                           : (double)static_cast<const float *>(t.p)[e0 + i];
-      sum += x * x;
+    for (int k = 0; k < 2; ++k) {
+      const int64_t e = e0 + k * (64 * STEP_WAVES * 8);
+      if (start + GRAD_CHUNK <= t.n)
+        s[k] = t.dtype == Dt::BF16 ? squares8<Dt::BF16, true>(t.p, e, 8) : squares8<Dt::F32, true>(t.p, e, 8);
+      else
+        s[k] = t.dtype == Dt::BF16 ? squares8<Dt::BF16, false>(t.p, e, t.n - e) : squares8<Dt::F32, false>(t.p, e, t.n - e);
     }
+    sum += s[0] + s[1];
   }
   sum = block_sum(sum, buf);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;

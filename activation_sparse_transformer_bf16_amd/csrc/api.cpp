@@ -959,6 +959,7 @@ constexpr int64_t ADAMW_MAX_N = (int64_t)1 << 40;
 twell_status check_mx4(const char *name, const twell_mx4 *q) {
   if (q == nullptr) return fail(TWELL_ERR_INVALID_ARG, "null %s", name);
   if (q->rows < 0 || q->cols <= 0) return fail(TWELL_ERR_INVALID_ARG, "%s: need rows >= 0 and cols > 0", name);
+  if (q->cols > MX4_MAX_COLS) return fail(TWELL_ERR_UNSUPPORTED, "%s: %d columns not built (at most %d)", name, q->cols, MX4_MAX_COLS);
   const int codes = q->cols / 2 + q->cols % 2, blocks = (q->cols - 1) / MX4_BLOCK + 1;
   twell_status st = check_rows(name, q->q, q->ld, codes, 1, q->rows);
   if (st != TWELL_OK) return st;

@@ -362,6 +362,7 @@ hipError_t int8_matmul(const Int8Args &a, void *workspace, hipStream_t s);
 
 // Rows of microscaled 4-bit floats (mx4.hpp): x -> q and scale, or q, scale and
 // factor -> y.
+constexpr int MX4_MAX_COLS = 1 << 30;
 struct Mx4Args {
   Dt dtype;              // of x, y
   int rows, cols;

@@ -46,6 +46,27 @@ constexpr int NON_TEMPORAL = 2;
 __device__ __forceinline__ void keep_offset(uint32_t &at) { asm volatile("" : "+v"(at)); }
 
 typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+
+// A chunk without its first n bytes (a multiple of the element's size S), zeros
+// behind the others.
+template <int S>
+__device__ __forceinline__ u32x4_t drop_bytes(u32x4_t w, int n) {
+  u32x4_t v = w;
+  if constexpr (S == 2) {
+    const bool half = (n & 2) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = half ? (v[i] >> 16) | (i < 3 ? w[i < 3 ? i + 1 : 3] << 16 : 0u) : v[i];
+  }
+  const bool one = (n & 4) != 0, two = (n & 8) != 0, all = n >= 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = one ? (i < 3 ? v[i < 3 ? i + 1 : 3] : 0u) : v[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = two ? (i < 2 ? w[i < 2 ? i + 2 : 3] : 0u) : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = all ? 0u : w[i];
+  return w;
+}
+
 template <Dt D, Rows R, bool NT = false>
 struct Row {
   using T = typename DtT<D>::T;
@@ -88,20 +109,7 @@ struct Row {
   __device__ __forceinline__ u32x4_t trim(u32x4_t w, int e0) const {
     if constexpr (R == Rows::ANY) {
       if (__builtin_amdgcn_readfirstlane(e0) + 64 * E > d) {  // the wave's chunks reach the end
-        const int n = max(e0 - (d - E), 0) * (int)sizeof(T);  // bytes to move by
-        u32x4_t v = w;
-        if constexpr (sizeof(T) == 2) {
-          const bool half = (n & 2) != 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = half ? (v[i] >> 16) | (i < 3 ? w[i < 3 ? i + 1 : 3] << 16 : 0u) : v[i];
-        }
-        const bool one = (n & 4) != 0, two = (n & 8) != 0, all = n >= 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = one ? (i < 3 ? v[i < 3 ? i + 1 : 3] : 0u) : v[i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = two ? (i < 2 ? w[i < 2 ? i + 2 : 3] : 0u) : w[i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = all ? 0u : w[i];
+        w = drop_bytes<(int)sizeof(T)>(w, max(e0 - (d - E), 0) * (int)sizeof(T));
       }
     }
     return w;

@@ -595,6 +595,7 @@ twell_status twell_int8_matmul(const twell_int8 *a, const twell_int8 *b, const f
  * groups of 16 bytes, each transposed as a 4 x 4 matrix, which is how the matrix
  * cores read them.
  * factor: one fp32 value per row that multiplies all of it, or NULL for 1.
+ * cols: at most 2^30.
  * q and scale are 16-byte aligned, ld and ld_scale multiples of 16; the bytes up
  * to the next multiple of 16 behind a row's codes and scales are READABLE
  * (buffers of rows * ld and rows * ld_scale bytes are enough).  Those past
@@ -620,7 +621,7 @@ typedef struct {
  * (Elements over 3.5 * 2^126 have 2^128 as their nearest value, which is read as
  * infinite.)  out->factor has to be NULL.
  * Errors: INVALID_ARG (NULL pointers, sizes, strides, a factor), UNSUPPORTED
- * (alignment), HIP.
+ * (alignment, cols), HIP.
  */
 twell_status twell_quantize_mx4(const void *x, int64_t ld_x, twell_dtype dtype, const twell_mx4 *out, void *stream);
 

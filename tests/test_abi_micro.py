@@ -30,6 +30,7 @@ BAD_ROWS = [
     (dict(cols=513, ld=256), INVALID),      # 257 bytes
     (dict(ld=264), UNSUPPORTED),            # not a multiple of 16
     (dict(ld=1 << 50), INVALID),
+    (dict(cols=(1 << 30) + 1, ld=1 << 30, ld_scale=1 << 26), UNSUPPORTED),
     (dict(q=None), INVALID),
     (dict(q=FAKE + 8), UNSUPPORTED),
     (dict(ld_scale=0), INVALID),
@@ -66,7 +67,7 @@ def test_rows_validation(kw, status):
     assert product(a=_q(**kw)) == status and product(b=_q(**kw)) == status
     if "factor" not in kw:
         assert quantize(out=_q(**kw)) == status
-    if "rows" not in kw and "cols" not in kw:
+    if "rows" not in kw and "cols" not in kw:  # the norm's own sizes come first
         assert norm(q=_q(**{"factor": FAKE, **kw})) == status
 
 
