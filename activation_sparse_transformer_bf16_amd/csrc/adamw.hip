@@ -40,28 +40,21 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// 2^e for the exponents of normal numbers.
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-
 // Codes are the top bits of an fp32 number whose exponent field is the code's own,
-// subnormal where the code is.  Such numbers are below 2^-90, so the scale comes
-// in two factors: 2^100, which is exact, and the rest.
-__device__ __forceinline__ float state_unit(uint32_t byte, int top) {
-  return byte > (uint32_t)E_MAX ? __uint_as_float(0x7FC00000u) : pow2(max((int)byte, E_MIN) - top - 100);
-}
-__device__ __forceinline__ float state_value(uint32_t code, float unit) {
-  return __uint_as_float(code << 20) * 0x1p100f * unit;
-}
+// subnormal where the code is, so that v_ldexp_f32 (one rounding, subnormal numbers
+// kept) takes a code to its value and back.  The exponent to add to a code:
+__device__ __forceinline__ int state_exponent(uint32_t byte, int top) { return max((int)byte, E_MIN) - top; }
+__device__ __forceinline__ bool state_is_nan(uint32_t byte) { return byte > (uint32_t)E_MAX; }
 // The scale byte of a block whose largest magnitude has these bits.
 __device__ __forceinline__ uint32_t state_scale(uint32_t top_bits) {
   const uint32_t e = (top_bits + 0xFFFFFu) >> 23;
   return e > (uint32_t)E_MAX ? 255u : max(e, (uint32_t)E_MIN);
 }
-// A magnitude to its code; `down` = 2^(top + 100 - E).  The dropped 20 bits plus
-// 16 random ones (and half of the last one's step) carry into the code.
-__device__ __forceinline__ uint32_t state_code(float x, float down, uint32_t random16) {
-  const float y = x * down * 0x1p-100f;
-  return (__float_as_uint(y) + (random16 << 4 | 8u)) >> 20;
+// The bits of x scaled down to its code, which the dropped 20 bits plus 16 random ones
+// (and half of the last one's step) carry into; the code is bits 20 to 27, the sign
+// stays in bit 31.
+__device__ __forceinline__ uint32_t state_bits(float x, int exponent, uint32_t random16) {
+  return __float_as_uint(__builtin_amdgcn_ldexpf(x, -exponent)) + (random16 << 4 | 8u);
 }
 
 // The largest of v over the 4 lanes (8 elements each) of a block.
@@ -74,7 +67,7 @@ __device__ __forceinline__ uint32_t quad_top(uint32_t v) {
 
 constexpr int STEP_WAVES = 4, STEP_EACH = 8;             // waves of a workgroup, elements of a lane
 constexpr int STEP_CHUNK = 64 * STEP_WAVES * STEP_EACH;  // elements of a workgroup
-constexpr int STEP_WGS = 2048;                           // eight workgroups per CU, which take chunks in turn
+constexpr int STEP_WGS = 1 << 20;                        // workgroups, which take more chunks in turn
 
 // Tensors of one launch and the number of their first chunk; by value, so that
 // nothing has to be copied to the GPU before it.
@@ -181,10 +174,23 @@ __device__ __forceinline__ void store8_codes(uint8_t *p, int64_t left, u32x2_t c
   }
 }
 
+// The bits of byte i's code as state_exponent() takes them.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t code_at(uint32_t c, int i) {
+  const uint32_t at20 = i < 3 ? c << (20 - 8 * i) : c >> 4;
+  return SIGNED ? (at20 & 0x07F00000u) | (c << (24 - 8 * i) & 0x80000000u) : at20 & 0x0FF00000u;
+}
+// The topmost bytes of four numbers, the first one lowest.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0C0C0703u), hi = __builtin_amdgcn_perm(d, c, 0x07030C0Cu);
+  return lo | hi;
+}
+
 // ---- the step ----------------------------------------------------------------------
 
 struct StepScalars {
   float beta1, rest1, beta2, rest2, eps;  // rest: 1 - beta
+  float rate, root;                       // with lr and step from the host
   double lr, log1, log2;                  // logarithms of the betas
   int64_t step;
   uint64_t seed;
@@ -194,6 +200,10 @@ struct StepScalars {
 };
 
 using StepList = List<AdamWTensor, ADAMW_LIST>;
+
+// lr / (1 - beta1^t) and 1 / sqrt(1 - beta2^t); log = log(beta)
+__host__ __device__ inline float step_rate(double lr, int64_t t, double log1) { return (float)(lr / -expm1((double)t * log1)); }
+__host__ __device__ inline float step_root(int64_t t, double log2) { return (float)(1.0 / sqrt(-expm1((double)t * log2))); }
 
 // A step's numbers, the same for all tensors.
 struct StepNow {
@@ -218,13 +228,19 @@ __device__ __forceinline__ void step8(const AdamWTensor &t, int64_t e0, const St
   if constexpr (BITS8) {
     const u32x2_t a = load8_codes<WHOLE>(mc, left), b = load8_codes<WHOLE>(vc, left);
     const bool some = WHOLE || left > 0;
-    const float mu = state_unit(some ? t.m_scale[block] : 0u, M_TOP), vu = state_unit(some ? t.v_scale[block] : 0u, V_TOP);
+    const uint32_t mb = some ? t.m_scale[block] : 0u, vb = some ? t.v_scale[block] : 0u;
+    const int me = state_exponent(mb, M_TOP), ve = state_exponent(vb, V_TOP);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t x = a[i / 4] >> (8 * (i % 4));
-      m[i] = state_value(x & 127u, mu);
-      m[i] = __uint_as_float(__float_as_uint(m[i]) | (x & 128u) << 24);
-      v[i] = state_value(b[i / 4] >> (8 * (i % 4)) & 255u, vu);
+      m[i] = __builtin_amdgcn_ldexpf(__uint_as_float(code_at<true>(a[i / 4], i % 4)), me);
+      v[i] = __builtin_amdgcn_ldexpf(__uint_as_float(code_at<false>(b[i / 4], i % 4)), ve);
+    }
+    if (__builtin_expect(state_is_nan(mb) || state_is_nan(vb), 0)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (state_is_nan(mb)) m[i] = __uint_as_float(0x7FC00000u);
+        if (state_is_nan(vb)) v[i] = __uint_as_float(0x7FC00000u);
+      }
     }
   } else {
     load8<Dt::F32, WHOLE>(t.m, e0, left, m);
@@ -237,39 +253,52 @@ __device__ __forceinline__ void step8(const AdamWTensor &t, int64_t e0, const St
     m[i] = m[i] * c.beta1 + x * c.rest1;
     v[i] = v[i] * c.beta2 + (x * c.rest2) * x;
     // the root and the reciprocal to 1 ulp each, as the instructions give them
-    const float denom = __builtin_amdgcn_sqrtf(v[i]) * now.root + c.eps;
-    w[i] = w[i] * keep - now.rate * (m[i] * __builtin_amdgcn_rcpf(denom));
+    const float denom = fmaf(__builtin_amdgcn_sqrtf(v[i]), now.root, c.eps);
+    w[i] = fmaf(-now.rate, m[i] * __builtin_amdgcn_rcpf(denom), w[i] * keep);
   }
   uint32_t random[8];
   if constexpr (BITS8 || (W == Dt::BF16 && !MASTER)) {
     const uint64_t group = (uint64_t)e0 / 8;
     const uint32_t key = mix32(now.key + (uint32_t)t.place) + (uint32_t)(group >> 32) * 0x9E3779B1u;
-    const uint32_t base = mix32((uint32_t)group + key);
+    // (base + i * 0x9E3779B9) * 0x85EBCA6B, the group's part multiplied once
+    const uint32_t base = mix32((uint32_t)group + key) * 0x85EBCA6Bu;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      random[i] = (base + (uint32_t)i * 0x9E3779B9u) * 0x85EBCA6Bu;
+      random[i] = base + (uint32_t)i * (0x9E3779B9u * 0x85EBCA6Bu);
       random[i] ^= random[i] >> 16;
     }
   }
   if constexpr (BITS8) {
-    uint32_t mt = 0, vt = 0;
+    // the largest magnitudes; NaN wins
+    float mt = 0.0f, vt = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      mt = max(mt, __float_as_uint(m[i]) & 0x7FFFFFFFu);
-      vt = max(vt, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      mt = __builtin_elementwise_maximum(mt, fabsf(m[i]));
+      vt = __builtin_elementwise_maximum(vt, v[i]);
     }
-    const uint32_t ms = state_scale(quad_top(mt)), vs = state_scale(quad_top(vt));
-    const float md = pow2(M_TOP + 100 - min((int)ms, E_MAX)), vd = pow2(V_TOP + 100 - min((int)vs, E_MAX));
-    u32x2_t a = {0u, 0u}, b = {0u, 0u};
+    const uint32_t ms = state_scale(quad_top(__float_as_uint(mt) & 0x7FFFFFFFu));
+    const uint32_t vs = state_scale(quad_top(__float_as_uint(vt) & 0x7FFFFFFFu));
+    const int md = state_exponent(min(ms, (uint32_t)E_MAX), M_TOP), vd = state_exponent(min(vs, (uint32_t)E_MAX), V_TOP);
+    uint32_t x[8], y[8], low = 0xFFFFFFFFu;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t x = state_code(fabsf(m[i]), md, random[i] & 0xFFFFu) | (__float_as_uint(m[i]) >> 31) << 7;
-      const uint32_t y = max(state_code(v[i], vd, random[i] >> 16), v[i] > 0.0f ? 1u : 0u);
-      a[i / 4] |= x << (8 * (i % 4));
-      b[i / 4] |= y << (8 * (i % 4));
+      x[i] = state_bits(m[i], md, random[i] & 0xFFFFu);
+      x[i] = (x[i] & 0x80000000u) | (x[i] << 4 & 0x7FFFFFFFu);  // sign and code in the topmost byte
+      y[i] = state_bits(v[i], vd, random[i] >> 16);
+      low = min(low, y[i]);
+      y[i] <<= 4;
     }
-    if (ms == 255u) a = u32x2_t{0u, 0u};
-    if (vs == 255u) b = u32x2_t{0u, 0u};
+    u32x2_t a = {top_bytes(x[0], x[1], x[2], x[3]), top_bytes(x[4], x[5], x[6], x[7])};
+    u32x2_t b = {top_bytes(y[0], y[1], y[2], y[3]), top_bytes(y[4], y[5], y[6], y[7])};
+    if (__builtin_expect(low < 1u << 20, 0)) {  // some v has the code 0: those above 0 get 1
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (y[i] < 1u << 24 && v[i] > 0.0f) b[i / 4] |= 1u << (8 * (i % 4));
+    }
+    if (__builtin_expect(ms == 255u || vs == 255u, 0)) {
+      if (ms == 255u) a = u32x2_t{0u, 0u};
+      if (vs == 255u) b = u32x2_t{0u, 0u};
+    }
     store8_codes<WHOLE>(mc, left, a);
     store8_codes<WHOLE>(vc, left, b);
     if (threadIdx.x % 4 == 0 && (WHOLE || left > 0)) {
@@ -283,12 +312,17 @@ __device__ __forceinline__ void step8(const AdamWTensor &t, int64_t e0, const St
   if constexpr (MASTER) store8_f32<Dt::F32, WHOLE>(t.master, e0, left, w);
   if constexpr (W == Dt::BF16 && !MASTER) {
     uint32_t bits[8];
+    float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      bits[i] = __float_as_uint(w[i]);
+      bits[i] = (__float_as_uint(w[i]) + (random[i] >> 8 & 0xFFFFu)) >> 16;
+      top = __builtin_elementwise_maximum(top, fabsf(w[i]));
+    }
+    if (__builtin_expect(!(top <= 3.4e38f), 0)) {
       // infinities and NaN as they are: the addition would carry through them
-      const bool finite = (bits[i] & 0x7F800000u) != 0x7F800000u;
-      bits[i] = finite ? (bits[i] + (random[i] >> 8 & 0xFFFFu)) >> 16 : (uint32_t)bf16_rne(w[i]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!(fabsf(w[i]) <= 3.4e38f)) bits[i] = bf16_rne(w[i]);
     }
     store8<W, WHOLE>(t.weight, e0, left, bits);
   } else {
@@ -301,11 +335,17 @@ __global__ __launch_bounds__(64 * STEP_WAVES) void k_adamw(StepList list, StepSc
   StepNow now;
   now.factor = c.clip != nullptr ? c.clip[1] : 1.0f;
   if (!(fabsf(now.factor) <= 3.0e38f)) return;  // gradients with inf or NaN: the step is left out
-  const int64_t step = c.step_device != nullptr ? *c.step_device : c.step;
-  if (step < 1) return;
-  now.lr = c.lr_device != nullptr ? (double)*c.lr_device : c.lr;
-  now.rate = (float)(now.lr / -expm1((double)step * c.log1));
-  now.root = (float)(1.0 / sqrt(-expm1((double)step * c.log2)));
+  int64_t step = c.step;
+  now.lr = c.lr;
+  now.rate = c.rate;
+  now.root = c.root;
+  if (c.step_device != nullptr || c.lr_device != nullptr) {  // about 1 us of fp64 arithmetic, once per wave
+    if (c.step_device != nullptr) step = *c.step_device;
+    if (step < 1) return;
+    if (c.lr_device != nullptr) now.lr = (double)*c.lr_device;
+    now.rate = step_rate(now.lr, step, c.log1);
+    now.root = step_root(step, c.log2);
+  }
   const uint64_t seed = c.seed + (uint64_t)step;
   now.key = mix32((uint32_t)seed ^ mix32((uint32_t)(seed >> 32)));
   const Finder<AdamWTensor, ADAMW_LIST> find(list);
@@ -355,8 +395,10 @@ hipError_t adamw_step(const AdamWTensor *t, int count, Dt weight, Dt grad, bool 
   if (count <= 0) return hipSuccess;
   if (count > ADAMW_LIST) return hipErrorInvalidValue;
   const bool master = t[0].master != nullptr;
+  const double log1 = log(a.beta1), log2 = log(a.beta2);
   const StepScalars c{(float)a.beta1, (float)(1.0 - a.beta1), (float)a.beta2, (float)(1.0 - a.beta2), (float)a.eps,
-                      a.lr, log(a.beta1), log(a.beta2), a.step, a.seed, a.lr_device, a.step_device, a.clip};
+                      step_rate(a.lr, a.step, log1), step_root(a.step, log2), a.lr, log1, log2, a.step, a.seed,
+                      a.lr_device, a.step_device, a.clip};
   if (weight == Dt::BF16)
     return grad == Dt::BF16 ? step_kinds<Dt::BF16, Dt::BF16>(t, count, bits8, master, c, s)
                             : step_kinds<Dt::BF16, Dt::F32>(t, count, bits8, master, c, s);
@@ -378,15 +420,14 @@ __global__ __launch_bounds__(64 * STEP_WAVES) void k_state_read(ReadList list) {
     const int64_t e0 = start + threadIdx.x * STEP_EACH, left = t.n - e0;
     if (left <= 0) continue;
     const bool whole = start + STEP_CHUNK <= t.n;
-    const float unit = state_unit(t.scale[e0 / STATE_BLOCK], t.is_signed ? M_TOP : V_TOP);
-    const uint32_t sign = t.is_signed ? 128u : 0u;
+    const uint32_t byte = t.scale[e0 / STATE_BLOCK];
+    const int e = state_exponent(byte, t.is_signed ? M_TOP : V_TOP);
     const u32x2_t c = whole ? load8_codes<true>(t.code + e0, left) : load8_codes<false>(t.code + e0, left);
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t b = c[i / 4] >> (8 * (i % 4)) & 255u;
-      x[i] = state_value(b & ~sign, unit);
-      x[i] = __uint_as_float(__float_as_uint(x[i]) | (b & sign) << 24);
+      const uint32_t b = t.is_signed ? code_at<true>(c[i / 4], i % 4) : code_at<false>(c[i / 4], i % 4);
+      x[i] = state_is_nan(byte) ? __uint_as_float(0x7FC00000u) : __builtin_amdgcn_ldexpf(__uint_as_float(b), e);
     }
     if (whole)
       store8_f32<D, true>(t.out, e0, left, x);
