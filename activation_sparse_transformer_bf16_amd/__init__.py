@@ -934,64 +934,105 @@ def _launch(device, fn, *args):
         _check(st)
 
 
-class Mx4Rows(NamedTuple):
+class Mx4Rows:
     """Rows of microscaled 4-bit floats (``twell_mx4`` in include/twell.h), as
-    ``twell_quantize_mx4`` lays them out; a row slice of each tensor is one of
-    fewer rows."""
+    ``twell_quantize_mx4`` lays them out: ``q`` uint8 [rows, ceil(cols / 2)] with
+    16-byte aligned rows, ``scale`` uint8 [rows, ceil(cols / 32) rounded up to 16],
+    ``factor`` float32 [rows] or None.  A row slice of each tensor is one of fewer
+    rows."""
 
-    q: object              # uint8 [rows, ceil(cols / 2)], rows 16-byte aligned
-    scale: object          # uint8 [rows, ceil(cols / 32) rounded up to 16]
-    cols: int
-    factor: object = None  # float32 [rows] or None
+    # Rows made here are one buffer (codes, scales, factors); its three tensors are
+    # made when they are asked for (1.5 us each, of a decoding step's 10).
+    __slots__ = ("rows", "cols", "_q", "_scale", "_factor", "_buf", "_has_factor")
+
+    def __init__(self, q, scale, cols: int, factor=None):
+        self.rows, self.cols = q.shape[0] if q.dim() else 0, cols
+        self._q, self._scale, self._factor, self._buf = q, scale, factor, None
+        self._has_factor = factor is not None
+
+    @classmethod
+    def _of(cls, buf, rows, cols, factor):
+        r = cls.__new__(cls)
+        r.rows, r.cols, r._buf, r._has_factor = rows, cols, buf, factor
+        r._q = r._scale = r._factor = None
+        return r
 
     @classmethod
     def empty(cls, rows: int, cols: int, device, factor: bool = False) -> "Mx4Rows":
         ld, lds = _mx4_strides(cols)
-        q = _t.empty((rows, ld), dtype=_UINT8, device=device)
-        n = (cols + 1) // 2
-        return cls(q if n == ld else q[:, :n], _t.empty((rows, lds), dtype=_UINT8, device=device), cols,
-                   _t.empty((rows,), dtype=_FLOAT32, device=device) if factor else None)
+        return cls._of(_t.empty((rows * (ld + lds + (4 if factor else 0)),), dtype=_UINT8, device=device), rows, cols,
+                       factor)
+
+    def _part(self, start, width, stride):
+        return self._buf.as_strided((self.rows, width), (stride, 1), start)
+
+    @property
+    def q(self):
+        if self._q is None:
+            self._q = self._part(0, (self.cols + 1) // 2, _mx4_strides(self.cols)[0])
+        return self._q
+
+    @property
+    def scale(self):
+        if self._scale is None:
+            ld, lds = _mx4_strides(self.cols)
+            self._scale = self._part(self.rows * ld, lds, lds)
+        return self._scale
+
+    @property
+    def factor(self):
+        if self._factor is None and self._has_factor:
+            self._factor = self._buf[self.rows * sum(_mx4_strides(self.cols)):].view(_FLOAT32)
+        return self._factor
+
+    @property
+    def device(self):
+        return (self._q if self._buf is None else self._buf).device
+
+    def _replace(self, **changed) -> "Mx4Rows":
+        return Mx4Rows(**{**dict(q=self.q, scale=self.scale, cols=self.cols, factor=self.factor), **changed})
 
 
 def _mx4_strides(cols):
     return (cols + 31) // 32 * 16, (cols + 511) // 512 * 16
 
 
-def _new_mx4(x, factor):
-    """Rows for those of x, and their descriptor."""
-    rows, cols = x.shape
+def _new_mx4(x, rows, cols, factor):
+    """Rows on x's device, and their descriptor."""
     ld, lds = _mx4_strides(cols)
-    q = x.new_empty((rows, ld), dtype=_UINT8)
-    scale = x.new_empty((rows, lds), dtype=_UINT8)
-    f = x.new_empty((rows,), dtype=_FLOAT32) if factor else None
-    desc = TwellMx4C(rows, cols, ld, q.data_ptr(), lds, scale.data_ptr(), None if f is None else f.data_ptr())
-    n = (cols + 1) // 2
-    return Mx4Rows(q if n == ld else q[:, :n], scale, cols, f), desc
+    buf = x.new_empty((rows * (ld + lds + (4 if factor else 0)),), dtype=_UINT8)
+    at = buf.data_ptr()
+    return Mx4Rows._of(buf, rows, cols, factor), TwellMx4C(rows, cols, ld, at, lds, at + rows * ld,
+                                                           at + rows * (ld + lds) if factor else None)
 
 
-def _mx4_rows(r, name, device, shape) -> TwellMx4C:
-    """The descriptor of 4-bit rows given as tensors: every row 16-byte aligned,
-    with its last 16-byte chunk inside the tensor's storage."""
+def _mx4_rows(r, name, device, rows, cols) -> TwellMx4C:
+    """The descriptor of 4-bit rows: every row 16-byte aligned, with its last 16-byte
+    chunk inside the tensor's storage."""
     if not isinstance(r, Mx4Rows):
         raise TypeError(f"{name} must be Mx4Rows, got {type(r).__name__}")
-    rows, cols = shape
-    if r.cols != cols or cols <= 0:
-        raise ValueError(f"{name} must have {cols} columns (at least 1), got {r.cols}")
-    if cols > _MAX_SIZE:
-        raise ValueError(f"{name}: {cols} columns exceed {_MAX_SIZE}")
-    n, (wide, lds) = (cols + 1) // 2, _mx4_strides(cols)
-    ld = _rows(r.q, f"{name}.q", device, _UINT8, (rows, n))
-    ld_scale = _rows(r.scale, f"{name}.scale", device, _UINT8, (rows, lds))
-    fp = None if r.factor is None else _vec(r.factor, f"{name}.factor", device, _FLOAT32, rows)
+    if r.cols != cols or r.rows != rows or not 0 < cols <= _MAX_SIZE:
+        raise ValueError(f"{name} must be {rows} x {cols} (and not without columns), got {r.rows} x {r.cols}")
+    wide, lds = _mx4_strides(cols)
+    buf = r._buf
+    if buf is not None:
+        if buf.device != device:
+            raise ValueError(f"{name} must be on {device}")
+        at = buf.data_ptr()
+        return TwellMx4C(rows, cols, wide, at, lds, at + rows * wide, at + rows * (wide + lds) if r._has_factor else None)
+    q, scale, n = r._q, r._scale, (cols + 1) // 2
+    ld = _rows(q, f"{name}.q", device, _UINT8, (rows, n))
+    ld_scale = _rows(scale, f"{name}.scale", device, _UINT8, (rows, lds))
+    fp = None if r._factor is None else _vec(r._factor, f"{name}.factor", device, _FLOAT32, rows)
     if rows <= 1:
         ld, ld_scale = wide, lds
     elif ld % 16 or ld_scale % 16:
         raise ValueError(f"{name}: row strides {ld} and {ld_scale} are not multiples of 16 (lay rows out as "
                          "twell_quantize_mx4 does)")
     end = (n + 15) // 16 * 16
-    if end != n and rows and r.q.storage_offset() + (rows - 1) * ld + end > r.q.untyped_storage().nbytes():
+    if end != n and rows and q.storage_offset() + (rows - 1) * ld + end > q.untyped_storage().nbytes():
         raise ValueError(f"{name}: the last row's 16-byte chunks run past the tensor's storage")
-    return TwellMx4C(rows, cols, ld, r.q.data_ptr(), ld_scale, r.scale.data_ptr(), fp)
+    return TwellMx4C(rows, cols, ld, q.data_ptr(), ld_scale, scale.data_ptr(), fp)
 
 
 def twell_quantize_mx4(x, out: Optional[Mx4Rows] = None) -> Mx4Rows:
@@ -1002,9 +1043,9 @@ def twell_quantize_mx4(x, out: Optional[Mx4Rows] = None) -> Mx4Rows:
         raise ValueError(f"x must be 2-D [rows, cols], got shape {tuple(shape)}")
     ld_x = _rows(x, "x", device, dtype, shape)
     if out is None:
-        out, desc = _new_mx4(x, False)
+        out, desc = _new_mx4(x, *shape, False)
     else:
-        desc = _mx4_rows(out, "out", device, shape)
+        desc = _mx4_rows(out, "out", device, *shape)
     _launch(device, _lib.twell_quantize_mx4, x.data_ptr(), ld_x, code, desc)
     return out
 
@@ -1014,15 +1055,15 @@ def twell_dequantize_mx4(rows: Mx4Rows, dtype=None, y=None):
     that of a given ``y``)."""
     if not isinstance(rows, Mx4Rows):
         raise TypeError(f"rows must be Mx4Rows, got {type(rows).__name__}")
-    device = rows.q.device
-    shape = (rows.q.shape[0], rows.cols)
-    desc = _mx4_rows(rows, "rows", device, shape)
+    device = rows.device
+    shape = (rows.rows, rows.cols)
+    desc = _mx4_rows(rows, "rows", device, *shape)
     if dtype is None:
         dtype = _BFLOAT16 if y is None else y.dtype
     code = _CODES[dtype] if dtype in _CODES else _dtype_code(dtype)
     ld_y = shape[1]
     if y is None:
-        y = rows.q.new_empty(shape, dtype=dtype)
+        y = _t.empty(shape, dtype=dtype, device=device)
     else:
         ld_y = _rows(y, "y", device, dtype, shape)
     _launch(device, _lib.twell_dequantize_mx4, desc, code, y.data_ptr(), ld_y)
@@ -1069,9 +1110,9 @@ def twell_rmsnorm_mx4(x, weight, eps: float = 1e-6, residual=None, h=None, y=Non
         y = _t.empty_like(x, memory_format=_CONTIGUOUS)
         yp = y.data_ptr()
     if q is None:
-        q, qd = _new_mx4(x, True)
+        q, qd = _new_mx4(x, rows, d, True)
     else:
-        qd = _mx4_rows(q, "q", device, shape)
+        qd = _mx4_rows(q, "q", device, rows, d)
     _launch(device, _lib.twell_rmsnorm_mx4, x.data_ptr(), ld_x, rp, ld_r, wp, eps, rows, d, code, hp, ld_h, yp, ld_y,
             qd)
     return RmsNormMx4Out(y, x if h is None else h, q)
@@ -1091,17 +1132,17 @@ def twell_mx4_matmul(a: Mx4Rows, b: Mx4Rows, row_bias=None, dtype=None, y=None, 
     given ``y``)."""
     if not isinstance(a, Mx4Rows) or not isinstance(b, Mx4Rows):
         raise TypeError(f"a and b must be Mx4Rows, got {type(a).__name__} and {type(b).__name__}")
-    device = a.q.device
-    M, N, K = a.q.shape[0], b.q.shape[0], a.cols
-    ad = _mx4_rows(a, "a", device, (M, K))
-    bd = _mx4_rows(b, "b", device, (N, K))
+    device = a.device
+    M, N, K = a.rows, b.rows, a.cols
+    ad = _mx4_rows(a, "a", device, M, K)
+    bd = _mx4_rows(b, "b", device, N, K)
     bp = None if row_bias is None else _vec(row_bias, "row_bias", device, _FLOAT32, M)
     if dtype is None:
         dtype = _BFLOAT16 if y is None else y.dtype
     code = _CODES[dtype] if dtype in _CODES else _dtype_code(dtype)
     ld_y = N
     if y is None:
-        y = a.q.new_empty((M, N), dtype=dtype)
+        y = _t.empty((M, N), dtype=dtype, device=device)
     else:
         ld_y = _rows(y, "y", device, dtype, (M, N))
     nbytes = twell_mx4_matmul_workspace_size(M, N, K)
@@ -1126,19 +1167,20 @@ def _adamw_struct(count: int) -> struct.Struct:
 def _grad_list(grads):
     """(the C list, device) of gradients alone."""
     flat = []
-    device = grads[0].device if grads else None
-    for i, g in enumerate(grads):
+    device = grads[0].device
+    for g in grads:
         if g.device != device or not g.is_cuda or not g.is_contiguous():
-            _need(g, f"grads[{i}]", device)
-        code = _CODES[g.dtype] if g.dtype in _CODES else _dtype_code(g.dtype)
-        flat += (g.numel(), 0, 0, g.data_ptr(), 0, 0, 0, 0, 0, code, 0.0)
+            _need(g, "grads", device)
+        dtype = g.dtype
+        flat += (g.numel(), 0, 0, g.data_ptr(), 0, 0, 0, 0, 0, _CODES[dtype] if dtype in _CODES else _dtype_code(dtype), 0.0)
     return _adamw_struct(len(grads)).pack(*flat), device
 
 
 def twell_grad_norm(grads, max_norm: float = float("inf"), out=None, workspace=None):
     """The norm of all gradients together and the factor that clips them to
     ``max_norm``: float32 [2], as ``twell_adamw_step`` takes it for ``clip``."""
-    grads = list(grads)
+    if not isinstance(grads, (list, tuple)):
+        grads = list(grads)
     if not grads:
         raise ValueError("grads is empty")
     table, device = _grad_list(grads)
@@ -1152,7 +1194,7 @@ def twell_grad_norm(grads, max_norm: float = float("inf"), out=None, workspace=N
 
 
 class TwellAdamW:
-    """Weights and optimiser states of ``twell_adamw_step``: lists with an entry
+    """Weights and optimiser states of ``twell_adamw_step``: tuples with an entry
     per weight tensor (``twell_adamw_tensor`` in include/twell.h).
 
     m, v: float32 like the weights, or uint8 codes [numel] with ``m_scale`` and
@@ -1162,16 +1204,19 @@ class TwellAdamW:
 
     def __init__(self, weights, m, v, m_scale=None, v_scale=None, master=None, weight_decay=0.0):
         n = len(weights)
-        self.weights, self.m, self.v = list(weights), list(m), list(v)
-        self.m_scale = [None] * n if m_scale is None else list(m_scale)
-        self.v_scale = [None] * n if v_scale is None else list(v_scale)
-        self.master = [None] * n if master is None else list(master)
-        self.weight_decay = ([float(weight_decay)] * n if isinstance(weight_decay, (int, float))
-                             else [float(d) for d in weight_decay])
+        none = (None,) * n
+        self.weights, self.m, self.v = tuple(weights), tuple(m), tuple(v)
+        self.m_scale = none if m_scale is None else tuple(m_scale)
+        self.v_scale = none if v_scale is None else tuple(v_scale)
+        self.master = none if master is None else tuple(master)
+        self.weight_decay = ((float(weight_decay),) * n if isinstance(weight_decay, (int, float))
+                             else tuple(float(d) for d in weight_decay))
         if not n:
             raise ValueError("no weights")
         self.device = self.weights[0].device
         self.validate()
+        # what each step checks the weights against: they may be given other storage from outside
+        self._is = tuple((w.shape, w.dtype, w.numel(), _CODES[w.dtype]) for w in self.weights)
 
     @classmethod
     def zeros(cls, weights, bits: int = 32, master: bool = False, weight_decay=0.0) -> "TwellAdamW":
@@ -1217,21 +1262,29 @@ class TwellAdamW:
                     raise ValueError(f"master[{i}]: float32 weights have no float32 copy")
                 _need(self.master[i], f"master[{i}]", device, _FLOAT32, w.shape)
 
-    def c_list(self, grads=None) -> bytes:
-        """The C list with this step's gradients (None: a list for reading the states)."""
+    def c_list(self, grads) -> bytes:
+        """The C list with this step's gradients."""
         flat = []
-        for i, w in enumerate(self.weights):
-            gp, gc = 0, 0
-            if grads is not None:
-                g = grads[i]
-                if g is None or g.device != self.device or g.shape != w.shape or not g.is_contiguous():
-                    _need(g, f"grads[{i}]", self.device, None, w.shape)
-                gp, gc = g.data_ptr(), _CODES[g.dtype] if g.dtype in _CODES else _dtype_code(g.dtype)
-            ms, vs, x = self.m_scale[i], self.v_scale[i], self.master[i]
-            flat += (w.numel(), w.data_ptr(), 0 if x is None else x.data_ptr(), gp, self.m[i].data_ptr(),
-                     self.v[i].data_ptr(), 0 if ms is None else ms.data_ptr(), 0 if vs is None else vs.data_ptr(),
-                     _CODES[w.dtype], gc, self.weight_decay[i])
+        device = self.device
+        for w, is_, x, g, m, v, ms, vs, decay in zip(self.weights, self._is, self.master, grads, self.m, self.v,
+                                                     self.m_scale, self.v_scale, self.weight_decay):
+            shape, dtype, n, code = is_
+            if g is None or g.shape != shape or g.device != device or not g.is_contiguous():
+                _need(g, "grads", device, None, shape)
+            if w.dtype != dtype or w.shape != shape or w.device != device or not w.is_contiguous():
+                _need(w, "weights", device, dtype, shape)
+            gt = g.dtype
+            flat += (n, w.data_ptr(), 0 if x is None else x.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
+                     0 if ms is None else ms.data_ptr(), 0 if vs is None else vs.data_ptr(), code,
+                     _CODES[gt] if gt in _CODES else _dtype_code(gt), decay)
         return _adamw_struct(len(self.weights)).pack(*flat)
+
+    def c_states(self) -> bytes:
+        """The C list for reading the states."""
+        flat = []
+        for is_, m, v, ms, vs in zip(self._is, self.m, self.v, self.m_scale, self.v_scale):
+            flat += (is_[2], 0, 0, 0, m.data_ptr(), v.data_ptr(), ms.data_ptr(), vs.data_ptr(), is_[3], 0, 0.0)
+        return _adamw_struct(len(self._is)).pack(*flat)
 
 
 def twell_adamw_step(opt: TwellAdamW, grads, lr, step, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -1244,7 +1297,8 @@ def twell_adamw_step(opt: TwellAdamW, grads, lr, step, beta1: float = 0.9, beta2
     returned (a factor that is not finite leaves the step out).  ``seed``: of the
     random roundings of 8-bit states and of bfloat16 weights without a copy."""
     device = opt.device
-    grads = list(grads)
+    if not isinstance(grads, (list, tuple)):
+        grads = list(grads)
     if len(grads) != len(opt.weights):
         raise ValueError(f"{len(grads)} gradients, {len(opt.weights)} weights")
     table = opt.c_list(grads)
@@ -1275,13 +1329,16 @@ def twell_adamw_states(opt: TwellAdamW, dtype=None):
     code = _dtype_code(dtype)
     if any(s is None for s in opt.m_scale):
         raise ValueError("states of 32 bits need no reading")
-    n = len(opt.weights)
-    m = [_t.empty_like(w, dtype=dtype, memory_format=_CONTIGUOUS) for w in opt.weights]
-    v = [_t.empty_like(w, dtype=dtype, memory_format=_CONTIGUOUS) for w in opt.weights]
+    # one buffer for all, each tensor's part 16-byte aligned: two calls for the 2 n tensors
+    n, sizes, step = len(opt.weights), [], 8 if dtype == _BFLOAT16 else 4
+    for is_ in opt._is:
+        sizes += (is_[2], -is_[2] % step)
+    parts = _t.empty((2 * sum(sizes),), dtype=dtype, device=opt.device).split(sizes * 2)[::2]
+    at = [t.data_ptr() for t in parts]
     pointers = ctypes.c_void_p * n
-    _launch(opt.device, _lib.twell_adamw_states, opt.c_list(), n, code, pointers(*[t.data_ptr() for t in m]),
-            pointers(*[t.data_ptr() for t in v]))
-    return m, v
+    _launch(opt.device, _lib.twell_adamw_states, opt.c_states(), n, code, pointers(*at[:n]), pointers(*at[n:]))
+    values = [t if len(is_[0]) == 1 else t.view(is_[0]) for t, is_ in zip(parts, opt._is * 2)]
+    return values[:n], values[n:]
 
 
 def twell_stream_probe(src, dst, mode: int) -> None:
