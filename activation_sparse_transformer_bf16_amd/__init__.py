@@ -1329,11 +1329,10 @@ def twell_adamw_states(opt: TwellAdamW, dtype=None):
     code = _dtype_code(dtype)
     if any(s is None for s in opt.m_scale):
         raise ValueError("states of 32 bits need no reading")
-    # one buffer for all, each tensor's part 16-byte aligned: two calls for the 2 n tensors
-    n, sizes, step = len(opt.weights), [], 8 if dtype == _BFLOAT16 else 4
-    for is_ in opt._is:
-        sizes += (is_[2], -is_[2] % step)
-    parts = _t.empty((2 * sum(sizes),), dtype=dtype, device=opt.device).split(sizes * 2)[::2]
+    # one buffer for all: two calls for the 2 n tensors
+    n = len(opt.weights)
+    sizes = [is_[2] for is_ in opt._is]
+    parts = _t.empty((2 * sum(sizes),), dtype=dtype, device=opt.device).split(sizes * 2)
     at = [t.data_ptr() for t in parts]
     pointers = ctypes.c_void_p * n
     _launch(opt.device, _lib.twell_adamw_states, opt.c_states(), n, code, pointers(*at[:n]), pointers(*at[n:]))

@@ -506,10 +506,10 @@ __device__ __forceinline__ int acc_row(int row0, int bm, int i, int lane) {
 
 // Grouped, XCD-aware order of (m-tile, n-tile) pairs: the tiles that run at the
 // same time on one XCD share GROUP_M row panels of A and a run of B panels.
+template <int GROUP_M = 4>
 __device__ __forceinline__ void tile_coords(int bid, int mt, int nt, int &tm, int &tn) {
   const int total = mt * nt;
   const int L = xcd_linear(bid, total);
-  constexpr int GROUP_M = 4;
   const int per_group = GROUP_M * nt;
   const int g = L / per_group;
   const int first_m = g * GROUP_M;

@@ -78,25 +78,24 @@ __device__ __forceinline__ void mx4_store4(typename DtT<D>::T *row, int n, int N
 
 // ---- tiles ----------------------------------------------------------------------
 
-// LDS: the ring of four stages (a group), two groups' scales (16 bytes per row),
-// then fa, bias and fb of the tile (fp32).
+// LDS: the ring, two groups' scales (32 bytes per row), then fa, bias and fb of the tile
+// (fp32).
 template <class Cfg, int BN>
 struct Mx4Tile {
   static constexpr int RING = gemm_dma_ring_bytes<Cfg>(BN);
   static constexpr int ROWS = Cfg::BM + BN;
-  static constexpr int SCALES = ROWS * 16;
+  static constexpr int SCALES = ROWS * 32;
   static constexpr int VALS = 2 * Cfg::BM + BN;
   static_assert(Cfg::BM % 64 == 0 && BN % 64 == 0, "copied 64 at a time");
-  static_assert(ROWS / 64 <= Cfg::WAVES, "one copy of scales per wave and group");
-  static_assert(Cfg::STAGES == 4, "the ring is a group");
-  static constexpr int LDS = RING + 2 * SCALES + VALS * 4;
+  static_assert(Cfg::STAGES == 4, "two pairs of slabs");
+  static constexpr int LDS = RING + SCALES + VALS * 4;
 };
 
 // Tiles as k_int8_tile's (int8.hip): a wave owns 64 columns (4 b fragments) and 2 H
 // 16-row blocks of a, taken in two halves; fragments and scales are read from LDS
 // half a slab ahead.  A slab is 64 bytes of each row, 128 elements.  The loop goes by
-// groups of four slabs, one for each byte of the scale dwords, and the ring holds a
-// group, so every LDS address is fixed.
+// groups of four slabs, one for each byte of the scale dwords; the scales of two groups
+// are copied at a time, once the last of those before are in registers everywhere.
 template <Dt D, class Cfg, int BN, bool STREAM>
 __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(Mx4MatmulArgs a, int tiles) {
   using T = typename DtT<D>::T;
@@ -114,7 +113,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row0 = WT::row0(wave), col0 = WT::col0(wave);
   int tm, tn;
-  tile_coords(blockIdx.x % tiles, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN, tm, tn);
+  tile_coords<1024 / BM>(blockIdx.x % tiles, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
   // this workgroup's range of K (whole groups): from here on the operands begin and end with it
   const int part = blockIdx.x / tiles;
@@ -127,38 +126,58 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
   const int groups = (a.K + MX4_GROUP - 1) / MX4_GROUP;
   const uint32_t base = lds_address(smem);
 
-  // factors and biases, 64 at a time, and scales; issued before the stages, so that
+  // 32 rows of scales at a time, 32 bytes of each for two groups (of the last one alone:
+  // twice its 16, as nothing behind a row is read)
+  constexpr int SCALE_COPIES = L::ROWS / 32, PER_WAVE = (SCALE_COPIES + WAVES - 1) / WAVES;
+  const uint8_t *scales[PER_WAVE];
+#pragma unroll
+  for (int c = 0; c < PER_WAVE; ++c) {
+    const int row = 32 * (wave + c * WAVES) + (lane >> 1);
+    scales[c] = row < BM ? a.a_scale + (int64_t)min(m0 + row, a.M - 1) * a.ld_sa
+                         : a.b_scale + (int64_t)min(n0 + row - BM, a.N - 1) * a.ld_sb;
+  }
+  auto copy_scales = [&](int g) {
+    const int at = min(g + (lane & 1), groups - 1) * 16;
+#pragma unroll
+    for (int c = 0; c < PER_WAVE; ++c)
+      if (wave + c * WAVES < SCALE_COPIES)
+        copy16(scales[c] + at, __builtin_amdgcn_readfirstlane((int)(base + L::RING + 1024 * (wave + c * WAVES))));
+  };
+  // scales, factors and biases, 64 at a time, are issued before the stages, so that
   // the stage waits below cover them (loads complete in order)
+  copy_scales(0);
 #pragma unroll
   for (int g = 0; g < L::VALS / 64; ++g) {
     if (g % WAVES != wave) continue;
-    const float *src = g < BM / 64       ? (a.a_factor ? a.a_factor + min(m0 + 64 * g + lane, a.M - 1) : nullptr)
-                       : g < 2 * BM / 64 ? (a.bias ? a.bias + min(m0 + 64 * (g - BM / 64) + lane, a.M - 1) : nullptr)
-                                         : (a.b_factor ? a.b_factor + min(n0 + 64 * (g - 2 * BM / 64) + lane, a.N - 1) : nullptr);
-    const bool some = g < BM / 64 ? a.a_factor != nullptr : g < 2 * BM / 64 ? a.bias != nullptr : a.b_factor != nullptr;
-    if (some) copy4(src, __builtin_amdgcn_readfirstlane((int)(base + L::RING + 2 * L::SCALES + 256 * g)));
+    const float *src = g < BM / 64 ? a.a_factor : g < 2 * BM / 64 ? a.bias : a.b_factor;
+    const int at = g < BM / 64       ? min(m0 + 64 * g + lane, a.M - 1)
+                   : g < 2 * BM / 64 ? min(m0 + 64 * (g - BM / 64) + lane, a.M - 1)
+                                     : min(n0 + 64 * (g - 2 * BM / 64) + lane, a.N - 1);
+    if (src != nullptr)
+      copy4(src + at, __builtin_amdgcn_readfirstlane((int)(base + L::RING + L::SCALES + 256 * g)));
   }
-  // the wave's 64 rows of scales, 16 bytes of each per group
-  const int srow = 64 * wave + lane;
-  const uint8_t *scales = srow < BM ? a.a_scale + (int64_t)min(m0 + srow, a.M - 1) * a.ld_sa
-                                    : a.b_scale + (int64_t)min(n0 + srow - BM, a.N - 1) * a.ld_sb;
-  const bool has_scales = 64 * wave < L::ROWS;
-  auto copy_scales = [&](int g) {
-    if (has_scales)
-      copy16(scales + (int64_t)g * 16,
-             __builtin_amdgcn_readfirstlane((int)(base + L::RING + (g & 1) * L::SCALES + 1024 * wave)));
-  };
-  copy_scales(0);
-  if (groups > 1) copy_scales(1);
   RowsA da;
   RowsB db;
   const int bytes = (a.K + 1) / 2;
   da.init(wave, lane, 0, reinterpret_cast<const int8_t *>(a.a), a.ld_a, m0, a.M, bytes);
   db.init(wave, lane, BM * SLAB, reinterpret_cast<const int8_t *>(a.b), a.ld_b, n0, a.N, bytes);
+  auto issue_pair = [&](int q, int p) {  // copies q of both slabs of a pair into the ring's half p
+    if (q < RowsA::PER_WAVE)
+      da.issue_pair(q, base + 2 * p * STAGE, base + (2 * p + 1) * STAGE);
+    else
+      db.issue_pair(q - RowsA::PER_WAVE, base + 2 * p * STAGE, base + (2 * p + 1) * STAGE);
+  };
+  auto next_pair = [&]() {
+    da.advance();
+    da.advance();
+    db.advance();
+    db.advance();
+  };
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) {
-    da.template issue_all<true>(base + s * STAGE);
-    db.template issue_all<true>(base + s * STAGE);
+  for (int p = 0; p < 2; ++p) {
+#pragma unroll
+    for (int q = 0; q < OPS; ++q) issue_pair(q, p);
+    next_pair();
   }
   f32x4_t acc[2 * H][NB];
 #pragma unroll
@@ -168,29 +187,39 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
   const int rho = lane & 15, h = lane >> 4;
   u32x4_t alo[H], ahi[H], b[NB];
   uint32_t salo[H], sahi[H], sb[NB];
-  auto read_a = [&](u32x4_t(&f)[H], int slot, int half) {
+  // Where the lane reads: fragments of a and their scales lie 16 rows apart, those of b
+  // as i8_col says, and the swizzle of a lane's rows is the same for all of them, so one
+  // offset each for the ring's two halves does, and constants for the rest.
+  const int col = i8_col<D>(0, rho);
+  uint32_t at_a[2], at_b[2];
+  const uint32_t at_sa = L::RING + (row0 + rho) * 32 + 4 * h, at_sb = L::RING + (BM + col0 + col) * 32 + 4 * h;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    at_a[p] = 2 * p * STAGE + (row0 + rho) * SLAB + ((h ^ i8_swizzle<2>(rho)) << 4);
+    at_b[p] = 2 * p * STAGE + BM * SLAB + (col0 + col) * SLAB + ((h ^ i8_swizzle<SB>(col)) << 4);
+    asm volatile("" : "+v"(at_a[p]), "+v"(at_b[p]));  // (else an address per read, and spills)
+  }
+  constexpr auto b_row = [](int j) { return i8_col<D>(j, 0); };
+  auto read_a = [&](u32x4_t(&f)[H], int s, int half) {
 #pragma unroll
     for (int i = 0; i < H; ++i)
-      f[i] = __builtin_bit_cast(u32x4_t, read_i8<2>(smem + slot * STAGE, row0 + 16 * (half * H + i) + rho, lane));
+      f[i] = *reinterpret_cast<const u32x4_t *>(smem + at_a[s / 2] + s % 2 * STAGE + 16 * (half * H + i) * SLAB);
   };
-  auto read_b = [&](int j, int slot) {
-    b[j] = __builtin_bit_cast(u32x4_t, read_i8<SB>(smem + slot * STAGE + BM * SLAB, col0 + i8_col<D>(j, rho), lane));
+  auto read_b = [&](int j, int s) {
+    b[j] = *reinterpret_cast<const u32x4_t *>(smem + at_b[s / 2] + s % 2 * STAGE + b_row(j) * SLAB);
   };
-  // scale dwords of group g: the lane's row, its quarter of the 16 bytes
-  auto scale_at = [&](int g, int row) {
-    return *reinterpret_cast<const uint32_t *>(smem + L::RING + (g & 1) * L::SCALES + row * 16 + 4 * h);
-  };
-  auto read_sa = [&](uint32_t(&f)[H], int g, int half) {
+  auto read_sa = [&](uint32_t(&f)[H], int half, int g) {
+    const char *p = smem + at_sa + (g & 1) * 16;
 #pragma unroll
-    for (int i = 0; i < H; ++i) f[i] = scale_at(g, row0 + 16 * (half * H + i) + rho);
+    for (int i = 0; i < H; ++i) f[i] = *reinterpret_cast<const uint32_t *>(p + 16 * (half * H + i) * 32);
   };
-  auto read_sb = [&](int j, int g) { sb[j] = scale_at(g, BM + col0 + i8_col<D>(j, rho)); };
+  auto read_sb = [&](int j, int g) { sb[j] = *reinterpret_cast<const uint32_t *>(smem + at_sb + (g & 1) * 16 + b_row(j) * 32); };
   auto multiply = [&](auto step, const u32x4_t(&f)[H], const uint32_t(&sf)[H], int half, int j) {
 #pragma unroll
     for (int i = 0; i < H; ++i)
       acc[half * H + i][j] = mx4_mfma<decltype(step)::value>(b[j], f[i], acc[half * H + i][j], sb[j], sf[i]);
   };
-  wait_vmcnt<(STAGES - 1) * OPS>();
+  wait_vmcnt<2 * OPS>();  // the second pair
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
@@ -199,78 +228,23 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
   }
   read_a(alo, 0, 0);
   read_sa(salo, 0, 0);
-  // slab S of group g; the next group follows
-  auto slab = [&](auto step, int g) {
+  const int left = a.K - (groups - 1) * MX4_GROUP;  // elements of the last group
+  // Slab S of a group.  LAST: of the last group, whose codes of a count up to K only.
+  auto slab = [&](auto step, auto last_c, int g) {
     constexpr int S = decltype(step)::value;
-    constexpr int next = (S + 1) % STAGES;
+    constexpr bool LAST = decltype(last_c)::value, ODD = S % 2 == 1;
+    constexpr bool ISSUE = !LAST && ODD, NEXT = !LAST || S < 3;
+    constexpr int next = (S + 1) % 4;
     read_a(ahi, S, 1);
-    if constexpr (S == 0) read_sa(sahi, g, 1);
-#pragma unroll
-    for (int j = 0; j < NB; ++j) multiply(step, alo, salo, 0, j);
-    __builtin_amdgcn_sched_barrier(0);
-    // every wave has read all of this slab (the barrier waits for its LDS reads) and
-    // the next slab has landed for every wave, and the scales before it
-    wait_vmcnt<(STAGES - 2) * OPS>();
-    __syncthreads();
     if constexpr (S == 0) {
-      if (g + 2 < groups) copy_scales(g + 2);
-    }
-    read_a(alo, next, 0);
-    if constexpr (S == 3) read_sa(salo, g + 1, 0);
-    // the loads of the slab a group ahead among the products, not in one block
+      read_sa(sahi, 1, g);
+      if constexpr (LAST) {
+        const uint32_t mask = mx4_scale_mask(left, h);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      multiply(step, ahi, sahi, 1, j);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int q = j; q < OPS; q += NB) {
-        if (q < RowsA::PER_WAVE)
-          da.issue(q, base + S * STAGE);
-        else
-          db.issue(q - RowsA::PER_WAVE, base + S * STAGE);
+        for (int i = 0; i < H; ++i) sahi[i] &= mask;
       }
-      read_b(j, next);
-      if constexpr (S == 3) read_sb(j, g + 1);
-      __builtin_amdgcn_sched_barrier(0);
     }
-    da.template advance<true>();
-    db.template advance<true>();
-  };
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  using I3 = std::integral_constant<int, 3>;
-  for (int g = 0; g < groups - 1; ++g) {
-    slab(I0(), g);
-    slab(I1(), g);
-    slab(I2(), g);
-    slab(I3(), g);
-  }
-  // the last group: all of it is in the ring or on its way
-  wait_vmcnt<0>();
-  __syncthreads();
-  const int left = a.K - (groups - 1) * MX4_GROUP;
-  read_sa(sahi, groups - 1, 1);
-  if (left < MX4_GROUP) {
-    const uint32_t mask = mx4_scale_mask(left, h);
-#pragma unroll
-    for (int i = 0; i < H; ++i) {
-      salo[i] &= mask;
-      sahi[i] &= mask;
-    }
-#pragma unroll
-    for (int j = 0; j < NB; ++j) sb[j] &= mask;
-  }
-  auto last = [&](auto step) {
-    constexpr int S = decltype(step)::value;
-    if (S * 128 >= left) return;
-    if constexpr (S > 0) {
-#pragma unroll
-      for (int j = 0; j < NB; ++j) read_b(j, S);
-      read_a(alo, S, 0);
-    }
-    read_a(ahi, S, 1);
-    if (left < (S + 1) * 128) {
+    if (LAST && left < (S + 1) * 128) {
       const int n = left - S * 128 - 32 * h;
 #pragma unroll
       for (int i = 0; i < H; ++i) {
@@ -279,16 +253,59 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
       }
     }
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      multiply(step, alo, salo, 0, j);
-      multiply(step, ahi, sahi, 1, j);
+    for (int j = 0; j < NB; ++j) multiply(step, alo, salo, 0, j);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (NEXT && ODD) {
+      // every wave has read all of this pair (the barrier waits for its LDS reads) and
+      // the next pair has landed for every wave, and the scales before it
+      wait_vmcnt<0>();
+      __syncthreads();
+      if (!LAST && S == 1 && g % 2 == 1) copy_scales(g + 1);
     }
+    if constexpr (NEXT) {
+      read_a(alo, next, 0);
+      if constexpr (S == 3) read_sa(salo, 0, g + 1);
+    }
+    // the copies of the pair that takes this one's place among the products, not in one block
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      multiply(step, ahi, sahi, 1, j);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (ISSUE) {
+#pragma unroll
+        for (int q = j; q < OPS; q += NB) issue_pair(q, S / 2);
+      }
+      if constexpr (NEXT) {
+        read_b(j, next);
+        if constexpr (S == 3) read_sb(j, g + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (ISSUE) next_pair();
   };
-  last(I0());
-  last(I1());
-  last(I2());
-  last(I3());
-
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
+  using BT = std::integral_constant<bool, true>;
+  using BF = std::integral_constant<bool, false>;
+  for (int g = 0; g < groups - 1; ++g) {
+    slab(I0(), BF(), g);
+    slab(I1(), BF(), g);
+    slab(I2(), BF(), g);
+    slab(I3(), BF(), g);
+  }
+  // the last group: scales count up to K only
+  const uint32_t mask = mx4_scale_mask(left, h);
+#pragma unroll
+  for (int i = 0; i < H; ++i) salo[i] &= mask;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) sb[j] &= mask;
+  slab(I0(), BT(), groups - 1);
+  if (left > 128) slab(I1(), BT(), groups - 1);
+  if (left > 256) slab(I2(), BT(), groups - 1);
+  if (left > 384) slab(I3(), BT(), groups - 1);
+  wait_vmcnt<0>();  // copies of slabs past K, into LDS that the results (or the next workgroup) take
   if (a.partial != nullptr) {
     // the range's sums, 4 columns per lane; rows of n_pad (a multiple of 4)
     const int n_pad = (a.N + 3) / 4 * 4;
@@ -313,7 +330,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
   constexpr int PITCH = 64 * S + 16, PER_ROW = 64 * S / 16;  // bytes of a staged row, lanes that store it
   static_assert(WAVES * 16 * PITCH <= L::RING, "the staged rows fit the ring");
   char *mine = smem + wave * 16 * PITCH;
-  const float *va = reinterpret_cast<const float *>(smem + L::RING + 2 * L::SCALES), *vbias = va + BM, *vb = va + 2 * BM;
+  const float *va = reinterpret_cast<const float *>(smem + L::RING + L::SCALES), *vbias = va + BM, *vb = va + 2 * BM;
   f32x4_t fb[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)

@@ -23,6 +23,13 @@ __device__ __forceinline__ void copy16_buffer(u32x4_t rsrc, uint32_t off, uint32
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(lds)
                : "memory", "m0");
 }
+// The same from 64 bytes further on, to where `lds` says.  (The instruction's offset
+// counts in the range check, and on the LDS side as well.)
+__device__ __forceinline__ void copy16_buffer_64(u32x4_t rsrc, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen offset:64 lds" ::"v"(off), "s"(rsrc),
+               "s"(lds - 64)
+               : "memory", "m0");
+}
 __device__ __forceinline__ void copy16(const void *g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
 }
@@ -57,14 +64,14 @@ struct I8Rows {
   static constexpr int PER_WAVE = NR / 16 / WAVES;
   static_assert(PER_WAVE >= 1 && NR % (16 * WAVES) == 0, "whole 1 KB blocks per wave");
   uint64_t start;  // of the present slab
-  uint32_t left;   // bytes from there to the end
+  int left;        // bytes from there to the end; below 0 behind it
   uint32_t off[PER_WAVE], lds[PER_WAVE];
 
   __device__ __forceinline__ void init(int wave, int lane, int region, const int8_t *base, int64_t ld, int r0,
                                        int rows, int K) {
     const int n = min(NR, rows - r0);
     start = (uint64_t)(uintptr_t)(base + (int64_t)r0 * ld);
-    left = (uint32_t)(n - 1) * (uint32_t)ld + (uint32_t)((K + 15) / 16 * 16);
+    left = (n - 1) * (int)ld + (K + 15) / 16 * 16;
 #pragma unroll
     for (int j = 0; j < PER_WAVE; ++j) {
       const int blk = wave * PER_WAVE + j;
@@ -73,24 +80,30 @@ struct I8Rows {
       off[j] = (uint32_t)row * (uint32_t)ld + (uint32_t)((lane & 3) ^ i8_swizzle<SWZ>(row)) * 16;
     }
   }
+  // of the present slab on (of one behind the end: nothing)
+  __device__ __forceinline__ u32x4_t descriptor() const {
+    return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)start),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(start >> 32) & 0xFFFFu)),
+                   (uint32_t)max(__builtin_amdgcn_readfirstlane(left), 0), 0x00020000u};
+  }
   // copy j of the present slab into its stage
   __device__ __forceinline__ void issue(int j, uint32_t stage) {
-    const u32x4_t rsrc = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)start),
-                          (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(start >> 32) & 0xFFFFu)),
-                          (uint32_t)__builtin_amdgcn_readfirstlane((int)left), 0x00020000u};
-    copy16_buffer(rsrc, off[j], __builtin_amdgcn_readfirstlane((int)(stage + lds[j])));
+    copy16_buffer(descriptor(), off[j], __builtin_amdgcn_readfirstlane((int)(stage + lds[j])));
   }
-  // to the next slab; PAST: it may lie behind the operand's end, and is then empty
-  template <bool PAST = false>
+  // copies j of the present slab and of the next one, both halves of each 128-byte line
+  __device__ __forceinline__ void issue_pair(int j, uint32_t stage, uint32_t next) {
+    const u32x4_t rsrc = descriptor();
+    copy16_buffer(rsrc, off[j], __builtin_amdgcn_readfirstlane((int)(stage + lds[j])));
+    copy16_buffer_64(rsrc, off[j], __builtin_amdgcn_readfirstlane((int)(next + lds[j])));
+  }
   __device__ __forceinline__ void advance() {
     start += SLAB;
-    left -= PAST ? min(left, (uint32_t)SLAB) : (uint32_t)SLAB;
+    left -= SLAB;
   }
-  template <bool PAST = false>
   __device__ __forceinline__ void issue_all(uint32_t stage) {
 #pragma unroll
     for (int j = 0; j < PER_WAVE; ++j) issue(j, stage);
-    advance<PAST>();
+    advance();
   }
 };
 
