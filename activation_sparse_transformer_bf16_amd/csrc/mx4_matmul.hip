@@ -542,15 +542,19 @@ __global__ __launch_bounds__(C::THREADS) void k_mx4_small(Mx4MatmulArgs a, int t
 
 // ---- launch -----------------------------------------------------------------------
 
-// The tile shapes of k_mx4_tile: rows, columns, and the time of one slab (128 elements
-// of K) per tile on a CU, in units of 10 ns.
+// The tile shapes of k_mx4_tile: rows, columns, workgroups that a CU holds, the time
+// of one slab (128 elements of K) per tile, and of a tile besides its slabs (start, ring
+// fill, results), in units of 10 ns.  Fitted, with those of k_mx4_small, to 159 sizes of
+// 1 to 8192 rows, each timed in every shape that could pay and with 1 to 8 ranges: the
+// shape chosen takes 0.8% longer than the fastest in the mean, 15% at most (328 x 9749 x
+// 2689); by the 8-bit product's figures 2% in the mean and 42% at most.
 enum Mx4Shape { MX4_256x256, MX4_256x128, MX4_128x128, MX4_64x128, MX4_SHAPES };
 struct Mx4ShapeCost {
-  int bm, bn, slab;
+  int bm, bn, held, slab, tile;
 };
-constexpr Mx4ShapeCost MX4_COST[MX4_SHAPES] = {{256, 256, 80}, {256, 128, 53}, {128, 128, 30}, {64, 128, 19}};
-constexpr int MX4_TILE_COST = 250;   // of a tile besides its slabs: start, ring fill, results
-constexpr int MX4_JOIN_COST = 250;   // of the second launch
+constexpr Mx4ShapeCost MX4_COST[MX4_SHAPES] = {
+    {256, 256, 1, 96, 436}, {256, 128, 1, 46, 366}, {128, 128, 2, 27, 182}, {64, 128, 2, 23, 186}};
+constexpr int MX4_JOIN_COST = 228;   // of the second launch
 constexpr int MX4_MAX_PARTS = 16;
 constexpr size_t MX4_MAX_PARTIAL = (size_t)64 << 20;
 
@@ -561,8 +565,8 @@ struct Mx4SmallCost {
   int bm, bn, held, start, round;
 };
 constexpr Mx4SmallCost MX4_SMALL[MX4_SMALL_SHAPES] = {
-    {16, 16, 2, 155, 85}, {16, 32, 3, 200, 40}, {32, 32, 2, 140, 115}, {32, 64, 1, 40, 235}, {64, 64, 1, 0, 380}};
-constexpr int MX4_SMALL_RATE = 1050;  // bytes a CU loads in 10 ns
+    {16, 16, 2, 34, 185}, {16, 32, 2, 107, 113}, {32, 32, 2, 49, 222}, {32, 64, 1, 182, 164}, {64, 64, 1, 99, 224}};
+constexpr int MX4_SMALL_RATE = 437;  // bytes a CU loads in 10 ns
 
 struct Mx4Plan {
   bool small;         // `shape` is an Mx4SmallShape
@@ -586,20 +590,22 @@ static Mx4Plan mx4_plan(int M, int N, int K) {
     const int64_t tiles = mx4_tiles(c.bm, c.bn, M, N);
     const int64_t per_cu = (tiles + 255) / 256, rounds = (tiles + 256 * c.held - 1) / (256 * c.held);
     const int64_t cost =
-        c.start + rounds * c.round + per_cu * ((int64_t)(c.bm + c.bn) * row / MX4_SMALL_RATE) + bytes / 140000;
+        c.start + rounds * c.round + per_cu * ((int64_t)(c.bm + c.bn) * row / MX4_SMALL_RATE);
     if (cost < least) {
       least = cost;
       best = Mx4Plan{true, shape, 1, ng * MX4_GROUP, 0};
     }
   }
   for (int shape = 0; shape < MX4_SHAPES; ++shape) {
-    const int64_t tiles = mx4_tiles(MX4_COST[shape].bm, MX4_COST[shape].bn, M, N);
+    const Mx4ShapeCost &c = MX4_COST[shape];
+    const int64_t tiles = mx4_tiles(c.bm, c.bn, M, N);
     for (int want = 1; want <= MX4_MAX_PARTS; want *= 2) {
       const int per = (ng + want - 1) / want, parts = (ng + per - 1) / per;
       const size_t sums = (size_t)parts * M * ((N + 3) / 4 * 4);
       if (want > 1 && (parts < want || sums * 4 > MX4_MAX_PARTIAL)) break;
-      const int64_t rounds = (tiles * parts + 255) / 256;
-      const int64_t cost = std::max(rounds * (4 * per * MX4_COST[shape].slab + MX4_TILE_COST), bytes / 50000 + MX4_TILE_COST) +
+      const int64_t rounds = (tiles * parts + 256 * c.held - 1) / (256 * c.held);
+      const int slabs = std::min((K + 127) / 128, 4 * per);
+      const int64_t cost = std::max(rounds * (slabs * c.held * c.slab + c.tile), bytes / 50000 + c.tile) +
                            (parts > 1 ? MX4_JOIN_COST + (int64_t)(sums / 5000) : 0);
       if (cost < least) {
         least = cost;
