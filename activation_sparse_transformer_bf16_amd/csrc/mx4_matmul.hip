@@ -84,6 +84,7 @@ template <class Cfg, int BN>
 struct Mx4Tile {
   static constexpr int RING = gemm_dma_ring_bytes<Cfg>(BN);
   static constexpr int ROWS = Cfg::BM + BN;
+  static constexpr bool RANGES = BN < 256;  // of K: the largest tile takes all of it (mx4_plan)
   static constexpr int SCALES = ROWS * 32;
   static constexpr int VALS = 2 * Cfg::BM + BN;
   static_assert(Cfg::BM % 64 == 0 && BN % 64 == 0, "copied 64 at a time");
@@ -306,7 +307,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
   if (left > 256) slab(I2(), BT(), groups - 1);
   if (left > 384) slab(I3(), BT(), groups - 1);
   wait_vmcnt<0>();  // copies of slabs past K, into LDS that the results (or the next workgroup) take
-  if (a.partial != nullptr) {
+  if (L::RANGES && a.partial != nullptr) {
     // the range's sums, 4 columns per lane; rows of n_pad (a multiple of 4)
     const int n_pad = (a.N + 3) / 4 * 4;
 #pragma unroll
@@ -602,7 +603,9 @@ static Mx4Plan mx4_plan(int M, int N, int K) {
     for (int want = 1; want <= MX4_MAX_PARTS; want *= 2) {
       const int per = (ng + want - 1) / want, parts = (ng + per - 1) / per;
       const size_t sums = (size_t)parts * M * ((N + 3) / 4 * 4);
-      if (want > 1 && (parts < want || sums * 4 > MX4_MAX_PARTIAL)) break;
+      // (P ranges of 256 x 256 tiles: as many workgroups as P / 2 of 256 x 128, of which two
+      // slabs take 92, one of theirs 96)
+      if (want > 1 && (shape == MX4_256x256 || parts < want || sums * 4 > MX4_MAX_PARTIAL)) break;
       const int64_t rounds = (tiles * parts + 256 * c.held - 1) / (256 * c.held);
       const int slabs = std::min((K + 127) / 128, 4 * per);
       const int64_t cost = std::max(rounds * (slabs * c.held * c.slab + c.tile), bytes / 50000 + c.tile) +

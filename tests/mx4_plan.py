@@ -1,0 +1,88 @@
+"""The 4-bit product's choice of kernel, tile and K ranges (mx4_plan in
+csrc/mx4_matmul.hip), written once more with the constants read from the source, so
+that tests can say which kernel a size pins.  test_mx4_plan.py holds it to the
+library's own choice."""
+
+from __future__ import annotations
+
+import os
+import re
+
+_SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       "activation_sparse_transformer_bf16_amd", "csrc", "mx4_matmul.hip")
+with open(_SOURCE) as f:
+    _TEXT = f.read()
+
+
+def _constant(name: str) -> int:
+    return int(re.search(rf"constexpr int {name} = (\d+);", _TEXT).group(1))
+
+
+def _table(name: str):
+    body = re.search(rf"{name}\[\w+\] = \{{(.*?)\}};", _TEXT, re.S).group(1)
+    return [tuple(int(v) for v in row.split(",")) for row in re.findall(r"\{([\d, ]+)\}", body)]
+
+
+TILES = _table("MX4_COST")    # rows, columns, workgroups a CU holds, cost of a slab and of a tile
+SMALL = _table("MX4_SMALL")   # rows, columns, workgroups a CU holds, start, round
+JOIN_COST, MAX_PARTS, SMALL_RATE = _constant("MX4_JOIN_COST"), _constant("MX4_MAX_PARTS"), _constant("MX4_SMALL_RATE")
+MAX_PARTIAL = 64 << 20
+GROUP = 512
+
+
+# One range of K per tile shape: with 1, 2, 3 and 4 slabs of 128 in the last group of 512,
+# an even and an odd number of groups before it, rows and columns that end inside a tile;
+# the last of each has a single group.
+UNSPLIT = {
+    (64, 128): [(68, 8719, 1564), (66, 8749, 1078), (73, 8327, 1667), (65, 8293, 1268), (66, 8235, 1899), (71, 8229, 1282),
+                (66, 8418, 2048), (66, 8662, 1426), (483, 266, 127)],
+    (128, 128): [(8243, 385, 1546), (6553, 517, 1054), (8792, 390, 1729), (8498, 386, 1212), (8366, 399, 1796),
+                 (6731, 519, 1328), (8616, 385, 1938), (8797, 389, 1447), (8511, 399, 102)],
+    (256, 128): [(8648, 445, 3599), (5519, 643, 3137), (8560, 387, 3302), (8579, 386, 2845), (8471, 397, 3361),
+                 (6623, 518, 2946), (5585, 644, 3542)],
+    (256, 256): [(6770, 1163, 1544), (4754, 1693, 1027), (8322, 936, 1745), (8385, 904, 1186), (7249, 1025, 1807),
+                 (8389, 910, 1329), (6114, 1299, 1921), (8314, 945, 1439), (962, 8418, 644)],
+}
+# Rows, columns and number of ranges.
+SPLIT = {
+    (64, 128, 2): (6111, 142, 3645), (64, 128, 4): (77, 5679, 8100), (64, 128, 8): (65, 1638, 15233),
+    (64, 128, 16): (80, 131, 23559),
+    (128, 128, 2): (267, 8348, 9462), (128, 128, 4): (5554, 136, 3707), (128, 128, 8): (2414, 142, 11808),
+    (128, 128, 16): (1030, 139, 16032),
+    (256, 128, 2): (8581, 129, 5967), (256, 128, 4): (4225, 133, 15654), (256, 128, 8): (2319, 134, 23889),
+    (256, 128, 16): (1028, 153, 46473),
+}
+# Results beyond 256 MB, and whole gates.
+LARGE = {"bf16": [(16401, 8203, 1391), (8192, 8192, 2048), (16384, 14336, 4096)], "f32": [(8201, 8203, 1391)]}
+
+
+def _up(a: int, b: int) -> int:
+    return -(-a // b)
+
+
+def plan(M: int, N: int, K: int):
+    """(kernel "tile" or "small", rows, columns, K ranges, workspace bytes)."""
+    ng, row = _up(K, GROUP), _up(K, 2)
+    read = (M + N) * row
+    best, least = None, None
+    for bm, bn, held, start, rnd in SMALL:
+        tiles = _up(M, bm) * _up(N, bn)
+        cost = start + _up(tiles, 256 * held) * rnd + _up(tiles, 256) * ((bm + bn) * row // SMALL_RATE)
+        if least is None or cost < least:
+            best, least = ("small", bm, bn, 1, 0), cost
+    for bm, bn, held, slab, tile in TILES:
+        tiles = _up(M, bm) * _up(N, bn)
+        want = 1
+        while want <= MAX_PARTS:
+            per = _up(ng, want)
+            parts = _up(ng, per)
+            sums = parts * M * _up(N, 4) * 4
+            if want > 1 and ((bm, bn) == (256, 256) or parts < want or sums * 4 > MAX_PARTIAL):
+                break
+            slabs = min(_up(K, 128), 4 * per)
+            cost = max(_up(tiles * parts, 256 * held) * (slabs * held * slab + tile), read // 50000 + tile)
+            cost += JOIN_COST + sums // 5000 if parts > 1 else 0
+            if cost < least:
+                best, least = ("tile", bm, bn, parts, _up(sums * 4, 256) * 256 if parts > 1 else 0), cost
+            want *= 2
+    return best
