@@ -78,24 +78,25 @@ __device__ __forceinline__ void mx4_store4(typename DtT<D>::T *row, int n, int N
 
 // ---- tiles ----------------------------------------------------------------------
 
-// LDS: the ring, two groups' scales (32 bytes per row), then fa, bias and fb of the tile
-// (fp32).
+// LDS: the ring and four groups' scales (64 bytes per row): all of it for the largest
+// tile.  fa, bias and fb of the tile (fp32) come last, to the end of the ring's first half.
 template <class Cfg, int BN>
 struct Mx4Tile {
   static constexpr int RING = gemm_dma_ring_bytes<Cfg>(BN);
   static constexpr int ROWS = Cfg::BM + BN;
   static constexpr bool RANGES = BN < 256;  // of K: the largest tile takes all of it (mx4_plan)
-  static constexpr int SCALES = ROWS * 32;
+  static constexpr int SCALES = ROWS * 64;
   static constexpr int VALS = 2 * Cfg::BM + BN;
   static_assert(Cfg::BM % 64 == 0 && BN % 64 == 0, "copied 64 at a time");
   static_assert(Cfg::STAGES == 4, "two pairs of slabs");
-  static constexpr int LDS = RING + SCALES + VALS * 4;
+  static constexpr int VALS_AT = RING / 2 - VALS * 4;
+  static constexpr int LDS = RING + SCALES;
 };
 
 // Tiles as k_int8_tile's (int8.hip): a wave owns 64 columns (4 b fragments) and 2 H
 // 16-row blocks of a, taken in two halves; fragments and scales are read from LDS
 // half a slab ahead.  A slab is 64 bytes of each row, 128 elements.  The loop goes by
-// groups of four slabs, one for each byte of the scale dwords; the scales of two groups
+// groups of four slabs, one for each byte of the scale dwords; the scales of four groups
 // are copied at a time, once the last of those before are in registers everywhere.
 template <Dt D, class Cfg, int BN, bool STREAM>
 __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(Mx4MatmulArgs a, int tiles) {
@@ -127,36 +128,40 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
   const int groups = (a.K + MX4_GROUP - 1) / MX4_GROUP;
   const uint32_t base = lds_address(smem);
 
-  // 32 rows of scales at a time, 32 bytes of each for two groups (of the last one alone:
-  // twice its 16, as nothing behind a row is read)
-  constexpr int SCALE_COPIES = L::ROWS / 32, PER_WAVE = (SCALE_COPIES + WAVES - 1) / WAVES;
-  const uint8_t *scales[PER_WAVE];
-#pragma unroll
-  for (int c = 0; c < PER_WAVE; ++c) {
-    const int row = 32 * (wave + c * WAVES) + (lane >> 1);
-    scales[c] = row < BM ? a.a_scale + (int64_t)min(m0 + row, a.M - 1) * a.ld_sa
-                         : a.b_scale + (int64_t)min(n0 + row - BM, a.N - 1) * a.ld_sb;
-  }
+  // 16 rows of scales at a time, 64 bytes of each for four groups (of fewer, the last
+  // one's again, as nothing behind a row is read); group g of row r is kept at (g ^ r / 4) % 4
+  // of its 64 bytes (b: r / 2^SB), so that the 16 rows of a fragment lie in all banks
+  constexpr int SCALE_COPIES = L::ROWS / 16;
   auto copy_scales = [&](int g) {
-    const int at = min(g + (lane & 1), groups - 1) * 16;
-#pragma unroll
-    for (int c = 0; c < PER_WAVE; ++c)
-      if (wave + c * WAVES < SCALE_COPIES)
-        copy16(scales[c] + at, __builtin_amdgcn_readfirstlane((int)(base + L::RING + 1024 * (wave + c * WAVES))));
+    int l = lane;
+    asm volatile("" : "+v"(l));  // (else the rows' addresses stay in registers)
+    for (int c = wave; c < SCALE_COPIES; c += WAVES) {
+      const int r = 16 * c + (l >> 2);
+      const uint8_t *p;
+      int f = r >> 2;
+      if (16 * c < BM) {
+        p = a.a_scale + (int64_t)min(m0 + r, a.M - 1) * a.ld_sa;
+      } else {
+        p = a.b_scale + (int64_t)min(n0 + r - BM, a.N - 1) * a.ld_sb;
+        f = r >> SB;
+      }
+      copy16(p + min(g + ((l ^ f) & 3), groups - 1) * 16, __builtin_amdgcn_readfirstlane((int)(base + L::RING + 1024 * c)));
+    }
   };
-  // scales, factors and biases, 64 at a time, are issued before the stages, so that
-  // the stage waits below cover them (loads complete in order)
+  static_assert(BM / 64 <= WAVES && BN / 64 <= WAVES, "64 factors for a wave");
+  auto copy_vals = [&]() {
+    auto copy = [&](const float *src, int first, int end, int count, int at) {
+      if (src != nullptr && wave < count / 64)
+        copy4(src + min(first + 64 * wave + lane, end - 1),
+              __builtin_amdgcn_readfirstlane((int)(base + L::VALS_AT + 4 * at + 256 * wave)));
+    };
+    copy(a.a_factor, m0, a.M, BM, 0);
+    copy(a.bias, m0, a.M, BM, BM);
+    copy(a.b_factor, n0, a.N, BN, 2 * BM);
+  };
+  // scales are issued before the stages, so that the stage waits below cover them (loads
+  // complete in order)
   copy_scales(0);
-#pragma unroll
-  for (int g = 0; g < L::VALS / 64; ++g) {
-    if (g % WAVES != wave) continue;
-    const float *src = g < BM / 64 ? a.a_factor : g < 2 * BM / 64 ? a.bias : a.b_factor;
-    const int at = g < BM / 64       ? min(m0 + 64 * g + lane, a.M - 1)
-                   : g < 2 * BM / 64 ? min(m0 + 64 * (g - BM / 64) + lane, a.M - 1)
-                                     : min(n0 + 64 * (g - 2 * BM / 64) + lane, a.N - 1);
-    if (src != nullptr)
-      copy4(src + at, __builtin_amdgcn_readfirstlane((int)(base + L::RING + L::SCALES + 256 * g)));
-  }
   RowsA da;
   RowsB db;
   const int bytes = (a.K + 1) / 2;
@@ -193,7 +198,8 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
   // offset each for the ring's two halves does, and constants for the rest.
   const int col = i8_col<D>(0, rho);
   uint32_t at_a[2], at_b[2];
-  const uint32_t at_sa = L::RING + (row0 + rho) * 32 + 4 * h, at_sb = L::RING + (BM + col0 + col) * 32 + 4 * h;
+  const uint32_t at_sa = L::RING + (row0 + rho) * 64 + ((rho >> 2) << 4) + 4 * h;
+  const uint32_t at_sb = L::RING + (BM + col0 + col) * 64 + ((rho >> 2) << 4) + 4 * h;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     at_a[p] = 2 * p * STAGE + (row0 + rho) * SLAB + ((h ^ i8_swizzle<2>(rho)) << 4);
@@ -210,11 +216,11 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
     b[j] = *reinterpret_cast<const u32x4_t *>(smem + at_b[s / 2] + s % 2 * STAGE + b_row(j) * SLAB);
   };
   auto read_sa = [&](uint32_t(&f)[H], int half, int g) {
-    const char *p = smem + at_sa + (g & 1) * 16;
+    const char *p = smem + (at_sa ^ (g & 3) << 4);
 #pragma unroll
-    for (int i = 0; i < H; ++i) f[i] = *reinterpret_cast<const uint32_t *>(p + 16 * (half * H + i) * 32);
+    for (int i = 0; i < H; ++i) f[i] = *reinterpret_cast<const uint32_t *>(p + 16 * (half * H + i) * 64);
   };
-  auto read_sb = [&](int j, int g) { sb[j] = *reinterpret_cast<const uint32_t *>(smem + at_sb + (g & 1) * 16 + b_row(j) * 32); };
+  auto read_sb = [&](int j, int g) { sb[j] = *reinterpret_cast<const uint32_t *>(smem + (at_sb ^ (g & 3) << 4) + b_row(j) * 64); };
   auto multiply = [&](auto step, const u32x4_t(&f)[H], const uint32_t(&sf)[H], int half, int j) {
 #pragma unroll
     for (int i = 0; i < H; ++i)
@@ -261,7 +267,8 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
       // the next pair has landed for every wave, and the scales before it
       wait_vmcnt<0>();
       __syncthreads();
-      if (!LAST && S == 1 && g % 2 == 1) copy_scales(g + 1);
+      if (!LAST && S == 1 && g % 4 == 3) copy_scales(g + 1);
+      if (LAST && S == 1) copy_vals();  // this half of the ring is done with
     }
     if constexpr (NEXT) {
       read_a(alo, next, 0);
@@ -324,14 +331,19 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
     return;
   }
   __syncthreads();  // every wave has read its last fragments: the ring is free
+  if (left <= 128) {
+    copy_vals();
+    wait_vmcnt<0>();
+    __syncthreads();
+  }
 
   // Results, 16 rows of 64 columns at a time through the wave's own LDS rows,
   // so that a store covers whole 128-byte lines.
   constexpr int S = DtT<D>::size;
   constexpr int PITCH = 64 * S + 16, PER_ROW = 64 * S / 16;  // bytes of a staged row, lanes that store it
-  static_assert(WAVES * 16 * PITCH <= L::RING, "the staged rows fit the ring");
+  static_assert(WAVES * 16 * PITCH <= L::VALS_AT, "the staged rows fit the ring, before the factors");
   char *mine = smem + wave * 16 * PITCH;
-  const float *va = reinterpret_cast<const float *>(smem + L::RING + L::SCALES), *vbias = va + BM, *vb = va + 2 * BM;
+  const float *va = reinterpret_cast<const float *>(smem + L::VALS_AT), *vbias = va + BM, *vb = va + 2 * BM;
   f32x4_t fb[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
