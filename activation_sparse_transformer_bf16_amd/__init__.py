@@ -1011,8 +1011,8 @@ def _mx4_rows(r, name, device, rows, cols) -> TwellMx4C:
     chunk inside the tensor's storage."""
     if not isinstance(r, Mx4Rows):
         raise TypeError(f"{name} must be Mx4Rows, got {type(r).__name__}")
-    if r.cols != cols or r.rows != rows or not 0 < cols <= _MAX_SIZE:
-        raise ValueError(f"{name} must be {rows} x {cols} (and not without columns), got {r.rows} x {r.cols}")
+    if r.cols != cols or r.rows != rows or not 0 < cols <= _MAX_SIZE or not 0 <= rows <= _MAX_SIZE:
+        raise ValueError(f"{name} must be {rows} x {cols} (with columns, each below 2^31), got {r.rows} x {r.cols}")
     wide, lds = _mx4_strides(cols)
     buf = r._buf
     if buf is not None:

@@ -123,6 +123,18 @@ def test_no_rows_launch_nothing():
     assert product(a=none, y=None) == OK and product(b=none, y=None) == OK
 
 
+def test_binding_refuses_rows_beyond_32_bits():
+    # (ctypes would pass their low 32 bits)
+    torch = pytest.importorskip("torch")
+    big = tw.Mx4Rows.empty((1 << 31) + 3, 32, "meta")
+    small = tw.Mx4Rows.empty(3, 32, "meta")
+    for call in (lambda: tw.twell_dequantize_mx4(big), lambda: tw.twell_mx4_matmul(big, small),
+                 lambda: tw.twell_mx4_matmul(small, big),
+                 lambda: tw.twell_quantize_mx4(torch.empty((1 << 31) + 3, 32, dtype=torch.bfloat16, device="meta"))):
+        with pytest.raises(ValueError, match="2147483651|meta"):
+            call()
+
+
 def test_product_workspace():
     size = tw.twell_mx4_matmul_workspace_size
     for M, N, K in [(0, 5, 5), (5, 0, 5), (5, 5, 0), (-1, 5, 5), (5, 5, (1 << 20) + 1), ((1 << 26) + 1, 1, 32),
