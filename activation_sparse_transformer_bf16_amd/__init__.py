@@ -1167,9 +1167,9 @@ def _adamw_struct(count: int) -> struct.Struct:
 def _grad_list(grads):
     """(the C list, device) of gradients alone."""
     flat = []
-    device = grads[0].device
+    device = None if grads[0] is None else grads[0].device
     for g in grads:
-        if g.device != device or not g.is_cuda or not g.is_contiguous():
+        if g is None or g.device != device or not g.is_cuda or not g.is_contiguous():
             _need(g, "grads", device)
         dtype = g.dtype
         flat += (g.numel(), 0, 0, g.data_ptr(), 0, 0, 0, 0, 0, _CODES[dtype] if dtype in _CODES else _dtype_code(dtype), 0.0)
@@ -1195,7 +1195,8 @@ def twell_grad_norm(grads, max_norm: float = float("inf"), out=None, workspace=N
 
 class TwellAdamW:
     """Weights and optimiser states of ``twell_adamw_step``: tuples with an entry
-    per weight tensor (``twell_adamw_tensor`` in include/twell.h).
+    per weight tensor (``twell_adamw_tensor`` in include/twell.h), none of which
+    share memory.
 
     m, v: float32 like the weights, or uint8 codes [numel] with ``m_scale`` and
     ``v_scale`` uint8 [ceil(numel / 32)] (None for a tensor with 32-bit states).
@@ -1261,6 +1262,13 @@ class TwellAdamW:
                 if w.dtype == _FLOAT32:
                     raise ValueError(f"master[{i}]: float32 weights have no float32 copy")
                 _need(self.master[i], f"master[{i}]", device, _FLOAT32, w.shape)
+        # a step writes all of them, in no order between tensors
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]")
+                       for name in ("weights", "master", "m", "v", "m_scale", "v_scale")
+                       for i, t in enumerate(getattr(self, name)) if t is not None and t.numel())
+        for (_, end, one), (start, _, two) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError(f"{one} and {two} share memory")
 
     def c_list(self, grads) -> bytes:
         """The C list with this step's gradients."""

@@ -24,6 +24,7 @@
 // place in the list and the element: the same call gives the same results.
 #include "launch.hpp"
 
+#include <float.h>
 #include <math.h>
 
 namespace twell {
@@ -356,7 +357,7 @@ template <Dt W, Dt G, bool BITS8, bool MASTER>
 __global__ __launch_bounds__(64 * STEP_WAVES) void k_adamw(StepList list, StepScalars c) {
   StepNow now;
   now.factor = c.clip != nullptr ? c.clip[1] : 1.0f;
-  if (!(fabsf(now.factor) <= 3.0e38f)) return;  // gradients with inf or NaN: the step is left out
+  if (!(fabsf(now.factor) <= FLT_MAX)) return;  // gradients with inf or NaN: the step is left out
   int64_t step = c.step;
   now.lr = c.lr;
   now.rate = c.rate;
@@ -550,7 +551,7 @@ __global__ __launch_bounds__(1024) void k_grad_norm(const double *partial, int n
   const float norm = (float)sqrt(sum);
   out[0] = norm;
   // an infinite or NaN norm gives a NaN factor, which the step takes as "leave it out"
-  out[1] = norm <= 3.0e38f ? fminf(1.0f, max_norm / norm) : __uint_as_float(0x7FC00000u);
+  out[1] = norm <= FLT_MAX ? fminf(1.0f, max_norm / norm) : __uint_as_float(0x7FC00000u);
 }
 
 static int64_t grad_fill(GradList &l, const GradRef *g, int count) {

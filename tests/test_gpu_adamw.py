@@ -415,3 +415,36 @@ def test_binding_refuses():
             tw.twell_adamw_step(o, c.grads, step=1, **kw)
     with pytest.raises(tw.TwellError):
         tw.twell_grad_norm(c.grads, 0.0)
+
+
+def test_tensors_that_share_memory_are_refused():
+    import torch
+    w = torch.zeros(4, 100, device="cuda:0")
+    v = [torch.zeros(100, device="cuda:0") for _ in range(4)]
+    one = tw.TwellAdamW([w[0], w[1]], v[:2], v[2:])  # side by side
+    tw.twell_adamw_step(one, [v[0] + 1, v[0] + 1], lr=1e-3, step=1)
+    empty = torch.zeros(0, device="cuda:0")
+    tw.TwellAdamW([empty, empty, w[0]], [empty, empty, v[0]], [empty, empty, v[1]])
+    flat = w.view(-1)
+    for call in (lambda: tw.TwellAdamW([w[0], w[0]], v[:2], v[2:]), lambda: tw.TwellAdamW([w[0], w[1]], v[:2], v[:2]),
+                 lambda: tw.TwellAdamW([w[0]], [w[0]], v[:1]), lambda: tw.TwellAdamW.zeros([w[0], flat[99:199]]),
+                 lambda: tw.TwellAdamW.zeros([w, w], bits=8)):
+        with pytest.raises(ValueError, match="share memory"):
+            call()
+
+
+def test_norm_refuses_a_missing_gradient():
+    import torch
+    g = torch.ones(3, device="cuda:0")
+    for grads in ([None], [None, g], [g, None]):
+        with pytest.raises(ValueError, match="required"):
+            tw.twell_grad_norm(grads)
+
+
+def test_norm_up_to_the_largest_number():
+    # 2^128 - 2^104 is finite: so is its norm, and it is clipped as any other
+    import torch
+    top = float(np.finfo(np.float32).max)
+    g = torch.tensor([top], device="cuda:0")
+    assert tw.twell_grad_norm([g], 1024.0).tolist() == [top, float(np.float32(1024.0) / np.float32(top))]
+    assert tw.twell_grad_norm([g]).tolist() == [top, 1.0]
