@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * MX4_WAVES) void k_mx4_dequantize(Mx4Args a, in
       if (R == Rows::WHOLE) {
         __builtin_nontemporal_store(out, reinterpret_cast<u32x4_t *>(y));
       } else if (p.e0 + E <= a.cols) {
-        *reinterpret_cast<u32x4_any_t *>(y) = out;
+        __builtin_nontemporal_store(out, reinterpret_cast<u32x4_any_t *>(y));
       } else {
 #pragma unroll
         for (int k = 0; k < E; ++k)

@@ -53,7 +53,7 @@ SPLIT = {
     (256, 128, 16): (1028, 153, 46473),
 }
 # Results beyond 256 MB, and whole gates.
-LARGE = {"bf16": [(16401, 8203, 1391), (8192, 8192, 2048), (16384, 14336, 4096)], "f32": [(8201, 8203, 1391)]}
+LARGE = {"bf16": [(16401, 8203, 2047), (8192, 8192, 2048), (16384, 14336, 4096)], "f32": [(16371, 8190, 2047)]}
 
 
 def _up(a: int, b: int) -> int:

@@ -78,7 +78,8 @@ SHAPES = [(1, 1, 1), (1, 5, 3), (2, 16, 16), (1, 64, 64), (1, 1000, 777), (3, 25
           (48, 512, 4096), (64, 2048, 8192), (32, 300, 16384), (17, 131, 5003), (100, 1, 4096),
           (300, 260, 20000), (129, 1000, 7777), (700, 520, 2000), (1500, 300, 288), (1024, 1024, 1024),
           (2076, 18, 42), (122, 1133, 548), (440, 578, 1664), (257, 1996, 983), (101, 4171, 39), (4564, 391, 33),
-          (4104, 928, 19), (2067, 1593, 150), (4, 6, 50556), (1, 1524, 24721), (2349, 39, 9705), (1637, 257, 8417)]
+          (4104, 928, 19), (2067, 1593, 150), (4, 6, 50556), (1, 1524, 24721), (2349, 39, 9705), (1637, 257, 8417),
+          (17, 8603, 2438), (708, 394, 2092), (5157, 38, 2082)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
