@@ -19,6 +19,9 @@
 //  * k_mx4_join, which adds them in order and writes the results.
 //  * k_mx4_small: products too small to fill the chip with such tiles: 16 to 64
 //    rows and columns per workgroup, whose waves split K.
+//
+// The instruction at full rate, from registers alone, does 7.0 PFLOP/s on random
+// codes and 9.7 on zeros (32 x 32 x 64: 6.3 and 9.65): the chip's power bounds it.
 #include "launch.hpp"
 #include "mx4.hpp"
 #include "narrow.hpp"
@@ -98,6 +101,24 @@ struct Mx4Tile {
 // half a slab ahead.  A slab is 64 bytes of each row, 128 elements.  The loop goes by
 // groups of four slabs, one for each byte of the scale dwords; the scales of four groups
 // are copied at a time, once the last of those before are in registers everywhere.
+//
+// Slabs are copied in pairs because a line is 128 bytes: copied one by one, every line
+// is fetched twice (8192^3: 41 million L2 requests, in pairs 25).
+//
+// 8192 x 8192 x 2048 bf16 96 to 100 us (2.8 PFLOP/s), 8192^3 275 to 287 (3.9), 16384 x
+// 14336 x 4096 468 to 485 (4.0), by card; MFMA busy 0.29 to 0.44.  What bounds it is
+// the copies: of the 233 us that another K = 8192 of 8192 x 8192 takes, 73 go without
+// them, 8 without the LDS reads, and the products alone take 140.  Two pairs of slabs fill
+// the LDS, so a pair has the time of one other to arrive, and a miss in L2 takes longer:
+// with all tiles reading the same rows 8192 x 8192 x 2048 takes 92 us, 8192^3 260.
+// Power is a fifth (operands of zeros: 78, 233 and 444 us).  Slower or no faster: one
+// workgroup per CU that starts the next tile's copies before its results' stores (K =
+// 2048 115 us, K = 512 66 against 54: copies behind stores wait for them), two
+// workgroups of 128 x 256 per CU (K = 2048 107, 8192^3 335), results straight from
+// registers (100, 495 at 16384 x 14336 x 4096), raised wave priority, panels of 1, 4 and
+// 8 tiles of rows where a panel has 1024 rows now (K = 2048 91 to 98, but 16384 x 14336
+// x 4096 476 to 522), non-temporal stores of 134 MB (83 us, but the kernel that reads the
+// result next takes 41 more).
 template <Dt D, class Cfg, int BN, bool STREAM>
 __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(Mx4MatmulArgs a, int tiles) {
   using T = typename DtT<D>::T;
@@ -383,7 +404,8 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(
 }
 
 // The ranges' sums added in order, scaled and written: 4 columns per thread, a row
-// per blockIdx.y; four ranges' loads in flight at a time.
+// per blockIdx.y; four ranges' loads in flight at a time.  A second launch costs 2.3 us
+// and the sums' bytes each way; 16 x 16 x 65536 in 16 ranges takes 11.5 us in all.
 template <Dt D>
 __global__ __launch_bounds__(256) void k_mx4_join(Mx4MatmulArgs a, int parts) {
   using T = typename DtT<D>::T;
@@ -417,6 +439,11 @@ __global__ __launch_bounds__(256) void k_mx4_join(Mx4MatmulArgs a, int parts) {
 // and add their sums through LDS at the end.  A slab's copies are 8 rows of 128 bytes
 // each, chunk c of row r kept at c ^ (r / 2 % 8), then a dword of scales for each lane
 // of each fragment, of which the slab uses two bytes.
+//
+// Bound by latency: 1 x 8192 x 2048 3.7 us (8.9 MB, 2.4 TB/s; an empty launch 2.0), 16
+// and 64 x 8192 x 2048 3.9 and 6.0, 64 x 2048 x 8192 7.4, 333 x 1000 x 777 4.5.  As tiles
+// of 64 x 128 with 8 ranges of K 64 x 2048 x 8192 takes 11.1 us, 1 x 2048 x 8192 6.8
+// (here 4.5).
 template <int MF_, int NF_, int WAVES_, int STAGES_>
 struct Mx4Small {
   static constexpr int MF = MF_, NF = NF_, WAVES = WAVES_, STAGES = STAGES_;

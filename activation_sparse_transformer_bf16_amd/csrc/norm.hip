@@ -140,6 +140,14 @@ constexpr int row_waves(int W) { return W > 4 ? W : 4; }
 // waves, 8 chunks) 97 to 139 of them are spilled, in the quantiser 20 to 61: 1000 x
 // 39999 bf16 212, 1000 x 24575 fp32 185 (quantiser 85 and 38, whole rows 23 and 22).
 // Of 32 to 64 KB only bf16 spills (24): 2000 x 24575 138 us, 2000 x 12287 fp32 79.
+//
+// Q4, rows in 4 bits: a block's lanes are 4 (bf16) or 8 (fp32) neighbours, so its scale
+// takes two or three DPP moves and no row maximum.  8192 x 2048 bf16 with residual
+// 22.7 us (143 MB, 6.3 TB/s), one row 2.7; 2000 x 12288 fp32 73, 2000 x 24576 bf16 79,
+// 1000 x 24576 fp32 77, 1000 x 40000 bf16 73 (4 to 5 TB/s).  Of rows of no alignment
+// those beyond 64 KB spill 42 (bf16) and 131 registers (fp32): 1000 x 39999 bf16 141
+// us, 1000 x 24575 fp32 222; shorter ones 8 or none: 8192 x 2047 bf16 26, 2000 x 24575
+// bf16 113, 2000 x 12287 fp32 91.
 template <Dt D, int W, int NC, Rows R, bool NORM, bool Q4>
 __global__ __launch_bounds__(64 * row_waves(W)) void k_norm_rows(NormArgs a) {
   static_assert(NORM || !Q4, "rows in 4 bits without a norm: mx4.hip");
