@@ -106,7 +106,7 @@ struct Mx4Tile {
 // is fetched twice (8192^3: 41 million L2 requests, in pairs 25).
 //
 // 8192 x 8192 x 2048 bf16 96 to 100 us (2.8 PFLOP/s), 8192^3 275 to 287 (3.9), 16384 x
-// 14336 x 4096 468 to 485 (4.0), by card; MFMA busy 0.29 to 0.44.  What bounds it is
+// 14336 x 4096 468 to 485 (4.0), by card; MFMA busy 0.31 to 0.43.  What bounds it is
 // the copies: of the 233 us that another K = 8192 of 8192 x 8192 takes, 73 go without
 // them, 8 without the LDS reads, and the products alone take 140.  Two pairs of slabs fill
 // the LDS, so a pair has the time of one other to arrive, and a miss in L2 takes longer:
