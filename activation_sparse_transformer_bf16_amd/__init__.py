@@ -1204,9 +1204,9 @@ class TwellAdamW:
     tensor).  weight_decay: one number, or one per tensor."""
 
     def __init__(self, weights, m, v, m_scale=None, v_scale=None, master=None, weight_decay=0.0):
-        n = len(weights)
-        none = (None,) * n
         self.weights, self.m, self.v = tuple(weights), tuple(m), tuple(v)
+        n = len(self.weights)
+        none = (None,) * n
         self.m_scale = none if m_scale is None else tuple(m_scale)
         self.v_scale = none if v_scale is None else tuple(v_scale)
         self.master = none if master is None else tuple(master)
@@ -1225,6 +1225,7 @@ class TwellAdamW:
         float32 copies of the bfloat16 weights."""
         if bits not in (8, 32):
             raise ValueError(f"states have 8 or 32 bits, not {bits}")
+        weights = tuple(weights)
 
         def states():
             if bits == 32:

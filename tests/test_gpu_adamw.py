@@ -448,3 +448,20 @@ def test_norm_up_to_the_largest_number():
     g = torch.tensor([top], device="cuda:0")
     assert tw.twell_grad_norm([g], 1024.0).tolist() == [top, float(np.float32(1024.0) / np.float32(top))]
     assert tw.twell_grad_norm([g]).tolist() == [top, 1.0]
+
+
+def test_weights_from_a_generator_and_of_no_dimension():
+    import torch
+    layer = torch.nn.Linear(40, 3, device="cuda:0")
+    scale = torch.nn.Parameter(torch.tensor(2.0, device="cuda:0"))
+    for bits in (32, 8):
+        weights = [*layer.parameters(), scale]
+        opt = tw.TwellAdamW.zeros((w for w in weights), bits=bits)
+        before = [w.detach().clone() for w in weights]
+        tw.twell_adamw_step(opt, (torch.ones_like(w) for w in weights), lr=0.125, step=1, eps=0.0)
+        # m / (1 - beta1) / sqrt(v / (1 - beta2)) = 1 but for the roundings of nine operations, 3 of them to 1 ulp
+        for w, b in zip(weights, before):
+            assert w.shape == b.shape and ((w - b + 0.125).abs() <= 0.125 * 16 * U + 2 * U * b.abs()).all()
+        if bits == 8:
+            m, v = tw.twell_adamw_states(opt)
+            assert [t.shape for t in m] == [w.shape for w in weights]

@@ -152,3 +152,44 @@ def test_rows_far_apart(M, N, K, ld):
     _check(tw.twell_mx4_matmul(a._replace(factor=fa), far, dtype=torch.float32), va, vb, fa, fb, None, "f32")
     swap = tw.twell_mx4_matmul(far, a._replace(factor=fa), dtype=torch.float32)
     _check(swap, vb, va, fb, fa, None, "f32")
+
+
+def test_ranges_in_a_captured_graph_with_one_workspace():
+    # three products in a row through the same workspace, replayed with other operands and
+    # eager products through it in between
+    import torch
+    shapes = [SPLIT[128, 128, 4], SPLIT[64, 128, 16], SPLIT[256, 128, 2]]
+    sets = [[_operands(M, N, K, 7 * i + seed) for i, (M, N, K) in enumerate(shapes)] for seed in (1, 2, 3)]
+    now = [tuple(tw.Mx4Rows.empty(r.rows, r.cols, "cuda:0") for r in (o[0], o[3])) for o in sets[0]]
+    workspace = torch.empty(max(tw.twell_mx4_matmul_workspace_size(*s) for s in shapes), dtype=torch.uint8, device="cuda:0")
+    results = [torch.empty(M, N, device="cuda:0") for M, N, _ in shapes]
+
+    def products(rows, ys):
+        for (a, b), y in zip(rows, ys):
+            tw.twell_mx4_matmul(a, b, y=y, workspace=workspace)
+
+    def load(of):
+        for to, o in zip(now, of):
+            for dst, src in zip(to, (o[0], o[3])):
+                # (what a view leaves out: the bytes up to the next multiple of 16, never read into a result)
+                dst.q.copy_(src.q)
+                dst.scale.copy_(src.scale)
+
+    load(sets[0])
+    products(now, results)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        products(now, results)
+    for of in (sets[1], sets[2], sets[0]):
+        load(of)
+        for r in results:
+            r.fill_(-1.0)
+        graph.replay()
+        got = [r.clone() for r in results]
+        eager = [torch.empty_like(r) for r in results]
+        products(now, eager)
+        torch.cuda.synchronize()
+        for g, e, o in zip(got, eager, of):
+            assert torch.equal(g, e)
+            _check(g, o[1], o[4], None, None, None, "f32")
