@@ -934,6 +934,11 @@ def _launch(device, fn, *args):
         _check(st)
 
 
+def _new(shape, dtype, device):
+    # (0.4 us less than torch.empty)
+    return _t.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+
+
 class Mx4Rows:
     """Rows of microscaled 4-bit floats (``twell_mx4`` in include/twell.h), as
     ``twell_quantize_mx4`` lays them out: ``q`` uint8 [rows, ceil(cols / 2)] with
@@ -1000,10 +1005,22 @@ def _mx4_strides(cols):
 def _new_mx4(x, rows, cols, factor):
     """Rows on x's device, and their descriptor."""
     ld, lds = _mx4_strides(cols)
-    buf = x.new_empty((rows * (ld + lds + (4 if factor else 0)),), dtype=_UINT8)
+    buf = _t.empty_strided((rows * (ld + lds + (4 if factor else 0)),), (1,), dtype=_UINT8, device=x.device)
     at = buf.data_ptr()
     return Mx4Rows._of(buf, rows, cols, factor), TwellMx4C(rows, cols, ld, at, lds, at + rows * ld,
                                                            at + rows * (ld + lds) if factor else None)
+
+
+def _byte_rows(t, name, part, device, rows, cols, stride) -> int:
+    """Checks codes or scales [rows, cols]; returns their row stride, or `stride` for a single row."""
+    if t is None or t.dtype != _UINT8 or t.device != device or not t.is_cuda or t.shape != (rows, cols):
+        _bad_rows(t, f"{name}.{part}", device, _UINT8, (rows, cols))
+    if rows <= 1:
+        return stride
+    across, along = t.stride()
+    if along != 1 and cols > 1:
+        _bad_rows(t, f"{name}.{part}", device, _UINT8, (rows, cols))
+    return across
 
 
 def _mx4_rows(r, name, device, rows, cols) -> TwellMx4C:
@@ -1021,12 +1038,10 @@ def _mx4_rows(r, name, device, rows, cols) -> TwellMx4C:
         at = buf.data_ptr()
         return TwellMx4C(rows, cols, wide, at, lds, at + rows * wide, at + rows * (wide + lds) if r._has_factor else None)
     q, scale, n = r._q, r._scale, (cols + 1) // 2
-    ld = _rows(q, f"{name}.q", device, _UINT8, (rows, n))
-    ld_scale = _rows(scale, f"{name}.scale", device, _UINT8, (rows, lds))
+    ld = _byte_rows(q, name, "q", device, rows, n, wide)
+    ld_scale = _byte_rows(scale, name, "scale", device, rows, lds, lds)
     fp = None if r._factor is None else _vec(r._factor, f"{name}.factor", device, _FLOAT32, rows)
-    if rows <= 1:
-        ld, ld_scale = wide, lds
-    elif ld % 16 or ld_scale % 16:
+    if ld % 16 or ld_scale % 16:
         raise ValueError(f"{name}: row strides {ld} and {ld_scale} are not multiples of 16 (lay rows out as "
                          "twell_quantize_mx4 does)")
     end = (n + 15) // 16 * 16
@@ -1063,7 +1078,7 @@ def twell_dequantize_mx4(rows: Mx4Rows, dtype=None, y=None):
     code = _CODES[dtype] if dtype in _CODES else _dtype_code(dtype)
     ld_y = shape[1]
     if y is None:
-        y = _t.empty(shape, dtype=dtype, device=device)
+        y = _new(shape, dtype, device)
     else:
         ld_y = _rows(y, "y", device, dtype, shape)
     _launch(device, _lib.twell_dequantize_mx4, desc, code, y.data_ptr(), ld_y)
@@ -1101,13 +1116,13 @@ def twell_rmsnorm_mx4(x, weight, eps: float = 1e-6, residual=None, h=None, y=Non
         ld_h = _rows(h, "h", device, dtype, shape)
         hp = h.data_ptr()
     elif residual is not None:
-        h = _t.empty_like(x, memory_format=_CONTIGUOUS)
+        h = _new(shape, dtype, device)
         hp = h.data_ptr()
     if y is not None:
         ld_y = _rows(y, "y", device, dtype, shape)
         yp = y.data_ptr()
     elif want_y:
-        y = _t.empty_like(x, memory_format=_CONTIGUOUS)
+        y = _new(shape, dtype, device)
         yp = y.data_ptr()
     if q is None:
         q, qd = _new_mx4(x, rows, d, True)
@@ -1142,7 +1157,7 @@ def twell_mx4_matmul(a: Mx4Rows, b: Mx4Rows, row_bias=None, dtype=None, y=None, 
     code = _CODES[dtype] if dtype in _CODES else _dtype_code(dtype)
     ld_y = N
     if y is None:
-        y = _t.empty((M, N), dtype=dtype, device=device)
+        y = _new((M, N), dtype, device)
     else:
         ld_y = _rows(y, "y", device, dtype, (M, N))
     nbytes = twell_mx4_matmul_workspace_size(M, N, K)
