@@ -1015,12 +1015,10 @@ def _byte_rows(t, name, part, device, rows, cols, stride) -> int:
     """Checks codes or scales [rows, cols]; returns their row stride, or `stride` for a single row."""
     if t is None or t.dtype != _UINT8 or t.device != device or not t.is_cuda or t.shape != (rows, cols):
         _bad_rows(t, f"{name}.{part}", device, _UINT8, (rows, cols))
-    if rows <= 1:
-        return stride
     across, along = t.stride()
-    if along != 1 and cols > 1:
+    if along != 1 and cols > 1 and rows:
         _bad_rows(t, f"{name}.{part}", device, _UINT8, (rows, cols))
-    return across
+    return across if rows > 1 else stride
 
 
 def _mx4_rows(r, name, device, rows, cols) -> TwellMx4C:
