@@ -943,22 +943,22 @@ class Mx4Rows:
     """Rows of microscaled 4-bit floats (``twell_mx4`` in include/twell.h), as
     ``twell_quantize_mx4`` lays them out: ``q`` uint8 [rows, ceil(cols / 2)] with
     16-byte aligned rows, ``scale`` uint8 [rows, ceil(cols / 32) rounded up to 16],
-    ``factor`` float32 [rows] or None.  A row slice of each tensor is one of fewer
-    rows."""
+    ``factor`` float32 [rows] or None.  ``rows`` and ``cols`` do not change; a row
+    slice of each tensor is one of fewer rows."""
 
     # Rows made here are one buffer (codes, scales, factors); its three tensors are
     # made when they are asked for (1.5 us each, of a decoding step's 10).
-    __slots__ = ("rows", "cols", "_q", "_scale", "_factor", "_buf", "_has_factor")
+    __slots__ = ("_rows", "_cols", "_q", "_scale", "_factor", "_buf", "_has_factor")
 
     def __init__(self, q, scale, cols: int, factor=None):
-        self.rows, self.cols = q.shape[0] if q.dim() else 0, cols
+        self._rows, self._cols = q.shape[0] if q.dim() else 0, cols
         self._q, self._scale, self._factor, self._buf = q, scale, factor, None
         self._has_factor = factor is not None
 
     @classmethod
     def _of(cls, buf, rows, cols, factor):
         r = cls.__new__(cls)
-        r.rows, r.cols, r._buf, r._has_factor = rows, cols, buf, factor
+        r._rows, r._cols, r._buf, r._has_factor = rows, cols, buf, factor
         r._q = r._scale = r._factor = None
         return r
 
@@ -969,25 +969,33 @@ class Mx4Rows:
                        factor)
 
     def _part(self, start, width, stride):
-        return self._buf.as_strided((self.rows, width), (stride, 1), start)
+        return self._buf.as_strided((self._rows, width), (stride, 1), start)
+
+    @property
+    def rows(self) -> int:
+        return self._rows
+
+    @property
+    def cols(self) -> int:
+        return self._cols
 
     @property
     def q(self):
         if self._q is None:
-            self._q = self._part(0, (self.cols + 1) // 2, _mx4_strides(self.cols)[0])
+            self._q = self._part(0, (self._cols + 1) // 2, _mx4_strides(self._cols)[0])
         return self._q
 
     @property
     def scale(self):
         if self._scale is None:
-            ld, lds = _mx4_strides(self.cols)
-            self._scale = self._part(self.rows * ld, lds, lds)
+            ld, lds = _mx4_strides(self._cols)
+            self._scale = self._part(self._rows * ld, lds, lds)
         return self._scale
 
     @property
     def factor(self):
         if self._factor is None and self._has_factor:
-            self._factor = self._buf[self.rows * sum(_mx4_strides(self.cols)):].view(_FLOAT32)
+            self._factor = self._buf[self._rows * sum(_mx4_strides(self._cols)):].view(_FLOAT32)
         return self._factor
 
     @property
@@ -995,7 +1003,7 @@ class Mx4Rows:
         return (self._q if self._buf is None else self._buf).device
 
     def _replace(self, **changed) -> "Mx4Rows":
-        return Mx4Rows(**{**dict(q=self.q, scale=self.scale, cols=self.cols, factor=self.factor), **changed})
+        return Mx4Rows(**{**dict(q=self.q, scale=self.scale, cols=self._cols, factor=self.factor), **changed})
 
 
 def _mx4_strides(cols):
@@ -1026,8 +1034,8 @@ def _mx4_rows(r, name, device, rows, cols) -> TwellMx4C:
     chunk inside the tensor's storage."""
     if not isinstance(r, Mx4Rows):
         raise TypeError(f"{name} must be Mx4Rows, got {type(r).__name__}")
-    if r.cols != cols or r.rows != rows or not 0 < cols <= _MAX_SIZE or not 0 <= rows <= _MAX_SIZE:
-        raise ValueError(f"{name} must be {rows} x {cols} (with columns, each below 2^31), got {r.rows} x {r.cols}")
+    if r._cols != cols or r._rows != rows or not 0 < cols <= _MAX_SIZE or not 0 <= rows <= _MAX_SIZE:
+        raise ValueError(f"{name} must be {rows} x {cols} (with columns, each below 2^31), got {r._rows} x {r._cols}")
     wide, lds = _mx4_strides(cols)
     buf = r._buf
     if buf is not None:
@@ -1069,7 +1077,7 @@ def twell_dequantize_mx4(rows: Mx4Rows, dtype=None, y=None):
     if not isinstance(rows, Mx4Rows):
         raise TypeError(f"rows must be Mx4Rows, got {type(rows).__name__}")
     device = rows.device
-    shape = (rows.rows, rows.cols)
+    shape = (rows._rows, rows._cols)
     desc = _mx4_rows(rows, "rows", device, *shape)
     if dtype is None:
         dtype = _BFLOAT16 if y is None else y.dtype
@@ -1146,7 +1154,7 @@ def twell_mx4_matmul(a: Mx4Rows, b: Mx4Rows, row_bias=None, dtype=None, y=None, 
     if not isinstance(a, Mx4Rows) or not isinstance(b, Mx4Rows):
         raise TypeError(f"a and b must be Mx4Rows, got {type(a).__name__} and {type(b).__name__}")
     device = a.device
-    M, N, K = a.rows, b.rows, a.cols
+    M, N, K = a._rows, b._rows, a._cols
     ad = _mx4_rows(a, "a", device, M, K)
     bd = _mx4_rows(b, "b", device, N, K)
     bp = None if row_bias is None else _vec(row_bias, "row_bias", device, _FLOAT32, M)

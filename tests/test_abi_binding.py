@@ -64,3 +64,14 @@ def test_a_single_row_of_any_row_stride(calls):
     byte = rows(torch.zeros(1, 16, dtype=torch.uint8).as_strided((1, 1), (16, 5)), torch.zeros(1, 16, dtype=torch.uint8), 2)
     tw.twell_quantize_mx4(gpu(torch.zeros(1, 2)), out=byte)
     assert len(calls) == 2
+
+
+def test_the_sizes_of_rows_are_fixed(calls):
+    # the library's rows lie in one buffer of exactly that many
+    made = tw.Mx4Rows.empty(3, 64, "cpu")
+    given = rows(torch.zeros(3, 32, dtype=torch.uint8), torch.zeros(3, 16, dtype=torch.uint8), 64)
+    for r in (made, given):
+        for name in ("rows", "cols", "q", "scale", "factor"):
+            with pytest.raises(AttributeError):
+                setattr(r, name, 1000)
+        assert (r.rows, r.cols) == (3, 64) and r.q.shape == (3, 32) and r.scale.shape == (3, 16)
