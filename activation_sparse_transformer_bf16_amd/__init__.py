@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import struct
 from dataclasses import dataclass
@@ -1214,6 +1215,9 @@ def twell_grad_norm(grads, max_norm: float = float("inf"), out=None, workspace=N
     return out
 
 
+_address, _nbytes = _t.Tensor.data_ptr, operator.attrgetter("nbytes")
+
+
 class TwellAdamW:
     """Weights and optimiser states of ``twell_adamw_step``: tuples with an entry
     per weight tensor (``twell_adamw_tensor`` in include/twell.h), none of which
@@ -1222,23 +1226,22 @@ class TwellAdamW:
     m, v: float32 like the weights, or uint8 codes [numel] with ``m_scale`` and
     ``v_scale`` uint8 [ceil(numel / 32)] (None for a tensor with 32-bit states).
     master: float32 copies of bfloat16 weights, or None (for all, or for a
-    tensor).  weight_decay: one number, or one per tensor."""
+    tensor).  weight_decay: one number, or one per tensor.
+
+    All of them may be assigned anew (a resumed run's states); the next step
+    checks what it finds."""
+
+    _GIVEN = frozenset(("weights", "m", "v", "m_scale", "v_scale", "master", "weight_decay"))
 
     def __init__(self, weights, m, v, m_scale=None, v_scale=None, master=None, weight_decay=0.0):
-        self.weights, self.m, self.v = tuple(weights), tuple(m), tuple(v)
-        n = len(self.weights)
-        none = (None,) * n
-        self.m_scale = none if m_scale is None else tuple(m_scale)
-        self.v_scale = none if v_scale is None else tuple(v_scale)
-        self.master = none if master is None else tuple(master)
-        self.weight_decay = ((float(weight_decay),) * n if isinstance(weight_decay, (int, float))
-                             else tuple(float(d) for d in weight_decay))
-        if not n:
-            raise ValueError("no weights")
-        self.device = self.weights[0].device
+        self.weights, self.m, self.v = weights, m, v
+        self.m_scale, self.v_scale, self.master, self.weight_decay = m_scale, v_scale, master, weight_decay
         self.validate()
-        # what each step checks the weights against: they may be given other storage from outside
-        self._is = tuple((w.shape, w.dtype, w.numel(), _CODES[w.dtype]) for w in self.weights)
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name in self._GIVEN:
+            object.__setattr__(self, "_checked", False)
 
     @classmethod
     def zeros(cls, weights, bits: int = 32, master: bool = False, weight_decay=0.0) -> "TwellAdamW":
@@ -1263,58 +1266,94 @@ class TwellAdamW:
 
     def validate(self) -> None:
         """Check every buffer before its pointers reach the library."""
-        n, device = len(self.weights), self.device
-        for name in ("m", "v", "m_scale", "v_scale", "master", "weight_decay"):
-            if len(getattr(self, name)) != n:
-                raise ValueError(f"{name}: {len(getattr(self, name))} entries, {n} weights")
-        for i, w in enumerate(self.weights):
+        weights = tuple(self.weights)
+        n = len(weights)
+        if not n:
+            raise ValueError("no weights")
+        device = weights[0].device
+        lists = {"weights": weights}
+        for name in ("master", "m", "v", "m_scale", "v_scale"):
+            given = getattr(self, name)
+            lists[name] = (None,) * n if given is None else tuple(given)
+        decay = self.weight_decay
+        decay = (float(decay),) * n if isinstance(decay, (int, float)) else tuple(float(d) for d in decay)
+        for name, entries in (*lists.items(), ("weight_decay", decay)):
+            if len(entries) != n:
+                raise ValueError(f"{name}: {len(entries)} entries, {n} weights")
+        for i, (w, x, *_, ms, vs) in enumerate(zip(*lists.values())):
             _need(w, f"weights[{i}]", device)
             _dtype_code(w.dtype)
-            if (self.m_scale[i] is None) != (self.v_scale[i] is None):
+            if (ms is None) != (vs is None):
                 raise ValueError(f"m_scale[{i}] and v_scale[{i}] go together")
             blocks = ((w.numel() + 31) // 32,)
             for name in ("m", "v"):
-                scale = getattr(self, f"{name}_scale")[i]
+                scale = lists[f"{name}_scale"][i]
                 if scale is None:
-                    _need(getattr(self, name)[i], f"{name}[{i}]", device, _FLOAT32, w.shape)
+                    _need(lists[name][i], f"{name}[{i}]", device, _FLOAT32, w.shape)
                 else:
-                    _need(getattr(self, name)[i], f"{name}[{i}]", device, _UINT8, (w.numel(),))
+                    _need(lists[name][i], f"{name}[{i}]", device, _UINT8, (w.numel(),))
                     _need(scale, f"{name}_scale[{i}]", device, _UINT8, blocks)
-            if self.master[i] is not None:
+            if x is not None:
                 if w.dtype == _FLOAT32:
                     raise ValueError(f"master[{i}]: float32 weights have no float32 copy")
-                _need(self.master[i], f"master[{i}]", device, _FLOAT32, w.shape)
+                _need(x, f"master[{i}]", device, _FLOAT32, w.shape)
         # a step writes all of them, in no order between tensors
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]")
-                       for name in ("weights", "master", "m", "v", "m_scale", "v_scale")
-                       for i, t in enumerate(getattr(self, name)) if t is not None and t.numel())
+        spans = []
+        for name, entries in lists.items():
+            for i, t in enumerate(entries):
+                if t is None or not t.numel():
+                    continue
+                if t.untyped_storage().nbytes() < (t.storage_offset() + t.numel()) * t.element_size():
+                    raise ValueError(f"{name}[{i}]: its storage ends before its elements")
+                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]"))
+        spans.sort()
         for (_, end, one), (start, _, two) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError(f"{one} and {two} share memory")
+        for name, entries in lists.items():
+            setattr(self, name, entries)
+        self.weight_decay, self.device = decay, device
+        self._shapes, self._dtypes = [w.shape for w in weights], [w.dtype for w in weights]
+        # A buffer of the same address and bytes is the one checked here; weights are given
+        # other storage from outside now and then.
+        self._others = [t for entries in list(lists.values())[1:] for t in entries if t is not None]
+        self._others_at = list(map(_address, self._others)), list(map(_nbytes, self._others))
+        self._weights_at = list(map(_address, weights)), list(map(_nbytes, weights))
+        # the C list but for the gradients: all that reading the states takes
+        self._fields = []
+        for w, x, m, v, ms, vs, d in zip(*lists.values(), decay):
+            self._fields += (w.numel(), w.data_ptr(), 0 if x is None else x.data_ptr(), 0, m.data_ptr(), v.data_ptr(),
+                             0 if ms is None else ms.data_ptr(), 0 if vs is None else vs.data_ptr(), _CODES[w.dtype], 0, d)
+        self._states = _adamw_struct(n).pack(*self._fields)
+        self._checked = True
+
+    def _check(self) -> None:
+        """validate() anew where a buffer is not the one that it has seen."""
+        if not self._checked or (list(map(_address, self._others)), list(map(_nbytes, self._others))) != self._others_at:
+            self.validate()
 
     def c_list(self, grads) -> bytes:
         """The C list with this step's gradients."""
-        flat = []
-        device = self.device
-        for w, is_, x, g, m, v, ms, vs, decay in zip(self.weights, self._is, self.master, grads, self.m, self.v,
-                                                     self.m_scale, self.v_scale, self.weight_decay):
-            shape, dtype, n, code = is_
+        self._check()
+        weights, device = self.weights, self.device
+        if (list(map(_address, weights)), list(map(_nbytes, weights))) != self._weights_at:
+            for w, dtype, shape in zip(weights, self._dtypes, self._shapes):
+                _need(w, "weights", device, dtype, shape)
+            self.validate()
+        for w, dtype, shape, g in zip(weights, self._dtypes, self._shapes, grads):
             if g is None or g.shape != shape or g.device != device or not g.is_contiguous():
                 _need(g, "grads", device, None, shape)
-            if w.dtype != dtype or w.shape != shape or w.device != device or not w.is_contiguous():
+            if w.dtype != dtype or not w.is_contiguous():
                 _need(w, "weights", device, dtype, shape)
-            gt = g.dtype
-            flat += (n, w.data_ptr(), 0 if x is None else x.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
-                     0 if ms is None else ms.data_ptr(), 0 if vs is None else vs.data_ptr(), code,
-                     _CODES[gt] if gt in _CODES else _dtype_code(gt), decay)
-        return _adamw_struct(len(self.weights)).pack(*flat)
+        codes = [_CODES[g.dtype] if g.dtype in _CODES else _dtype_code(g.dtype) for g in grads]
+        flat = self._fields.copy()
+        flat[3::11], flat[9::11] = map(_address, grads), codes
+        return _adamw_struct(len(weights)).pack(*flat)
 
     def c_states(self) -> bytes:
         """The C list for reading the states."""
-        flat = []
-        for is_, m, v, ms, vs in zip(self._is, self.m, self.v, self.m_scale, self.v_scale):
-            flat += (is_[2], 0, 0, 0, m.data_ptr(), v.data_ptr(), ms.data_ptr(), vs.data_ptr(), is_[3], 0, 0.0)
-        return _adamw_struct(len(self._is)).pack(*flat)
+        self._check()
+        return self._states
 
 
 def twell_adamw_step(opt: TwellAdamW, grads, lr, step, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -1357,16 +1396,17 @@ def twell_adamw_states(opt: TwellAdamW, dtype=None):
     in ``dtype`` (default bfloat16, which holds them exactly)."""
     dtype = _BFLOAT16 if dtype is None else dtype
     code = _dtype_code(dtype)
+    table = opt.c_states()
     if any(s is None for s in opt.m_scale):
         raise ValueError("states of 32 bits need no reading")
     # one buffer for all: two calls for the 2 n tensors
     n = len(opt.weights)
-    sizes = [is_[2] for is_ in opt._is]
+    sizes = opt._fields[::11]
     parts = _t.empty((2 * sum(sizes),), dtype=dtype, device=opt.device).split(sizes * 2)
     at = [t.data_ptr() for t in parts]
     pointers = ctypes.c_void_p * n
-    _launch(opt.device, _lib.twell_adamw_states, opt.c_states(), n, code, pointers(*at[:n]), pointers(*at[n:]))
-    values = [t if len(is_[0]) == 1 else t.view(is_[0]) for t, is_ in zip(parts, opt._is * 2)]
+    _launch(opt.device, _lib.twell_adamw_states, table, n, code, pointers(*at[:n]), pointers(*at[n:]))
+    values = [t if len(shape) == 1 else t.view(shape) for t, shape in zip(parts, opt._shapes * 2)]
     return values[:n], values[n:]
 
 

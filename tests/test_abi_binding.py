@@ -75,3 +75,105 @@ def test_the_sizes_of_rows_are_fixed(calls):
             with pytest.raises(AttributeError):
                 setattr(r, name, 1000)
         assert (r.rows, r.cols) == (3, 64) and r.q.shape == (3, 32) and r.scale.shape == (3, 16)
+
+
+def optimizer(bits=8, sizes=(40, 50)):
+    """(optimiser, gradients) of float32 weights."""
+    zeros = [gpu(torch.zeros(n)) for n in sizes]
+    blocks = [-(-n // 32) for n in sizes]
+    states = [[gpu(torch.zeros(n, dtype=torch.uint8 if bits == 8 else torch.float32)) for n in sizes] for _ in range(2)]
+    scales = [[gpu(torch.zeros(n, dtype=torch.uint8)) for n in blocks] if bits == 8 else None for _ in range(2)]
+    return tw.TwellAdamW(zeros, *states, *scales), [gpu(torch.ones(n)) for n in sizes]
+
+
+def step(opt, grads):
+    tw.twell_adamw_step(opt, grads, lr=1e-3, step=1)
+
+
+def _listed(call, opt, field):
+    """A field of twell_adamw_tensor in the list that a call passed."""
+    table = (tw.TwellAdamWTensorC * len(opt.weights)).from_buffer_copy(call[0])
+    return [getattr(t, field) for t in table]
+
+
+# what a resumed run may put in the place of the states: on the host, too short, of another type, too few, none
+BAD_STATES = [lambda a: [t.as_subclass(torch.Tensor) for t in a], lambda a: [a[0], a[1][:49]], lambda a: [t.short() for t in a],
+              lambda a: a[:1], lambda a: None, lambda a: [a[0], None], lambda a: [a[0], a[0]]]
+
+
+@pytest.mark.parametrize("name", ["m", "v", "m_scale", "v_scale"])
+@pytest.mark.parametrize("bad", range(len(BAD_STATES)))
+def test_states_put_in_place_are_checked(name, bad, calls):
+    opt, grads = optimizer()
+    step(opt, grads)
+    good = getattr(opt, name)
+    setattr(opt, name, BAD_STATES[bad](list(good)))
+    if name.endswith("scale") and bad == 1:
+        getattr(opt, name)[1] = good[1][:1]
+    for call in (lambda: step(opt, grads), lambda: tw.twell_adamw_states(opt)) * 2:  # refused again, not once
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    assert len(calls) == 1
+    setattr(opt, name, [t.clone() for t in good])
+    step(opt, grads)
+    assert _listed(calls[-1], opt, name) == [t.data_ptr() for t in getattr(opt, name)]
+    assert getattr(opt, name)[0].data_ptr() != good[0].data_ptr()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_given_other_storage_are_checked(bits, calls):
+    for name in ("m", "v"):
+        opt, grads = optimizer(bits)
+        t = getattr(opt, name)[1]
+        t.data = torch.zeros(50, dtype=t.dtype)
+        step(opt, grads)
+        assert _listed(calls[-1], opt, name)[1] == t.data_ptr()
+        t.data = torch.zeros(49, dtype=t.dtype)
+        with pytest.raises(ValueError):
+            step(opt, grads)
+        # fewer elements of the same memory; memory that was given back
+        opt, grads = optimizer(bits)
+        t = getattr(opt, name)[1]
+        t.data = t.data[:49]
+        with pytest.raises(ValueError):
+            step(opt, grads)
+        opt, grads = optimizer(bits)
+        getattr(opt, name)[1].untyped_storage().resize_(16)
+        with pytest.raises(ValueError, match="storage"):
+            step(opt, grads)
+
+
+def test_decay_put_in_place(calls):
+    opt, grads = optimizer()
+    opt.weight_decay = 0.5
+    step(opt, grads)
+    assert _listed(calls[-1], opt, "weight_decay") == [0.5, 0.5]
+    opt.weight_decay = [0.25]
+    with pytest.raises(ValueError):
+        step(opt, grads)
+
+
+def test_weights_given_other_storage_are_checked(calls):
+    opt, grads = optimizer()
+    a, b = opt.weights
+    b.data = torch.zeros(50)  # as a module's own conversions do
+    step(opt, grads)
+    assert _listed(calls[-1], opt, "weight") == [a.data_ptr(), b.data_ptr()]
+    # side by side in one buffer; then one over the other
+    whole = torch.zeros(90)
+    a.data, b.data = whole[:40], whole[40:]
+    step(opt, grads)
+    b.data = whole[39:89]
+    for _ in range(2):
+        with pytest.raises(ValueError, match="share memory"):
+            step(opt, grads)
+    for bad, error in ((torch.zeros(50).bfloat16(), TypeError), (torch.zeros(51), ValueError), (torch.zeros(100)[::2], ValueError)):
+        opt, grads = optimizer()
+        opt.weights[1].data = bad
+        for _ in range(2):
+            with pytest.raises(error):
+                step(opt, grads)
+    opt, grads = optimizer()
+    opt.weights = [gpu(torch.zeros(40)), gpu(torch.zeros(51))]
+    with pytest.raises(ValueError):
+        step(opt, grads)
