@@ -9,8 +9,10 @@ library has not been built (``python activation_sparse_transformer_bf16_amd/buil
 
 from __future__ import annotations
 
+import bisect
 import ctypes
 import functools
+import itertools
 import operator
 import os
 import struct
@@ -180,6 +182,7 @@ _torch_c = _t._C
 _INT8, _UINT8, _INT64 = _t.int8, _t.uint8, _t.int64
 _FLOAT32, _BFLOAT16 = _t.float32, _t.bfloat16
 _CODES = {_FLOAT32: TWELL_F32, _BFLOAT16: TWELL_BF16}
+_SIZES = (4, 2)  # bytes, by code
 _CONTIGUOUS = _t.contiguous_format
 
 # Names every build of the library must export (checked by the CPU tests).
@@ -1313,6 +1316,10 @@ class TwellAdamW:
         for name, entries in lists.items():
             setattr(self, name, entries)
         self.weight_decay, self.device = decay, device
+        self._views = [None if w.dim() == 1 else w.shape for w in weights] * 2  # of the states' values
+        self._scales = {None if ms is None else True for ms in lists["m_scale"]}
+        # where the written memory begins and ends, in turn
+        self._bounds = [at for span in spans for at in span[:2]] + [1 << 64]
         self._shapes, self._dtypes = [w.shape for w in weights], [w.dtype for w in weights]
         # A buffer of the same address and bytes is the one checked here; weights are given
         # other storage from outside now and then.
@@ -1340,14 +1347,21 @@ class TwellAdamW:
             for w, dtype, shape in zip(weights, self._dtypes, self._shapes):
                 _need(w, "weights", device, dtype, shape)
             self.validate()
-        for w, dtype, shape, g in zip(weights, self._dtypes, self._shapes, grads):
+        flat, bounds, find = self._fields.copy(), self._bounds, bisect.bisect_right
+        at, codes = [], []
+        for w, dtype, shape, n, g in zip(weights, self._dtypes, self._shapes, flat[::11], grads):
             if g is None or g.shape != shape or g.device != device or not g.is_contiguous():
                 _need(g, "grads", device, None, shape)
             if w.dtype != dtype or not w.is_contiguous():
                 _need(w, "weights", device, dtype, shape)
-        codes = [_CODES[g.dtype] if g.dtype in _CODES else _dtype_code(g.dtype) for g in grads]
-        flat = self._fields.copy()
-        flat[3::11], flat[9::11] = map(_address, grads), codes
+            kind, start = g.dtype, g.data_ptr()
+            code = _CODES[kind] if kind in _CODES else _dtype_code(kind)
+            i = find(bounds, start)
+            if (i & 1 or bounds[i] < start + n * _SIZES[code]) and n:  # inside a buffer, or up into the next one
+                raise ValueError(f"grads[{len(at)}] and a buffer that the step writes share memory")
+            at.append(start)
+            codes.append(code)
+        flat[3::11], flat[9::11] = at, codes
         return _adamw_struct(len(weights)).pack(*flat)
 
     def c_states(self) -> bytes:
@@ -1359,7 +1373,7 @@ class TwellAdamW:
 def twell_adamw_step(opt: TwellAdamW, grads, lr, step, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                      clip=None, seed: int = 0) -> None:
     """One AdamW step over all of ``opt``'s tensors, in place, with ``grads``
-    (float32 or bfloat16) like the weights.
+    (float32 or bfloat16) like the weights, none of them in memory that it writes.
 
     ``step`` counts from 1; it or ``lr`` may be a tensor of one element on the GPU
     (int64, float32), read when the step runs.  ``clip``: what ``twell_grad_norm``
@@ -1397,16 +1411,18 @@ def twell_adamw_states(opt: TwellAdamW, dtype=None):
     dtype = _BFLOAT16 if dtype is None else dtype
     code = _dtype_code(dtype)
     table = opt.c_states()
-    if any(s is None for s in opt.m_scale):
+    if None in opt._scales:
         raise ValueError("states of 32 bits need no reading")
     # one buffer for all: two calls for the 2 n tensors
     n = len(opt.weights)
-    sizes = opt._fields[::11]
-    parts = _t.empty((2 * sum(sizes),), dtype=dtype, device=opt.device).split(sizes * 2)
-    at = [t.data_ptr() for t in parts]
-    pointers = ctypes.c_void_p * n
-    _launch(opt.device, _lib.twell_adamw_states, table, n, code, pointers(*at[:n]), pointers(*at[n:]))
-    values = [t if len(shape) == 1 else t.view(shape) for t, shape in zip(parts, opt._shapes * 2)]
+    sizes = opt._fields[::11] * 2
+    whole = _t.empty((sum(sizes),), dtype=dtype, device=opt.device)
+    size, base = _SIZES[code], whole.data_ptr()
+    at = [base + size * k for k in itertools.accumulate(sizes, initial=0)]
+    parts = whole.split_with_sizes(sizes)
+    pointers = struct.Struct(f"@{n}P").pack
+    _launch(opt.device, _lib.twell_adamw_states, table, n, code, pointers(*at[:n]), pointers(*at[n:-1]))
+    values = [t if shape is None else t.view(shape) for t, shape in zip(parts, opt._views)]
     return values[:n], values[n:]
 
 

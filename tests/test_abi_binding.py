@@ -177,3 +177,49 @@ def test_weights_given_other_storage_are_checked(calls):
     opt.weights = [gpu(torch.zeros(40)), gpu(torch.zeros(51))]
     with pytest.raises(ValueError):
         step(opt, grads)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_gradients_in_written_memory_are_refused(bits, calls):
+    # a step reads them while it writes the others
+    whole = torch.zeros(1000)
+    w = [gpu(whole[100:140]), gpu(whole[140:190])]  # side by side
+    opt, _ = optimizer(bits)
+    opt.weights = w
+    fine = [gpu(whole[60:100]), gpu(whole[190:240])]  # up to their first byte and from their last on
+    step(opt, fine)
+    step(opt, [gpu(whole[300:340]), gpu(whole[290:340])])  # each other's memory, which is only read
+    assert _listed(calls[-1], opt, "grad") == [whole[300:].data_ptr(), whole[290:].data_ptr()]
+    half = whole.view(torch.bfloat16)
+    step(opt, [gpu(half[160:200]), gpu(half[380:430])])
+    states = [t for name in ("m", "v", "m_scale", "v_scale") for t in getattr(opt, name) if t is not None]
+    inside = [whole[61:101], whole[100:140], whole[101:141], whole[139:179], whole[150:190], whole[189:229],
+              half[161:201], half[379:419]]
+    for one in inside:
+        with pytest.raises(ValueError, match="share memory"):
+            step(opt, [gpu(one), fine[1]])
+    for t in states:
+        if t.dtype == torch.float32 and t.numel() == 40:
+            with pytest.raises(ValueError, match="share memory"):
+                step(opt, [t, fine[1]])
+    if bits == 8:  # bytes of codes, as an element of a gradient
+        one, grads = optimizer(8, (4, 1))
+        with pytest.raises(ValueError, match="share memory"):
+            step(one, [grads[0], gpu(one.m[0].as_subclass(torch.Tensor).view(torch.float32))])
+    n = len(calls)
+    # a tensor without elements lies nowhere
+    opt, grads = optimizer(bits, (0, 40, 0))
+    opt.weights = [opt.weights[0], opt.weights[1], gpu(opt.weights[1].as_subclass(torch.Tensor)[:0])]
+    grads[2] = gpu(opt.weights[1].as_subclass(torch.Tensor)[20:20])
+    step(opt, grads)
+    assert len(calls) == n + 1
+
+
+def test_gradients_in_the_copies_are_refused(calls):
+    w = gpu(torch.zeros(64, dtype=torch.bfloat16))
+    opt = tw.TwellAdamW([w], [gpu(torch.zeros(64))], [gpu(torch.zeros(64))], master=[gpu(torch.zeros(64))])
+    step(opt, [gpu(torch.zeros(64))])
+    for grad in (opt.master[0], opt.m[0], opt.v[0], w):
+        with pytest.raises(ValueError, match="share memory"):
+            step(opt, [grad])
+    assert len(calls) == 1
