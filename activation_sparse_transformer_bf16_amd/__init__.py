@@ -1316,6 +1316,7 @@ class TwellAdamW:
         for name, entries in lists.items():
             setattr(self, name, entries)
         self.weight_decay, self.device = decay, device
+        self._versioned = [*weights, *(x for x in lists["master"] if x is not None)]
         self._views = [None if w.dim() == 1 else w.shape for w in weights] * 2  # of the states' values
         self._scales = {None if ms is None else True for ms in lists["m_scale"]}
         # where the written memory begins and ends, in turn
@@ -1378,7 +1379,10 @@ def twell_adamw_step(opt: TwellAdamW, grads, lr, step, beta1: float = 0.9, beta2
     ``step`` counts from 1; it or ``lr`` may be a tensor of one element on the GPU
     (int64, float32), read when the step runs.  ``clip``: what ``twell_grad_norm``
     returned (a factor that is not finite leaves the step out).  ``seed``: of the
-    random roundings of 8-bit states and of bfloat16 weights without a copy."""
+    random roundings of 8-bit states and of bfloat16 weights without a copy.
+
+    Autograd counts the step as a change in place, as torch's optimisers do: a
+    backward through a graph that saved a weight before it raises."""
     device = opt.device
     if not isinstance(grads, (list, tuple)):
         grads = list(grads)
@@ -1396,6 +1400,7 @@ def twell_adamw_step(opt: TwellAdamW, grads, lr, step, beta1: float = 0.9, beta2
         cp = _vec(clip, "clip", device, _FLOAT32, 2)
     args = TwellAdamWC(lr, beta1, beta2, eps, step, seed & 0xFFFFFFFFFFFFFFFF, lp, sp)
     _launch(device, _lib.twell_adamw_step, table, len(grads), args, cp)
+    _t.autograd.graph.increment_version(opt._versioned)
 
 
 def _one(t, name, device, dtype) -> int:

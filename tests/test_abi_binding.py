@@ -223,3 +223,27 @@ def test_gradients_in_the_copies_are_refused(calls):
         with pytest.raises(ValueError, match="share memory"):
             step(opt, [grad])
     assert len(calls) == 1
+
+
+def test_autograd_sees_the_step(calls):
+    # a backward through a graph of the weights before the step would use those after it
+    w = gpu(torch.full((40,), 2.0)).requires_grad_()
+    b = gpu(torch.zeros(40, dtype=torch.bfloat16))
+    with torch.inference_mode():
+        i = gpu(torch.zeros(40))  # has no version
+    copy = gpu(torch.zeros(40))
+    zeros = lambda: [gpu(torch.zeros(40)) for _ in range(3)]  # noqa: E731
+    opt = tw.TwellAdamW([w, b, i], zeros(), zeros(), master=[None, copy, None])
+    loss, later = (w * w).sum(), (w * 3).sum()
+    before = w._version, b._version, copy._version
+    step(opt, zeros())
+    assert all(t._version > v for t, v in zip((w, b, copy), before)) and len(calls) == 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    later.backward()  # needs no weight
+    assert torch.equal(w.grad.as_subclass(torch.Tensor), torch.full((40,), 3.0))
+    # a refused step has written nothing
+    before = w._version
+    with pytest.raises(ValueError):
+        tw.twell_adamw_step(opt, zeros(), lr=1e-3, step=0)
+    assert w._version == before
