@@ -247,3 +247,15 @@ def test_autograd_sees_the_step(calls):
     with pytest.raises(ValueError):
         tw.twell_adamw_step(opt, zeros(), lr=1e-3, step=0)
     assert w._version == before
+
+
+def test_the_quantiser_refuses_rows_beyond_32_bits(calls):
+    # (ctypes would pass their low 32 bits); without memory, but on the GPU as far as the checks can tell
+    for shape in (((1 << 31) + 3, 32), (3, 1 << 31)):
+        x = gpu(torch.empty(shape, dtype=torch.bfloat16, device="meta"))
+        for call in (lambda: tw.twell_quantize_mx4(x), lambda: tw.twell_rmsnorm_mx4(x, gpu(torch.empty(shape[1], device="meta")))):
+            with pytest.raises(ValueError, match=f"sizes of .*{max(shape)}.* exceed"):
+                call()
+    small = gpu(torch.zeros(3, 32))
+    tw.twell_quantize_mx4(small, out=rows(torch.zeros(3, 16, dtype=torch.uint8), torch.zeros(3, 16, dtype=torch.uint8), 32))
+    assert len(calls) == 1
