@@ -741,8 +741,8 @@ twell_status twell_adamw_step(const twell_adamw_tensor *tensors, int count, cons
 
 /*
  * twell_adamw_states -- the values of the list's 8-bit states: m[i], v[i] [n] in dtype
- * (bf16 holds them exactly but for values below 2^-126).  m and v are HOST arrays of
- * count pointers; either may be NULL, and so may any of their entries (not read).
+ * (bf16 holds them exactly: besides 0, m is at least 2^-104 and v 2^-120).  m and v are
+ * HOST arrays of count pointers; either may be NULL, and so may any of their entries (not read).
  * Only n, m, v and their scales are read of the tensors.
  * Errors: INVALID_ARG (NULL list or states, no scales, dtype, sizes), UNSUPPORTED
  * (alignment, n), HIP.

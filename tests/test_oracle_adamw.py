@@ -110,3 +110,12 @@ def test_grad_norm():
     assert grad_norm([[3.0], [4.0]], 10.0) == (5.0, 1.0)
     assert grad_norm([[0.0]], 1.0) == (0.0, 1.0)
     assert np.isnan(grad_norm([[np.inf]], 1.0)[1])
+
+
+@pytest.mark.parametrize("fields,smallest", [(16, 2.0 ** -104), (32, 2.0 ** -120)])
+def test_bf16_holds_every_state(fields, smallest):
+    # at most 4 significant bits, from `smallest` (a normal number) on
+    code, byte = np.tile(np.arange(256, dtype=np.uint8), 241), np.repeat(np.arange(241, dtype=np.uint8), 8)
+    v = decode(code, byte, fields)
+    assert np.array_equal((v.astype(np.float32).view(np.uint32) & 0xFFFF0000).view(np.float32).astype(np.float64), v)
+    assert np.abs(v[v != 0]).min() == smallest
