@@ -106,19 +106,21 @@ struct Mx4Tile {
 // is fetched twice (8192^3: 41 million L2 requests, in pairs 25).
 //
 // 8192 x 8192 x 2048 bf16 96 to 100 us (2.8 PFLOP/s), 8192^3 275 to 287 (3.9), 16384 x
-// 14336 x 4096 468 to 485 (4.0), by card; MFMA busy 0.31 to 0.43.  What bounds it is
-// the copies: of the 233 us that another K = 8192 of 8192 x 8192 takes, 73 go without
+// 14336 x 4096 468 to 485 (4.0), by card; MFMA busy 0.31 to 0.43.  What bounds the loop
+// is the copies: of the 233 us that another K = 8192 of 8192 x 8192 takes, 73 go without
 // them, 8 without the LDS reads, and the products alone take 140.  Two pairs of slabs fill
-// the LDS, so a pair has the time of one other to arrive, and a miss in L2 takes longer:
-// with all tiles reading the same rows 8192 x 8192 x 2048 takes 92 us, 8192^3 260.
-// Power is a fifth (operands of zeros: 78, 233 and 444 us).  Slower or no faster: one
-// workgroup per CU that starts the next tile's copies before its results' stores (K =
-// 2048 115 us, K = 512 66 against 54: copies behind stores wait for them), two
-// workgroups of 128 x 256 per CU (K = 2048 107, 8192^3 335), results straight from
-// registers (100, 495 at 16384 x 14336 x 4096), raised wave priority, panels of 1, 4 and
-// 8 tiles of rows where a panel has 1024 rows now (K = 2048 91 to 98, but 16384 x 14336
-// x 4096 476 to 522), non-temporal stores of 134 MB (83 us, but the kernel that reads the
-// result next takes 41 more).
+// the LDS, so a pair has the time of one other to arrive, and a miss in L2 takes longer;
+// but with all tiles reading the same rows 8192 x 8192 x 2048 takes 92 us, 8192^3 260, so
+// misses are at most 17 of the 73, and the rest (issue and waits, LDS writes beside reads,
+// a barrier per pair) is not told apart.  At K = 2048 the loop is 58 of 98 us, the
+// tiles' starts and results 40.  Power is a fifth (operands of zeros: 78, 233 and 444
+// us).  Slower or no faster: one workgroup per CU that starts the next tile's copies
+// before its results' stores (K = 2048 115 us, K = 512 66 against 54: copies behind
+// stores wait for them), two workgroups of 128 x 256 per CU (K = 2048 107, 8192^3
+// 335), results straight from registers (100, 495 at 16384 x 14336 x 4096), raised
+// wave priority, panels of 1, 4 and 8 tiles of rows where a panel has 1024 rows now (K
+// = 2048 91 to 98, but 16384 x 14336 x 4096 476 to 522), non-temporal stores of 134 MB
+// (83 us, but the kernel that reads the result next takes 41 more).
 template <Dt D, class Cfg, int BN, bool STREAM>
 __global__ __launch_bounds__(Cfg::THREADS, Cfg::WAVES_PER_SIMD) void k_mx4_tile(Mx4MatmulArgs a, int tiles) {
   using T = typename DtT<D>::T;
@@ -443,7 +445,7 @@ __global__ __launch_bounds__(256) void k_mx4_join(Mx4MatmulArgs a, int parts) {
 // Bound by latency: 1 x 8192 x 2048 3.7 us (8.9 MB, 2.4 TB/s; an empty launch 2.0), 16
 // and 64 x 8192 x 2048 3.9 and 6.0, 64 x 2048 x 8192 7.4, 333 x 1000 x 777 4.5.  As tiles
 // of 64 x 128 with 8 ranges of K 64 x 2048 x 8192 takes 11.1 us, 1 x 2048 x 8192 6.8
-// (here 4.5).
+// (here 4.5).  K is not cut across workgroups: 16 x 300 x 60000, in 19 of them, 27 us.
 template <int MF_, int NF_, int WAVES_, int STAGES_>
 struct Mx4Small {
   static constexpr int MF = MF_, NF = NF_, WAVES = WAVES_, STAGES = STAGES_;
@@ -619,7 +621,9 @@ static int64_t mx4_tiles(int bm, int bn, int M, int N) { return (int64_t)((M - 1
 
 // The kernel, shape and number of K ranges with the least estimated time: 256
 // CUs take the tiles in rounds; the ranges' sums are written and read once (4
-// bytes each way at about 4 TB/s), the operands read at 5 TB/s at most.
+// bytes each way at about 4 TB/s), the operands read at 5 TB/s at most.  Numbers of
+// ranges are powers of two up to the first that K's groups do not fill (118 groups:
+// 15 ranges and not 16), which leaves some out that would be 10 to 40% faster.
 static Mx4Plan mx4_plan(int M, int N, int K) {
   const int ng = (K + MX4_GROUP - 1) / MX4_GROUP, row = (K + 1) / 2;
   Mx4Plan best{false, MX4_256x256, 1, ng * MX4_GROUP, 0};
