@@ -623,7 +623,7 @@ static int64_t mx4_tiles(int bm, int bn, int M, int N) { return (int64_t)((M - 1
 // CUs take the tiles in rounds; the ranges' sums are written and read once (4
 // bytes each way at about 4 TB/s), the operands read at 5 TB/s at most.  Numbers of
 // ranges are powers of two up to the first that K's groups do not fill (118 groups:
-// 15 ranges and not 16), which leaves some out that would be 10 to 40% faster.
+// 15 ranges and not 16), which leaves some out whose estimates are 10 to 40% lower.
 static Mx4Plan mx4_plan(int M, int N, int K) {
   const int ng = (K + MX4_GROUP - 1) / MX4_GROUP, row = (K + 1) / 2;
   Mx4Plan best{false, MX4_256x256, 1, ng * MX4_GROUP, 0};
