@@ -1283,36 +1283,44 @@ class TwellAdamW:
         for name, entries in (*lists.items(), ("weight_decay", decay)):
             if len(entries) != n:
                 raise ValueError(f"{name}: {len(entries)} entries, {n} weights")
-        for i, (w, x, *_, ms, vs) in enumerate(zip(*lists.values())):
-            _need(w, f"weights[{i}]", device)
-            _dtype_code(w.dtype)
+        def need(t, name, i, dtype, shape):
+            if (t is None or t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda
+                    or not t.is_contiguous()):
+                _need(t, f"{name}[{i}]", device, dtype, shape)
+
+        for i, (w, x, m, v, ms, vs) in enumerate(zip(*lists.values())):
+            dtype, shape = w.dtype, w.shape
+            need(w, "weights", i, dtype, shape)
+            if dtype not in _CODES:
+                _dtype_code(dtype)
             if (ms is None) != (vs is None):
                 raise ValueError(f"m_scale[{i}] and v_scale[{i}] go together")
-            blocks = ((w.numel() + 31) // 32,)
-            for name in ("m", "v"):
-                scale = lists[f"{name}_scale"][i]
-                if scale is None:
-                    _need(lists[name][i], f"{name}[{i}]", device, _FLOAT32, w.shape)
-                else:
-                    _need(lists[name][i], f"{name}[{i}]", device, _UINT8, (w.numel(),))
-                    _need(scale, f"{name}_scale[{i}]", device, _UINT8, blocks)
+            if ms is None:
+                need(m, "m", i, _FLOAT32, shape)
+                need(v, "v", i, _FLOAT32, shape)
+            else:
+                codes = (w.numel(),)
+                blocks = ((codes[0] + 31) // 32,)
+                need(m, "m", i, _UINT8, codes)
+                need(ms, "m_scale", i, _UINT8, blocks)
+                need(v, "v", i, _UINT8, codes)
+                need(vs, "v_scale", i, _UINT8, blocks)
             if x is not None:
-                if w.dtype == _FLOAT32:
+                if dtype == _FLOAT32:
                     raise ValueError(f"master[{i}]: float32 weights have no float32 copy")
-                _need(x, f"master[{i}]", device, _FLOAT32, w.shape)
+                need(x, "master", i, _FLOAT32, shape)
         # a step writes all of them, in no order between tensors
-        spans = []
-        for name, entries in lists.items():
-            for i, t in enumerate(entries):
-                if t is None or not t.numel():
-                    continue
-                if t.untyped_storage().nbytes() < (t.storage_offset() + t.numel()) * t.element_size():
-                    raise ValueError(f"{name}[{i}]: its storage ends before its elements")
-                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]"))
-        spans.sort()
+        names = [(name, i) for name, entries in lists.items() for i, t in enumerate(entries) if t is not None]
+        others = [t for entries in list(lists.values())[1:] for t in entries if t is not None]
+        all_ = [*weights, *others]
+        at, sizes = list(map(_address, all_)), list(map(_nbytes, all_))
+        spans = sorted((start, start + size, name) for start, size, name in zip(at, sizes, names) if size)
+        for t, size, (name, i) in zip(all_, sizes, names):
+            if t.untyped_storage().nbytes() < size:
+                raise ValueError(f"{name}[{i}]: its storage has been given back")
         for (_, end, one), (start, _, two) in zip(spans, spans[1:]):
             if start < end:
-                raise ValueError(f"{one} and {two} share memory")
+                raise ValueError(f"{one[0]}[{one[1]}] and {two[0]}[{two[1]}] share memory")
         for name, entries in lists.items():
             setattr(self, name, entries)
         self.weight_decay, self.device = decay, device
@@ -1320,18 +1328,21 @@ class TwellAdamW:
         self._views = [None if w.dim() == 1 else w.shape for w in weights] * 2  # of the states' values
         self._scales = {None if ms is None else True for ms in lists["m_scale"]}
         # where the written memory begins and ends, in turn
-        self._bounds = [at for span in spans for at in span[:2]] + [1 << 64]
+        self._bounds = [end for span in spans for end in span[:2]] + [1 << 64]
         self._shapes, self._dtypes = [w.shape for w in weights], [w.dtype for w in weights]
         # A buffer of the same address and bytes is the one checked here; weights are given
         # other storage from outside now and then.
-        self._others = [t for entries in list(lists.values())[1:] for t in entries if t is not None]
-        self._others_at = list(map(_address, self._others)), list(map(_nbytes, self._others))
-        self._weights_at = list(map(_address, weights)), list(map(_nbytes, weights))
+        self._others, self._others_at, self._weights_at = others, (at[n:], sizes[n:]), (at[:n], sizes[:n])
         # the C list but for the gradients: all that reading the states takes
-        self._fields = []
-        for w, x, m, v, ms, vs, d in zip(*lists.values(), decay):
-            self._fields += (w.numel(), w.data_ptr(), 0 if x is None else x.data_ptr(), 0, m.data_ptr(), v.data_ptr(),
-                             0 if ms is None else ms.data_ptr(), 0 if vs is None else vs.data_ptr(), _CODES[w.dtype], 0, d)
+        where = {name: [0] * n for name in lists}
+        for (name, i), start in zip(names, at):
+            where[name][i] = start
+        self._fields = [0] * (11 * n)
+        self._fields[::11] = [w.numel() for w in weights]
+        for k, name in ((1, "weights"), (2, "master"), (4, "m"), (5, "v"), (6, "m_scale"), (7, "v_scale")):
+            self._fields[k::11] = where[name]
+        self._fields[8::11] = [_CODES[w.dtype] for w in weights]
+        self._fields[10::11] = decay
         self._states = _adamw_struct(n).pack(*self._fields)
         self._checked = True
 

@@ -138,7 +138,7 @@ def test_states_given_other_storage_are_checked(bits, calls):
         with pytest.raises(ValueError):
             step(opt, grads)
         opt, grads = optimizer(bits)
-        getattr(opt, name)[1].untyped_storage().resize_(16)
+        getattr(opt, name)[1].untyped_storage().resize_(0)
         with pytest.raises(ValueError, match="storage"):
             step(opt, grads)
 
@@ -259,3 +259,19 @@ def test_the_quantiser_refuses_rows_beyond_32_bits(calls):
     small = gpu(torch.zeros(3, 32))
     tw.twell_quantize_mx4(small, out=rows(torch.zeros(3, 16, dtype=torch.uint8), torch.zeros(3, 16, dtype=torch.uint8), 32))
     assert len(calls) == 1
+
+
+def test_storage_given_back_is_refused(calls):
+    # as a sharded module gives back its flat buffer between steps; a view's address is then small and not 0
+    flat = torch.zeros(200)
+    opt, grads = optimizer(8, (40, 50))
+    opt.weights = [gpu(flat[100:140]), gpu(flat[140:190])]
+    step(opt, grads)
+    flat.untyped_storage().resize_(0)
+    for _ in range(2):
+        with pytest.raises(ValueError, match="given back"):
+            step(opt, grads)
+    assert len(calls) == 1
+    flat.untyped_storage().resize_(800)
+    step(opt, grads)
+    assert _listed(calls[-1], opt, "weight") == [flat[100:].data_ptr(), flat[140:].data_ptr()]
