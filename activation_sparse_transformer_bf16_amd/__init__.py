@@ -1242,9 +1242,10 @@ class TwellAdamW:
         self.validate()
 
     def __setattr__(self, name, value):
-        object.__setattr__(self, name, value)
         if name in self._GIVEN:
+            value = value if value is None or isinstance(value, (int, float)) else tuple(value)
             object.__setattr__(self, "_checked", False)
+        object.__setattr__(self, name, value)
 
     @classmethod
     def zeros(cls, weights, bits: int = 32, master: bool = False, weight_decay=0.0) -> "TwellAdamW":
@@ -1269,20 +1270,20 @@ class TwellAdamW:
 
     def validate(self) -> None:
         """Check every buffer before its pointers reach the library."""
-        weights = tuple(self.weights)
-        n = len(weights)
-        if not n:
+        weights = self.weights
+        if not weights:
             raise ValueError("no weights")
-        device = weights[0].device
+        n, device = len(weights), weights[0].device
         lists = {"weights": weights}
         for name in ("master", "m", "v", "m_scale", "v_scale"):
             given = getattr(self, name)
-            lists[name] = (None,) * n if given is None else tuple(given)
+            lists[name] = (None,) * n if given is None else given
         decay = self.weight_decay
         decay = (float(decay),) * n if isinstance(decay, (int, float)) else tuple(float(d) for d in decay)
         for name, entries in (*lists.items(), ("weight_decay", decay)):
             if len(entries) != n:
                 raise ValueError(f"{name}: {len(entries)} entries, {n} weights")
+
         def need(t, name, i, dtype, shape):
             if (t is None or t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda
                     or not t.is_contiguous()):
@@ -1394,12 +1395,12 @@ def twell_adamw_step(opt: TwellAdamW, grads, lr, step, beta1: float = 0.9, beta2
 
     Autograd counts the step as a change in place, as torch's optimisers do: a
     backward through a graph that saved a weight before it raises."""
-    device = opt.device
     if not isinstance(grads, (list, tuple)):
         grads = list(grads)
     if len(grads) != len(opt.weights):
         raise ValueError(f"{len(grads)} gradients, {len(opt.weights)} weights")
     table = opt.c_list(grads)
+    device = opt.device
     lp = sp = cp = None
     if isinstance(lr, _t.Tensor):
         lp, lr = _one(lr, "lr", device, _FLOAT32), 0.0

@@ -107,9 +107,7 @@ def test_states_put_in_place_are_checked(name, bad, calls):
     opt, grads = optimizer()
     step(opt, grads)
     good = getattr(opt, name)
-    setattr(opt, name, BAD_STATES[bad](list(good)))
-    if name.endswith("scale") and bad == 1:
-        getattr(opt, name)[1] = good[1][:1]
+    setattr(opt, name, [good[0], good[1][:1]] if name.endswith("scale") and bad == 1 else BAD_STATES[bad](list(good)))
     for call in (lambda: step(opt, grads), lambda: tw.twell_adamw_states(opt)) * 2:  # refused again, not once
         with pytest.raises((ValueError, TypeError)):
             call()
@@ -275,3 +273,24 @@ def test_storage_given_back_is_refused(calls):
     flat.untyped_storage().resize_(800)
     step(opt, grads)
     assert _listed(calls[-1], opt, "weight") == [flat[100:].data_ptr(), flat[140:].data_ptr()]
+
+
+class Elsewhere(OnGpu):
+    device = property(lambda self: torch.device("cuda:1"))
+
+
+def test_an_optimiser_moved_to_another_device(monkeypatch):
+    seen = []
+    monkeypatch.setattr(tw, "_launch", lambda device, fn, *args: seen.append(device))
+    opt, grads = optimizer(32)
+    step(opt, grads)
+    for name in ("weights", "m", "v"):
+        setattr(opt, name, (t.as_subclass(Elsewhere) for t in getattr(opt, name)))  # (any iterable)
+    lr = torch.zeros(1).as_subclass(Elsewhere)
+    with pytest.raises(ValueError):
+        step(opt, grads)
+    there = [g.as_subclass(Elsewhere) for g in grads]
+    with pytest.raises(ValueError):
+        tw.twell_adamw_step(opt, there, lr=gpu(torch.zeros(1)), step=1)
+    tw.twell_adamw_step(opt, there, lr=lr, step=1)
+    assert seen == [torch.device("cuda:0"), torch.device("cuda:1")]
